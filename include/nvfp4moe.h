@@ -140,7 +140,35 @@ typedef struct {
     const uint16_t* sh_gate_w;       /* bf16 [H]                                 */
 } moe_layer_desc;
 
+/* Element type of the output of the 8-bit and of the grouped products. */
+typedef enum {
+    NVFP4_OUT_BF16 = 0,
+    NVFP4_OUT_F32 = 1
+} nvfp4_out_type;
+
+/*
+ * Rows grouped by expert, as moe_route_topk lists them: list position r in
+ * [expert_offsets[e], expert_offsets[e+1]) belongs to expert e.
+ *   gather    0: position r reads row r of x [R, K].
+ *             1: position r reads row token_list[r] / k of x [R/k, K] (R % k == 0): the
+ *                token of its entry.
+ *   scatter   0: position r writes row r of y [R, N]; 1: row token_list[r] (entry order, so
+ *                that y viewed as [T, k, N] holds each token's k rows).
+ * token_list may be NULL when gather and scatter are 0.
+ */
+typedef struct {
+    int32_t R;                       /* list positions (T * k), the rows of y    */
+    int32_t E;                       /* experts                                  */
+    int32_t k;                       /* entries per token                        */
+    int32_t gather;
+    int32_t scatter;
+    const int32_t* expert_offsets;   /* int32 [E + 1] device                     */
+    const int32_t* token_list;       /* int32 [R] device, or NULL                */
+} moe_groups;
+
 /* ------------------------------------------------------------------ limits */
+#define NVFP4_MAX_PRODUCT_ROWS 1048576  /* fp8_gemm_block128: T, moe_groups: R    */
+#define NVFP4_MAX_PRODUCT_K 65536       /* K of the 8-bit and grouped products    */
 #define NVFP4_MAX_TOPK 8          /* k <= 8                                    */
 #define NVFP4_MAX_EXPERTS 256     /* E <= 256                                  */
 #define NVFP4_MAX_GEMV_TOKENS 64  /* nvfp4_gemv_w4a16: 1 <= T <= 64            */
@@ -274,6 +302,78 @@ NVFP4_API nvfp4_status moe_layer_forward_residual(const moe_layer_desc* d, const
                                                   int32_t* topk_ids_out, float* topk_w_out, void* workspace,
                                                   size_t workspace_bytes, void* stream);
 NVFP4_API size_t moe_layer_residual_workspace_size(const moe_layer_desc* d, int32_t T);
+
+/*
+ * fp8_quantize_block128 - bf16 -> FP8-E4M3 codes with one fp32 scale per block of 128, the
+ * operands of fp8_gemm_block128 and moe_grouped_gemm_fp8.
+ *   Per block with largest magnitude a = max |x|:
+ *     scale = a / 448 rounded to fp32 (1 where a = 0)
+ *     code  = the E4M3 value nearest to 448 x / a (the real quotient), ties to even
+ *   so x is approximated by code * scale. A block that holds an infinity has scale infinity
+ *   and codes 0 (finite x) or NaN (infinite x); one that holds a NaN has scale and codes NaN.
+ *   x           bf16 [B, R, K] device: B matrices of R rows
+ *   block_rows  1: blocks of 1 x 128 (activations), scales fp32 [B, R, ceil(K/128)]
+ *               128: blocks of 128 x 128 (weights), scales fp32 [B, ceil(R/128), ceil(K/128)]
+ *               The last block of a row or a matrix may be partial.
+ *   q           uint8 [B, R, K] device, written;  scales device (4-byte aligned), written
+ *   Shapes: B, R >= 0, K >= 16, K % 16 == 0, K <= NVFP4_MAX_PRODUCT_K, B * R < 2^31.
+ *   B * R == 0 enqueues nothing.
+ */
+NVFP4_API nvfp4_status fp8_quantize_block128(const uint16_t* x, int32_t B, int32_t R, int32_t K,
+                                             int32_t block_rows, uint8_t* q, float* scales, void* stream);
+
+/*
+ * fp8_gemm_block128 - dense product of block-scaled E4M3 operands:
+ *   y[t,n] = sum_b x_scales[t,b] * w_scales[n/128,b] * sum_{k in block b} x[t,k] * w[n,k]
+ *   over the blocks b of 128 columns; every block's sum and the running sum in fp32, one
+ *   rounding to the output type.
+ *   x         uint8 E4M3 [T, K] device;  x_scales  fp32 [T, ceil(K/128)]
+ *   w         uint8 E4M3 [N, K] device;  w_scales  fp32 [ceil(N/128), ceil(K/128)]
+ *   y         bf16 or fp32 [T, N] device (y_type), written
+ *   workspace NULL (0 bytes), or >= 256 bytes of device memory zeroed with
+ *       nvfp4_workspace_init: the call needs no scratch, but a bounded device wait that ran
+ *       out is recorded in its status word. Such a wait also writes quiet NaN into the rows
+ *       of y that it touches.
+ *   Scales, offsets and lists are 4-byte aligned, everything else 16-byte.
+ *   Shapes: 0 <= T <= NVFP4_MAX_PRODUCT_ROWS, 1 <= N <= 2^22, K >= 16, K % 16 == 0,
+ *   K <= NVFP4_MAX_PRODUCT_K. T == 0 enqueues nothing.
+ */
+NVFP4_API nvfp4_status fp8_gemm_block128(const uint8_t* x, const float* x_scales, int32_t T, const uint8_t* w,
+                                         const float* w_scales, int32_t N, int32_t K, void* y, int32_t y_type,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_grouped_gemm_bf16 - each expert's matrix times the rows routed to it:
+ *   y[o(r),:] = W[e] x[i(r),:]  for expert_offsets[e] <= r < expert_offsets[e+1]
+ *   with i(r), o(r) as moe_groups says; fp32 sums, one rounding to the output type.
+ *   Defined by: lynn-engine README, P2/P3-A notes (the routed path as batched projections
+ *   over each expert's tokens) and "next steps" (grouped GEMM instead of per-expert
+ *   launches), for experts kept in bf16.
+ *   x  bf16 device, [R, K] or with gather [R/k, K];  w  bf16 [E, N, K] device
+ *   y  bf16 or fp32 [R, N] device (y_type). Rows that no list position writes (positions
+ *      behind expert_offsets[E], or before expert_offsets[0]) are left as they were.
+ *   workspace  as for fp8_gemm_block128.
+ *   The offsets are device data and not checked on the host. Offsets are taken into [0, R]
+ *   and a group that ends before it begins is empty; a list entry outside [0, R) reads a
+ *   row of zeros (gather) or writes nothing (scatter). Groups that overlap, or a list that
+ *   names an entry twice, leave rows of y that several positions write undefined.
+ *   Shapes: 0 <= R <= NVFP4_MAX_PRODUCT_ROWS, 1 <= E <= NVFP4_MAX_EXPERTS, k >= 1,
+ *   1 <= N <= 2^22, E * N < 2^31, K >= 8, K % 8 == 0, K <= NVFP4_MAX_PRODUCT_K.
+ *   R == 0 enqueues nothing.
+ */
+NVFP4_API nvfp4_status moe_grouped_gemm_bf16(const moe_groups* g, const uint16_t* x, const uint16_t* w, int32_t N,
+                                             int32_t K, void* y, int32_t y_type, void* workspace,
+                                             size_t workspace_bytes, void* stream);
+
+/*
+ * moe_grouped_gemm_fp8 - moe_grouped_gemm_bf16 with the block-scaled E4M3 operands of
+ * fp8_gemm_block128: x uint8 (rows as above) with x_scales fp32 [rows of x, ceil(K/128)],
+ * w uint8 [E, N, K] with w_scales fp32 [E, ceil(N/128), ceil(K/128)]. K >= 16, K % 16 == 0.
+ */
+NVFP4_API nvfp4_status moe_grouped_gemm_fp8(const moe_groups* g, const uint8_t* x, const float* x_scales,
+                                            const uint8_t* w, const float* w_scales, int32_t N, int32_t K,
+                                            void* y, int32_t y_type, void* workspace, size_t workspace_bytes,
+                                            void* stream);
 
 /*
  * moe_layer_forward_noalloc - the same layer as moe_layer_forward, for callers

@@ -7,7 +7,8 @@ There is no fallback: if the shared library is missing, importing this module
 raises.
 
 The function names are those of the C ABI in ``include/nvfp4moe.h``:
-``nvfp4_pack``, ``nvfp4_gemv_w4a16``, ``moe_route_topk``, ``moe_layer_forward``.
+``nvfp4_pack``, ``nvfp4_gemv_w4a16``, ``moe_route_topk``, ``moe_layer_forward``,
+``fp8_quantize_block128``, ``fp8_gemm_block128``, ``moe_grouped_gemm_bf16``, ``moe_grouped_gemm_fp8``.
 """
 from __future__ import annotations
 
@@ -100,6 +101,11 @@ class MoELayerDescC(ctypes.Structure):
                 ("sh_gate_w", _P)]
 
 
+class MoEGroupsC(ctypes.Structure):
+    _fields_ = [("R", _i32), ("E", _i32), ("k", _i32), ("gather", _i32), ("scatter", _i32),
+                ("expert_offsets", _P), ("token_list", _P)]
+
+
 lib = ctypes.CDLL(LIB_PATH)
 lib.nvfp4_pack.restype = _i32
 lib.nvfp4_pack.argtypes = [_P, _i32, _i32, _i32, _P, _P, _P, _P, _sz, _P]
@@ -136,6 +142,14 @@ lib.nvfp4_status_string.restype = ctypes.c_char_p
 lib.nvfp4_status_string.argtypes = [_i32]
 lib.nvfp4_version.restype = _i32
 lib.nvfp4_version.argtypes = []
+lib.fp8_quantize_block128.restype = _i32
+lib.fp8_quantize_block128.argtypes = [_P, _i32, _i32, _i32, _i32, _P, _P, _P]
+lib.fp8_gemm_block128.restype = _i32
+lib.fp8_gemm_block128.argtypes = [_P, _P, _i32, _P, _P, _i32, _i32, _P, _i32, _P, _sz, _P]
+lib.moe_grouped_gemm_bf16.restype = _i32
+lib.moe_grouped_gemm_bf16.argtypes = [ctypes.POINTER(MoEGroupsC), _P, _P, _i32, _i32, _P, _i32, _P, _sz, _P]
+lib.moe_grouped_gemm_fp8.restype = _i32
+lib.moe_grouped_gemm_fp8.argtypes = [ctypes.POINTER(MoEGroupsC), _P, _P, _P, _P, _i32, _i32, _P, _i32, _P, _sz, _P]
 lib.moe_layer_forward_noalloc.restype = _i32
 lib.moe_layer_forward_noalloc.argtypes = [ctypes.POINTER(MoELayerDescC), _P, _i32, _P, _P, _P, _P]
 lib.nvfp4_noalloc_status.restype = _i32
@@ -273,6 +287,147 @@ def moe_route_topk(logits: torch.Tensor, k: int, stream=None):
     _check(lib.moe_route_topk(_ptr(logits), T, E, k, _ptr(ids), _ptr(w), _ptr(offsets), _ptr(tl),
                               _stream(stream)), "moe_route_topk")
     return ids, w, offsets, tl[:T * k]
+
+
+# ---------------------------------------------------------------- 8-bit and grouped products
+
+_OUT_TYPE = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _refuse(where: str, why: str, status: int = NVFP4_ERR_INVALID_ARG):
+    raise NVFP4Error(status, "%s: %s" % (where, why))
+
+
+def _operand(t: torch.Tensor, dtype, shape, where: str, name: str, device=None):
+    """A contiguous CUDA tensor of the given type and shape (None: any size), on ``device``."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        _refuse(where, "%s must be a contiguous CUDA tensor of %s" % (name, dtype))
+    if len(t.shape) != len(shape) or any(w is not None and g != w for g, w in zip(t.shape, shape)):
+        _refuse(where, "%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if device is not None and t.device != device:
+        _refuse(where, "%s is on %s, x on %s" % (name, t.device, device))
+    return t.data_ptr()
+
+
+def _output(y, shape, dtype, where: str, name: str, device, stream):
+    """The caller's output, checked, or a new one that belongs to the stream the call runs on."""
+    if y is None:
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+    _operand(y, dtype, shape, where, name, device)
+    return y
+
+
+def _enqueue(fn, where: str, device, stream, *args):
+    """Call a library entry point with ``device`` current, on ``stream`` or the device's current one."""
+    if stream is not None and stream.device != device:
+        _refuse(where, "the stream is on %s, x on %s" % (stream.device, device))
+    if device.index == torch.cuda.current_device():
+        s = stream if stream is not None else torch.cuda.current_stream(device)
+        _check(fn(*args, s.cuda_stream), where)
+    else:
+        with torch.cuda.device(device):
+            s = stream if stream is not None else torch.cuda.current_stream(device)
+            _check(fn(*args, s.cuda_stream), where)
+
+
+def fp8_quantize_block128(x: torch.Tensor, block_rows: int = 1, q: Optional[torch.Tensor] = None,
+                          scales: Optional[torch.Tensor] = None, stream=None):
+    """(codes float8_e4m3fn like x, scales fp32) of bf16 x [R, K] or [B, R, K]: one scale per 1 x 128
+    elements (``block_rows`` 1, activations) or 128 x 128 (``block_rows`` 128, weights)."""
+    where = "fp8_quantize_block128"
+    if block_rows not in (1, 128):
+        _refuse(where, "block_rows must be 1 or 128")
+    if x.dim() not in (2, 3):
+        _refuse(where, "x must be [R, K] or [B, R, K]")
+    px = _operand(x, torch.bfloat16, (None,) * x.dim(), where, "x")
+    R, K = x.shape[-2:]
+    B = x.shape[0] if x.dim() == 3 else 1
+    sshape = (R if block_rows == 1 else (R + 127) // 128, (K + 127) // 128)
+    if x.dim() == 3 or (scales is not None and scales.dim() == 3 and B == 1):
+        sshape = (B,) + sshape
+    q = _output(q, tuple(x.shape), torch.float8_e4m3fn, where, "q", x.device, stream)
+    scales = _output(scales, sshape, torch.float32, where, "scales", x.device, stream)
+    _enqueue(lib.fp8_quantize_block128, where, x.device, stream, px, B, R, K, block_rows, q.data_ptr(),
+             scales.data_ptr())
+    return q, scales
+
+
+def fp8_gemm_block128(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                      y: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, ws: Optional[Workspace] = None,
+                      stream=None):
+    """y [T, N] (bf16 or fp32) = x w^T for E4M3 x [T, K], w [N, K] with the scales of
+    ``fp8_quantize_block128``: x_scales [T, ceil(K/128)], w_scales [ceil(N/128), ceil(K/128)].
+    ``ws`` (optional) receives a device wait that ran out in its status word."""
+    where = "fp8_gemm_block128"
+    px = _operand(x, torch.float8_e4m3fn, (None, None), where, "x")
+    T, K = x.shape
+    pw = _operand(w, torch.float8_e4m3fn, (None, K), where, "w", x.device)
+    N, KB = w.shape[0], (K + 127) // 128
+    pxs = _operand(x_scales, torch.float32, (T, KB), where, "x_scales", x.device)
+    pws = _operand(w_scales, torch.float32, ((N + 127) // 128, KB), where, "w_scales", x.device)
+    dt = out_dtype if y is None else y.dtype
+    if dt not in _OUT_TYPE:
+        _refuse(where, "the output is bfloat16 or float32, not %s" % dt)
+    y = _output(y, (T, N), dt, where, "y", x.device, stream)
+    _enqueue(lib.fp8_gemm_block128, where, x.device, stream, px, pxs, T, pw, pws, N, K, y.data_ptr(), _OUT_TYPE[dt],
+             None if ws is None else ws.buf.data_ptr(), 0 if ws is None else ws.nbytes)
+    return y
+
+
+def _grouped(where, fn, x, x_scales, w, w_scales, dtype, offsets, token_list, k, gather, scatter, y, out_dtype, ws,
+             stream):
+    px = _operand(x, dtype, (None, None), where, "x")
+    dev, K = x.device, x.shape[1]
+    pw = _operand(w, dtype, (None, None, K), where, "w", dev)
+    E, N = w.shape[:2]
+    if k < 1:
+        _refuse(where, "k must be at least 1")
+    R = x.shape[0] * k if gather else x.shape[0]
+    g = MoEGroupsC(R, E, k, 1 if gather else 0, 1 if scatter else 0,
+                   _operand(offsets, torch.int32, (E + 1,), where, "offsets", dev), None)
+    if token_list is not None:
+        g.token_list = _operand(token_list, torch.int32, (R,), where, "token_list", dev)
+    elif gather or scatter:
+        _refuse(where, "gather and scatter need token_list")
+    dt = out_dtype if y is None else y.dtype
+    if dt not in _OUT_TYPE:
+        _refuse(where, "the output is bfloat16 or float32, not %s" % dt)
+    y = _output(y, (R, N), dt, where, "y", dev, stream)
+    scales = ()
+    if w_scales is not None:
+        KB = (K + 127) // 128
+        scales = (_operand(x_scales, torch.float32, (x.shape[0], KB), where, "x_scales", dev),
+                  _operand(w_scales, torch.float32, (E, (N + 127) // 128, KB), where, "w_scales", dev))
+    operands = (px, pw) if not scales else (px, scales[0], pw, scales[1])
+    _enqueue(fn, where, dev, stream, ctypes.byref(g), *operands, N, K, y.data_ptr(), _OUT_TYPE[dt],
+             None if ws is None else ws.buf.data_ptr(), 0 if ws is None else ws.nbytes)
+    return y
+
+
+def moe_grouped_gemm_bf16(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
+                          token_list: Optional[torch.Tensor] = None, k: int = 1, gather: bool = False,
+                          scatter: bool = False, y: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                          ws: Optional[Workspace] = None, stream=None):
+    """y [R, N] (bf16 or fp32): row o(r) = w[e] x[i(r)] for the list positions r of expert e
+    (offsets[e] <= r < offsets[e+1]), with bf16 x [., K], w [E, N, K] and offsets / token_list as
+    ``moe_route_topk`` returns them. ``gather``: x is [R/k, K], the tokens, and i(r) =
+    token_list[r] / k; otherwise x is [R, K] and i(r) = r. ``scatter``: o(r) = token_list[r],
+    otherwise r. Rows that no list position writes are left as they were (a new y: undefined)."""
+    return _grouped("moe_grouped_gemm_bf16", lib.moe_grouped_gemm_bf16, x, None, w, None, torch.bfloat16, offsets,
+                    token_list, k, gather, scatter, y, out_dtype, ws, stream)
+
+
+def moe_grouped_gemm_fp8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                         offsets: torch.Tensor, token_list: Optional[torch.Tensor] = None, k: int = 1,
+                         gather: bool = False, scatter: bool = False, y: Optional[torch.Tensor] = None,
+                         out_dtype=torch.bfloat16, ws: Optional[Workspace] = None, stream=None):
+    """``moe_grouped_gemm_bf16`` with E4M3 x and w [E, N, K] and their block scales: x_scales
+    [rows of x, ceil(K/128)], w_scales [E, ceil(N/128), ceil(K/128)]."""
+    return _grouped("moe_grouped_gemm_fp8", lib.moe_grouped_gemm_fp8, x, x_scales, w, w_scales, torch.float8_e4m3fn,
+                    offsets, token_list, k, gather, scatter, y, out_dtype, ws, stream)
 
 
 # ---------------------------------------------------------------- layer

@@ -127,6 +127,49 @@ nvfp4_status dispatch_layer(const moe_layer_desc& d, const uint16_t* x, int T, u
     return from_cuda(launch_moe_decode(d, x, T, y, ids_out, w_out, ws, dev, g_wait_limit.load(), s, resid));
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Checks and launch shared by the 8-bit dense and the grouped products (P filled but for x_rows,
+// R > 0 where there is work to do).
+nvfp4_status run_product(RowsProduct P, bool fp8, int32_t y_type, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+    if (y_type != NVFP4_OUT_BF16 && y_type != NVFP4_OUT_F32) return NVFP4_ERR_INVALID_ARG;
+    if (P.R < 0 || P.R > NVFP4_MAX_PRODUCT_ROWS) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (P.N < 1 || P.N > (1 << 22) || (long long)P.E * P.N > 0x7FFFFFFFll) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    const int unit = fp8 ? 16 : 8;
+    if (P.K < unit || P.K % unit != 0 || P.K > NVFP4_MAX_PRODUCT_K) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (workspace && !aligned16(workspace)) return NVFP4_ERR_MISALIGNED;
+    if (workspace && workspace_bytes < sizeof(WsHeader)) return NVFP4_ERR_WORKSPACE_TOO_SMALL;
+    if (P.R > 0) {
+        if (!P.x || !P.w || !P.y || (fp8 && (!P.xs || !P.ws))) return NVFP4_ERR_INVALID_ARG;
+        if (!aligned16(P.x) || !aligned16(P.w) || !aligned16(P.y) || !aligned4(P.xs) || !aligned4(P.ws))
+            return NVFP4_ERR_MISALIGNED;
+    }
+    P.x_rows = P.gather ? P.R / P.k : P.R;
+    P.y_f32 = y_type == NVFP4_OUT_F32;
+    DeviceInfo dev;
+    if (nvfp4_status st = device_info(&dev); st != NVFP4_OK) return st;
+    if (P.R == 0) return NVFP4_OK;
+    return from_cuda(launch_rows_stream(P, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status run_grouped(const moe_groups* g, const void* x, const float* xs, const void* w, const float* ws,
+                         bool fp8, int32_t N, int32_t K, void* y, int32_t y_type, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    if (!g) return NVFP4_ERR_INVALID_ARG;
+    if (g->E < 1 || g->E > NVFP4_MAX_EXPERTS || g->k < 1 || g->R < 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (g->gather && g->R % g->k != 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (g->R > 0 && (!g->expert_offsets || ((g->gather || g->scatter) && !g->token_list)))
+        return NVFP4_ERR_INVALID_ARG;
+    if (!aligned4(g->expert_offsets) || !aligned4(g->token_list)) return NVFP4_ERR_MISALIGNED;
+    RowsProduct P{};
+    P.x = x, P.xs = xs, P.w = w, P.ws = ws, P.y = y;
+    P.offsets = g->expert_offsets, P.list = g->token_list;
+    P.R = g->R, P.E = g->E, P.N = N, P.K = K, P.k = g->k;
+    P.gather = g->gather != 0, P.scatter = g->scatter != 0;
+    return run_product(P, fp8, y_type, workspace, workspace_bytes, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -239,6 +282,40 @@ nvfp4_status moe_layer_forward_residual(const moe_layer_desc* d, const uint16_t*
     uint16_t* xn = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + align256(layer_bytes(*d, T)));
     if (cudaError_t e = launch_rmsnorm(h, T, d->H, norm_w, eps, xn, s); e != cudaSuccess) return NVFP4_ERR_CUDA;
     return dispatch_layer(*d, xn, T, h_out, topk_ids_out, topk_w_out, workspace, dev, s, h);
+}
+
+nvfp4_status fp8_quantize_block128(const uint16_t* x, int32_t B, int32_t R, int32_t K, int32_t block_rows,
+                                   uint8_t* q, float* scales, void* stream) {
+    if (block_rows != 1 && block_rows != 128) return NVFP4_ERR_INVALID_ARG;
+    if (B < 0 || R < 0 || (long long)B * R > 0x7FFFFFFFll) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (K < 16 || K % 16 != 0 || K > NVFP4_MAX_PRODUCT_K) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    const bool empty = B == 0 || R == 0;
+    if (!empty && (!x || !q || !scales)) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(q) || !aligned4(scales)) return NVFP4_ERR_MISALIGNED;
+    DeviceInfo dev;
+    if (nvfp4_status st = device_info(&dev); st != NVFP4_OK) return st;
+    if (empty) return NVFP4_OK;
+    return from_cuda(launch_fp8_quantize(x, B, R, K, block_rows, q, scales, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status fp8_gemm_block128(const uint8_t* x, const float* x_scales, int32_t T, const uint8_t* w,
+                               const float* w_scales, int32_t N, int32_t K, void* y, int32_t y_type,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+    RowsProduct P{};
+    P.x = x, P.xs = x_scales, P.w = w, P.ws = w_scales, P.y = y;
+    P.R = T, P.E = 1, P.N = N, P.K = K, P.k = 1;
+    return run_product(P, true, y_type, workspace, workspace_bytes, stream);
+}
+
+nvfp4_status moe_grouped_gemm_bf16(const moe_groups* g, const uint16_t* x, const uint16_t* w, int32_t N, int32_t K,
+                                   void* y, int32_t y_type, void* workspace, size_t workspace_bytes, void* stream) {
+    return run_grouped(g, x, nullptr, w, nullptr, false, N, K, y, y_type, workspace, workspace_bytes, stream);
+}
+
+nvfp4_status moe_grouped_gemm_fp8(const moe_groups* g, const uint8_t* x, const float* x_scales, const uint8_t* w,
+                                  const float* w_scales, int32_t N, int32_t K, void* y, int32_t y_type,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+    return run_grouped(g, x, x_scales, w, w_scales, true, N, K, y, y_type, workspace, workspace_bytes, stream);
 }
 
 nvfp4_status nvfp4_scale_kind_of(int32_t N, int32_t K, size_t scale_count, int32_t scale_elem_bytes,

@@ -2,6 +2,8 @@
 // arguments and calls these).
 #pragma once
 
+#include <algorithm>
+
 #include "common.cuh"
 
 namespace nvfp4 {
@@ -160,5 +162,38 @@ cudaError_t launch_moe_prefill(const moe_layer_desc& d, const uint16_t* x, int T
 // SwiGLU epilogue (x -> h, hs), mode 1 = down with the weighted epilogue (h, hs -> Y).
 cudaError_t launch_grouped_tc(const GroupedParams& P, int mode, int tiles_max, WsHeader* hdr,
                               uint64_t wait_limit, cudaStream_t s);
+
+// bf16 [B, R, K] -> E4M3 codes and fp32 scales of 1 x 128 (block_rows 1) or 128 x 128 blocks.
+cudaError_t launch_fp8_quantize(const uint16_t* x, int B, int R, int K, int block_rows, uint8_t* q, float* scales,
+                                cudaStream_t s);
+
+// Products of rows of x with one matrix (offsets NULL) or with each expert's:
+// y[o(r)] = W[e(r)] x[i(r)] for the list positions r of every expert. xs NULL: bf16 operands;
+// otherwise E4M3 codes with the scales xs [x_rows, ceil(K/128)], ws [E, ceil(N/128), ceil(K/128)].
+struct RowsProduct {
+    const void* x;           // [x_rows, K]
+    const float* xs;
+    const void* w;           // [E, N, K]
+    const float* ws;
+    void* y;                 // [R, N] bf16, or fp32 where y_f32
+    const int32_t* offsets;  // [E + 1] or NULL
+    const int32_t* list;     // [R] entries t*k + j, or NULL
+    int R, x_rows, E, N, K, k;
+    int gather, scatter, y_f32;
+};
+
+// Row of x and of y of list position r; -1 for an entry outside [0, R).
+__device__ __forceinline__ int x_row(const RowsProduct& P, int r) {
+    if (!P.gather) return r;
+    const int entry = __ldg(P.list + r);
+    return (unsigned)entry < (unsigned)P.R ? entry / P.k : -1;
+}
+__device__ __forceinline__ int y_row(const RowsProduct& P, int r) {
+    if (!P.scatter) return r;
+    const int entry = __ldg(P.list + r);
+    return (unsigned)entry < (unsigned)P.R ? entry : -1;
+}
+
+cudaError_t launch_rows_stream(const RowsProduct& P, cudaStream_t s);
 
 }  // namespace nvfp4

@@ -1,0 +1,123 @@
+"""Checks of the 8-bit and grouped products that need no GPU: the 64-bit forms that the GPU tests
+compare with, and the refusals of the C entry points (all before CUDA is touched)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import products_ref as ref
+
+
+@pytest.fixture(scope="module")
+def nv():
+    import __graft_entry__
+    __graft_entry__.build()
+    import nvfp4_w4a16_moe_gb300 as nv
+    return nv
+
+
+def test_reference_decodes_and_rounds_like_torch():
+    codes = torch.arange(256, dtype=torch.uint8)
+    want = codes.view(torch.float8_e4m3fn).float().numpy()
+    assert np.array_equal(np.isnan(want), np.isnan(ref.E4M3))
+    fin = ~np.isnan(want)
+    assert np.array_equal(want[fin], ref.E4M3[fin])
+    mid = (ref.GRID[1:] + ref.GRID[:-1]) / 2          # every tie
+    v = np.concatenate([ref.GRID, mid, mid * (1 + 1e-6), mid * (1 - 1e-6), np.linspace(0, 448, 1001)])
+    v = np.concatenate([v, -v]).astype(np.float32)
+    t = torch.from_numpy(v).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    assert np.array_equal(ref.nearest_code(v.astype(np.float64)), t)
+
+
+def test_quantised_values_are_within_half_a_step():
+    g = torch.Generator().manual_seed(3)
+    x = (torch.randn(2, 130, 200, generator=g) * 3).to(torch.bfloat16)
+    for br in (1, 128):
+        q, s = ref.quantize(x, br)
+        back = ref.E4M3[q] * ref.spread(s.astype(np.float64), br, 130, 200)
+        d = ref.f64(x)
+        amax = ref.spread(s.astype(np.float64), br, 130, 200) * 448
+        # half a step of E4M3 is 2^-4 of the value, or 2^-10 of the scale below the smallest normal
+        assert np.all(np.abs(back - d) <= np.maximum(np.abs(d) * 2.0 ** -4, amax / 448 * 2.0 ** -10) * (1 + 1e-6))
+
+
+def test_ratio_of_bf16_significands_stays_off_the_rounding_points():
+    """The quantiser rounds 448 x / a from an fp32 value within 2^-22 of it, put on 16 significant
+    bits: no quotient of two bf16 significands comes nearer than 2^-13 to a point where the
+    rounding changes without being on it."""
+    m = np.arange(128, 256)
+    nearest = np.inf
+    for j in range(1, 32, 2):
+        for d in range(-12, 13):
+            num = 7 * m[:, None] * 2.0 ** d - j * m[None, :]
+            rel = np.abs(num) / (j * m[None, :])
+            nearest = min(nearest, rel[rel > 0].min())
+    assert nearest >= 2.0 ** -13
+
+
+FAKE = 0x100000        # never dereferenced: the checks fail first
+
+
+def _status(nv, fn, *args):
+    return getattr(nv.lib, fn)(*args)
+
+
+def test_quantize_refusals(nv):
+    call = lambda x=FAKE, B=1, R=4, K=64, br=1, q=FAKE, s=FAKE: _status(nv, "fp8_quantize_block128", x, B, R, K, br,
+                                                                        q, s, None)
+    assert call(br=64) == nv.NVFP4_ERR_INVALID_ARG
+    for kw in (dict(x=None), dict(q=None), dict(s=None)):
+        assert call(**kw) == nv.NVFP4_ERR_INVALID_ARG
+    for kw in (dict(B=-1), dict(R=-1), dict(K=0), dict(K=8), dict(K=24), dict(K=65552), dict(B=1 << 16, R=1 << 16)):
+        assert call(**kw) == nv.NVFP4_ERR_UNSUPPORTED_SHAPE
+    for kw in (dict(x=FAKE + 8), dict(q=FAKE + 8), dict(s=FAKE + 2)):
+        assert call(**kw) == nv.NVFP4_ERR_MISALIGNED
+
+
+def test_dense_refusals(nv):
+    def call(x=FAKE, xs=FAKE, T=4, w=FAKE, ws=FAKE, N=16, K=64, y=FAKE, yt=0, wk=None, wb=0):
+        return _status(nv, "fp8_gemm_block128", x, xs, T, w, ws, N, K, y, yt, wk, wb, None)
+    assert call(yt=2) == nv.NVFP4_ERR_INVALID_ARG
+    for kw in (dict(x=None), dict(xs=None), dict(w=None), dict(ws=None), dict(y=None)):
+        assert call(**kw) == nv.NVFP4_ERR_INVALID_ARG
+    for kw in (dict(T=-1), dict(T=(1 << 20) + 1), dict(N=0), dict(N=(1 << 22) + 1), dict(K=0), dict(K=40),
+               dict(K=65552)):
+        assert call(**kw) == nv.NVFP4_ERR_UNSUPPORTED_SHAPE
+    for kw in (dict(x=FAKE + 8), dict(w=FAKE + 4), dict(y=FAKE + 2), dict(xs=FAKE + 2), dict(ws=FAKE + 1),
+               dict(wk=FAKE + 8, wb=256)):
+        assert call(**kw) == nv.NVFP4_ERR_MISALIGNED
+    assert call(wk=FAKE, wb=128) == nv.NVFP4_ERR_WORKSPACE_TOO_SMALL
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_grouped_refusals(nv, fp8):
+    def call(R=8, E=4, k=2, gather=0, scatter=0, off=FAKE, lst=FAKE, x=FAKE, w=FAKE, N=16, K=64, y=FAKE, yt=0,
+             wk=None, wb=0, xs=FAKE, ws=FAKE, null=False):
+        g = nv.MoEGroupsC(R, E, k, gather, scatter, off, lst)
+        p = None if null else ctypes.byref(g)
+        if fp8:
+            return _status(nv, "moe_grouped_gemm_fp8", p, x, xs, w, ws, N, K, y, yt, wk, wb, None)
+        return _status(nv, "moe_grouped_gemm_bf16", p, x, w, N, K, y, yt, wk, wb, None)
+    for kw in (dict(null=True), dict(off=None), dict(lst=None, gather=1), dict(lst=None, scatter=1), dict(x=None),
+               dict(w=None), dict(y=None), dict(yt=-1)):
+        assert call(**kw) == nv.NVFP4_ERR_INVALID_ARG
+    for kw in (dict(R=-1), dict(R=(1 << 20) + 2), dict(E=0), dict(E=257), dict(k=0), dict(R=7, gather=1), dict(N=0),
+               dict(K=0), dict(K=20), dict(K=24 if fp8 else 4), dict(E=256, N=1 << 23)):
+        assert call(**kw) == nv.NVFP4_ERR_UNSUPPORTED_SHAPE, kw
+    assert call(E=256, N=1 << 22, x=None) == nv.NVFP4_ERR_INVALID_ARG    # 2^30 rows of W: the next check is reached
+    for kw in (dict(x=FAKE + 8), dict(w=FAKE + 8), dict(y=FAKE + 4), dict(off=FAKE + 2), dict(lst=FAKE + 1)):
+        assert call(**kw) == nv.NVFP4_ERR_MISALIGNED
+    if fp8:
+        assert call(xs=None) == nv.NVFP4_ERR_INVALID_ARG and call(ws=FAKE + 2) == nv.NVFP4_ERR_MISALIGNED
+    assert call(wk=FAKE, wb=16) == nv.NVFP4_ERR_WORKSPACE_TOO_SMALL
+
+
+def test_python_refuses_host_tensors(nv):
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(nv.NVFP4Error):
+        nv.fp8_quantize_block128(x)
+    with pytest.raises(nv.NVFP4Error):
+        nv.fp8_quantize_block128(x, block_rows=64)
+    with pytest.raises(nv.NVFP4Error):
+        nv.moe_grouped_gemm_bf16(x, torch.zeros(2, 8, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32))
