@@ -45,14 +45,11 @@
 // bf16 of the same value times 2^-112; one bf16x2 multiply by (block scale * 2^112)
 // restores the scale. Every product has at most 6 significant bits and lies in
 // [2^-10, 2688], so no step rounds.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <cstring>
-#include <mutex>
 
 #include "common.cuh"
 #include "kernels.cuh"
+#include "tc_common.cuh"
 
 namespace nvfp4 {
 
@@ -86,98 +83,6 @@ constexpr int kNumBars = 2 * kMaxRaw + 2 * kMaxB + 4 + 1;
 constexpr int kSmemBytes = 1024 + kOffBar + kNumBars * 8 + 16;
 constexpr int kTmemCols = 512;
 constexpr int kAccStride = 256;   // TMEM column offset of the second accumulator
-
-// ---------------------------------------------------------------- PTX wrappers
-__device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, uint32_t src_bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(src_bytes) : "memory");
-}
-
-// Arrive on `bar` when every cp.async issued so far by this thread has landed (the
-// arrival is counted in the barrier's expected count).
-__device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(su32(bar)) : "memory");
-}
-
-// 2D tensor copy global -> shared (TMA), completing on `bar`'s transaction count.
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(su32(bar)) : "memory");
-}
-
-// generic-proxy writes to shared memory -> visible to the tensor cores' async proxy
-__device__ __forceinline__ void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(su32(bar)) : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// TMEM allocation (one full warp); the allocated base address is written to *slot.
-template <int kCols>
-__device__ __forceinline__ void tmem_alloc(uint32_t* slot) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(su32(slot)), "n"(kCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-template <int kCols>
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(taddr), "n"(kCols) : "memory");
-}
-
-// Shared-memory matrix descriptor: K-major operand in the 128-byte swizzle layout
-// (8-row x 128-byte atoms, 1024 bytes apart); start address in 16-byte units.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu)      // start address
-           | ((uint64_t)1 << 16)                    // leading byte offset (unused for swizzled K-major)
-           | ((uint64_t)(1024 >> 4) << 32)          // stride byte offset: next 8-row group
-           | ((uint64_t)1 << 46)                    // descriptor version
-           | ((uint64_t)2 << 61);                   // swizzle mode: 128-byte
-}
-
-// Instruction descriptor of kind::f16: bf16 A and B (both K-major), fp32 D, M x N.
-__device__ __forceinline__ uint32_t f16_idesc(int M, int N) {
-    return (1u << 4)                                // D format: f32
-           | (1u << 7)                              // A format: bf16
-           | (1u << 10)                             // B format: bf16
-           | ((uint32_t)(N >> 3) << 17)             // N / 8
-           | ((uint32_t)(M >> 4) << 24);            // M / 16
-}
-
-__device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-        :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
-}
-
-// Arrive on `bar` once every MMA issued so far by this thread has completed.
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(su32(bar))
-                 : "memory");
-}
-
-// 16 consecutive fp32 columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void named_bar_sync(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
-}
 
 // ---------------------------------------------------------------- NVFP4 -> bf16
 // Two E4M3 block scales (low 16 bits of `two`) -> two bf16x2 words, each holding
@@ -245,30 +150,6 @@ __device__ __forceinline__ bool locate_tc_tile(const GroupedParams& P, int tt, T
         tr->n_rows = min(kTokTile, P.T - tr->p0);
     }
     return true;
-}
-
-// Bounded wait on an mbarrier phase. A wait that runs out records the timeout and
-// raises the CTA's abort flag; once raised, every wait returns at once.
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                              WsHeader* hdr, unsigned long long limit_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = global_timer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (*abort_flag) return false;
-        if (global_timer_ns() - t0 > limit_ns) {
-            *abort_flag = 1;
-            record_status(hdr, NVFP4_ERR_DEVICE_TIMEOUT);
-            return false;
-        }
-    }
-    return true;
-}
-
-// Bounded wait that ignores the abort flag: after an abort, a thread that issued bulk copies
-// or MMAs waits (with the library's fixed limit) until they have landed, so that the CTA
-// never exits with its own asynchronous operations in flight.
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
-    mbar_wait_bounded(bar, parity, kDefaultWaitLimit);
 }
 
 constexpr int kHS = kM + 8;   // bf16 staging row stride of the gate/up epilogue
@@ -613,20 +494,6 @@ grouped_tc_kernel(const GroupedParams P, const __grid_constant__ TcMaps maps, in
 }  // namespace
 
 namespace {
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
 
 // Byte matrix [rows, inner] read in boxes of box_inner bytes x 128 rows.
 bool encode_u8(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* m, const void* base, uint64_t inner,

@@ -194,6 +194,9 @@ __device__ __forceinline__ int y_row(const RowsProduct& P, int r) {
     return (unsigned)entry < (unsigned)P.R ? entry : -1;
 }
 
+// Few rows: weights streamed through warp-level MMAs. Many rows: tcgen05 tiles.
 cudaError_t launch_rows_stream(const RowsProduct& P, cudaStream_t s);
+cudaError_t launch_rows_tc(const RowsProduct& P, WsHeader* hdr, const DeviceInfo& dev, uint64_t wait_limit,
+                           cudaStream_t s);
 
 }  // namespace nvfp4

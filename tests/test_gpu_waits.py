@@ -125,3 +125,37 @@ def test_multi_token_path_has_no_waits(nv):
         nv.set_device_wait_limit(0)
     assert ws.status() == nv.NVFP4_OK
     check_layer_parity(L, x, y, ids, w)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_products_wait_timeout_is_reported(nv, fp8):
+    """The tile products' barrier waits with the limit at 1 ns: the status and the NaN rows go together,
+    the CTAs drain their copies and MMAs and return, and the next call is exact again."""
+    g = torch.Generator().manual_seed(4)
+    T, N, K = 700, 513, 4096
+    x = torch.randint(-2, 3, (T, K), generator=g).float()
+    w = torch.randint(-2, 3, (N, K), generator=g).float()
+    want = (x @ w.t()).cuda()
+    off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    ws = nv.Workspace(256)
+    y = torch.zeros(T, N, device="cuda")
+    if fp8:
+        one = lambda r: torch.ones(r, K // 128, device="cuda")
+        xq, wq = x.to(torch.float8_e4m3fn).cuda(), w.to(torch.float8_e4m3fn).cuda()
+        call = lambda: nv.fp8_gemm_block128(xq, one(T), wq, one((N + 127) // 128), y=y, ws=ws)
+    else:
+        xb, wb = x.to(torch.bfloat16).cuda(), w.to(torch.bfloat16).cuda()[None]
+        call = lambda: nv.moe_grouped_gemm_bf16(xb, wb, off, y=y, ws=ws)
+    try:
+        nv.set_device_wait_limit(1)
+        call()
+        torch.cuda.synchronize()
+        code = ws.status(clear=True)
+        nan = bool(torch.isnan(y).any())
+        assert (code == nv.NVFP4_ERR_DEVICE_TIMEOUT) == nan
+        assert code in (nv.NVFP4_OK, nv.NVFP4_ERR_DEVICE_TIMEOUT)
+    finally:
+        nv.set_device_wait_limit(0)
+    call()
+    assert ws.status() == nv.NVFP4_OK
+    assert torch.equal(y, want)
