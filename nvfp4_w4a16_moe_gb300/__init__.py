@@ -298,39 +298,48 @@ def _refuse(where: str, why: str, status: int = NVFP4_ERR_INVALID_ARG):
     raise NVFP4Error(status, "%s: %s" % (where, why))
 
 
-def _operand(t: torch.Tensor, dtype, shape, where: str, name: str, device=None):
-    """A contiguous CUDA tensor of the given type and shape (None: any size), on ``device``."""
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        _refuse(where, "%s must be a contiguous CUDA tensor of %s" % (name, dtype))
-    if len(t.shape) != len(shape) or any(w is not None and g != w for g, w in zip(t.shape, shape)):
-        _refuse(where, "%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if device is not None and t.device != device:
-        _refuse(where, "%s is on %s, x on %s" % (name, t.device, device))
-    return t.data_ptr()
+def _first(t: torch.Tensor, dtype, where: str, dims=(2,)):
+    """(address, shape, device index) of x, the operand that names the device of a call."""
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.dim() not in dims:
+        _refuse(where, "x must be a contiguous CUDA tensor of %s with %s dimensions" % (
+            dtype, " or ".join(map(str, dims))))
+    shape = t.shape
+    if max(shape) > 0x7FFFFFFF:          # the C ABI takes int32
+        _refuse(where, "x has shape %s" % (tuple(shape),), NVFP4_ERR_UNSUPPORTED_SHAPE)
+    return t.data_ptr(), shape, t.get_device()
 
 
-def _output(y, shape, dtype, where: str, name: str, device, stream):
-    """The caller's output, checked, or a new one that belongs to the stream the call runs on."""
-    if y is None:
-        if stream is None:
-            return torch.empty(shape, dtype=dtype, device=device)
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=device)
-    _operand(y, dtype, shape, where, name, device)
-    return y
+def _operand(t: torch.Tensor, dtype, shape, index: int, where: str, name: str):
+    """The address of a contiguous tensor of this type and shape on CUDA device ``index``."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(where, "%s must be a contiguous tensor of %s with shape %s on cuda:%d, not %s %s on %s"
+            % (name, dtype, tuple(shape), index, t.dtype, tuple(t.shape), t.device))
 
 
-def _enqueue(fn, where: str, device, stream, *args):
-    """Call a library entry point with ``device`` current, on ``stream`` or the device's current one."""
-    if stream is not None and stream.device != device:
-        _refuse(where, "the stream is on %s, x on %s" % (stream.device, device))
-    if device.index == torch.cuda.current_device():
-        s = stream if stream is not None else torch.cuda.current_stream(device)
-        _check(fn(*args, s.cuda_stream), where)
+def _output(shape, dtype, device, stream):
+    """A new output that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _enqueue(fn, where: str, index: int, stream, *args):
+    """Call a library entry point with device ``index`` current, on ``stream`` or the device's current one."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)     # torch.cuda.current_stream builds an object: 2 us
+    elif stream.device.index != index:
+        _refuse(where, "the stream is on %s, x on cuda:%d" % (stream.device, index))
     else:
-        with torch.cuda.device(device):
-            s = stream if stream is not None else torch.cuda.current_stream(device)
-            _check(fn(*args, s.cuda_stream), where)
+        raw = stream.cuda_stream
+    if index == torch.cuda.current_device():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, raw)
+    if status != NVFP4_OK:
+        raise NVFP4Error(status, where)
 
 
 def fp8_quantize_block128(x: torch.Tensor, block_rows: int = 1, q: Optional[torch.Tensor] = None,
@@ -338,20 +347,19 @@ def fp8_quantize_block128(x: torch.Tensor, block_rows: int = 1, q: Optional[torc
     """(codes float8_e4m3fn like x, scales fp32) of bf16 x [R, K] or [B, R, K]: one scale per 1 x 128
     elements (``block_rows`` 1, activations) or 128 x 128 (``block_rows`` 128, weights)."""
     where = "fp8_quantize_block128"
-    if block_rows not in (1, 128):
+    if block_rows != 1 and block_rows != 128:
         _refuse(where, "block_rows must be 1 or 128")
-    if x.dim() not in (2, 3):
-        _refuse(where, "x must be [R, K] or [B, R, K]")
-    px = _operand(x, torch.bfloat16, (None,) * x.dim(), where, "x")
-    R, K = x.shape[-2:]
-    B = x.shape[0] if x.dim() == 3 else 1
-    sshape = (R if block_rows == 1 else (R + 127) // 128, (K + 127) // 128)
-    if x.dim() == 3 or (scales is not None and scales.dim() == 3 and B == 1):
-        sshape = (B,) + sshape
-    q = _output(q, tuple(x.shape), torch.float8_e4m3fn, where, "q", x.device, stream)
-    scales = _output(scales, sshape, torch.float32, where, "scales", x.device, stream)
-    _enqueue(lib.fp8_quantize_block128, where, x.device, stream, px, B, R, K, block_rows, q.data_ptr(),
-             scales.data_ptr())
+    px, shape, dev = _first(x, torch.bfloat16, where, (2, 3))
+    R, K = shape[-2:]
+    B = shape[0] if len(shape) == 3 else 1
+    sshape = (*shape[:-2], R if block_rows == 1 else (R + 127) // 128, (K + 127) // 128)
+    if q is None:
+        q = _output(shape, torch.float8_e4m3fn, x.device, stream)
+    if scales is None:
+        scales = _output(sshape, torch.float32, x.device, stream)
+    _enqueue(lib.fp8_quantize_block128, where, dev, stream, px, B, R, K, block_rows,
+             _operand(q, torch.float8_e4m3fn, shape, dev, where, "q"),
+             _operand(scales, torch.float32, sshape, dev, where, "scales"))
     return q, scales
 
 
@@ -362,48 +370,53 @@ def fp8_gemm_block128(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, 
     ``fp8_quantize_block128``: x_scales [T, ceil(K/128)], w_scales [ceil(N/128), ceil(K/128)].
     ``ws`` (optional) receives a device wait that ran out in its status word."""
     where = "fp8_gemm_block128"
-    px = _operand(x, torch.float8_e4m3fn, (None, None), where, "x")
-    T, K = x.shape
-    pw = _operand(w, torch.float8_e4m3fn, (None, K), where, "w", x.device)
+    px, (T, K), dev = _first(x, torch.float8_e4m3fn, where)
     N, KB = w.shape[0], (K + 127) // 128
-    pxs = _operand(x_scales, torch.float32, (T, KB), where, "x_scales", x.device)
-    pws = _operand(w_scales, torch.float32, ((N + 127) // 128, KB), where, "w_scales", x.device)
-    dt = out_dtype if y is None else y.dtype
-    if dt not in _OUT_TYPE:
-        _refuse(where, "the output is bfloat16 or float32, not %s" % dt)
-    y = _output(y, (T, N), dt, where, "y", x.device, stream)
-    _enqueue(lib.fp8_gemm_block128, where, x.device, stream, px, pxs, T, pw, pws, N, K, y.data_ptr(), _OUT_TYPE[dt],
+    if y is None:
+        y = _output((T, N), out_dtype, x.device, stream)
+    if y.dtype not in _OUT_TYPE:
+        _refuse(where, "the output is bfloat16 or float32, not %s" % y.dtype)
+    _enqueue(lib.fp8_gemm_block128, where, dev, stream, px,
+             _operand(x_scales, torch.float32, (T, KB), dev, where, "x_scales"), T,
+             _operand(w, torch.float8_e4m3fn, (N, K), dev, where, "w"),
+             _operand(w_scales, torch.float32, ((N + 127) // 128, KB), dev, where, "w_scales"), N, K,
+             _operand(y, y.dtype, (T, N), dev, where, "y"), _OUT_TYPE[y.dtype],
              None if ws is None else ws.buf.data_ptr(), 0 if ws is None else ws.nbytes)
     return y
 
 
 def _grouped(where, fn, x, x_scales, w, w_scales, dtype, offsets, token_list, k, gather, scatter, y, out_dtype, ws,
              stream):
-    px = _operand(x, dtype, (None, None), where, "x")
-    dev, K = x.device, x.shape[1]
-    pw = _operand(w, dtype, (None, None, K), where, "w", dev)
-    E, N = w.shape[:2]
+    px, (rows, K), dev = _first(x, dtype, where)
+    if w.dim() != 3:
+        _refuse(where, "w must be [E, N, K]")
+    E, N, _ = w.shape
     if k < 1:
         _refuse(where, "k must be at least 1")
-    R = x.shape[0] * k if gather else x.shape[0]
-    g = MoEGroupsC(R, E, k, 1 if gather else 0, 1 if scatter else 0,
-                   _operand(offsets, torch.int32, (E + 1,), where, "offsets", dev), None)
+    R = rows * k if gather else rows
+    if R > 0x7FFFFFFF or k > 0x7FFFFFFF:
+        _refuse(where, "%d list positions" % R, NVFP4_ERR_UNSUPPORTED_SHAPE)
     if token_list is not None:
-        g.token_list = _operand(token_list, torch.int32, (R,), where, "token_list", dev)
+        pl = _operand(token_list, torch.int32, (R,), dev, where, "token_list")
     elif gather or scatter:
         _refuse(where, "gather and scatter need token_list")
-    dt = out_dtype if y is None else y.dtype
-    if dt not in _OUT_TYPE:
-        _refuse(where, "the output is bfloat16 or float32, not %s" % dt)
-    y = _output(y, (R, N), dt, where, "y", dev, stream)
-    scales = ()
-    if w_scales is not None:
+    else:
+        pl = None
+    g = MoEGroupsC(R, E, k, 1 if gather else 0, 1 if scatter else 0,
+                   _operand(offsets, torch.int32, (E + 1,), dev, where, "offsets"), pl)
+    if y is None:
+        y = _output((R, N), out_dtype, x.device, stream)
+    if y.dtype not in _OUT_TYPE:
+        _refuse(where, "the output is bfloat16 or float32, not %s" % y.dtype)
+    pw = _operand(w, dtype, (E, N, K), dev, where, "w")
+    if w_scales is None:
+        operands = (px, pw)
+    else:
         KB = (K + 127) // 128
-        scales = (_operand(x_scales, torch.float32, (x.shape[0], KB), where, "x_scales", dev),
-                  _operand(w_scales, torch.float32, (E, (N + 127) // 128, KB), where, "w_scales", dev))
-    operands = (px, pw) if not scales else (px, scales[0], pw, scales[1])
-    _enqueue(fn, where, dev, stream, ctypes.byref(g), *operands, N, K, y.data_ptr(), _OUT_TYPE[dt],
-             None if ws is None else ws.buf.data_ptr(), 0 if ws is None else ws.nbytes)
+        operands = (px, _operand(x_scales, torch.float32, (rows, KB), dev, where, "x_scales"), pw,
+                    _operand(w_scales, torch.float32, (E, (N + 127) // 128, KB), dev, where, "w_scales"))
+    _enqueue(fn, where, dev, stream, ctypes.byref(g), *operands, N, K, _operand(y, y.dtype, (R, N), dev, where, "y"),
+             _OUT_TYPE[y.dtype], None if ws is None else ws.buf.data_ptr(), 0 if ws is None else ws.nbytes)
     return y
 
 
