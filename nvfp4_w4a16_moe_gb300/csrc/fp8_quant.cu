@@ -80,8 +80,8 @@ __device__ __forceinline__ uint2 quantize8(const uint4 v, const BlockScale b) {
 constexpr int kUnroll = 4;
 
 __global__ void __launch_bounds__(kQThreads)
-quantize_rows_kernel(const uint16_t* __restrict__ x, size_t blocks, int K, int KB, uint8_t* __restrict__ q,
-                     float* __restrict__ scales) {
+quantize_rows_kernel(const uint16_t* x, size_t blocks, int K, int KB, uint8_t* q,
+                     float* scales) {
     const int lane = threadIdx.x & 31, unit = lane & 15, half = lane >> 4;
     const size_t warp = (size_t)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
     const size_t first = warp * (2 * kUnroll) + half;
@@ -97,7 +97,7 @@ quantize_rows_kernel(const uint16_t* __restrict__ x, size_t blocks, int K, int K
             const int col = (int)(blk - row * KB) * 128 + unit * 8;
             if (col < K) {
                 at[u] = row * K + col;
-                v[u] = ld_stream_v4(x + at[u]);
+                v[u] = ld_once_v4(x + at[u]);
             }
         }
     }
@@ -114,8 +114,8 @@ quantize_rows_kernel(const uint16_t* __restrict__ x, size_t blocks, int K, int K
 
 // 128 x 128 blocks: one CTA per block, which it keeps in registers (eight 16-byte units a thread).
 __global__ void __launch_bounds__(kQThreads)
-quantize_tiles_kernel(const uint16_t* __restrict__ x, int R, int K, int RB, int KB, uint8_t* __restrict__ q,
-                      float* __restrict__ scales) {
+quantize_tiles_kernel(const uint16_t* x, int R, int K, int RB, int KB, uint8_t* q,
+                      float* scales) {
     __shared__ uint32_t s_max[kQThreads / 32];
     const size_t blk = blockIdx.x;
     const size_t mat = blk / ((size_t)RB * KB);
@@ -128,7 +128,7 @@ quantize_tiles_kernel(const uint16_t* __restrict__ x, int R, int K, int RB, int 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         v[i] = make_uint4(0, 0, 0, 0);
-        if (col < K && row0 + 16 * i < R) v[i] = ld_stream_v4(x + base + (size_t)16 * i * K);
+        if (col < K && row0 + 16 * i < R) v[i] = ld_once_v4(x + base + (size_t)16 * i * K);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, absmax8(v[i]));

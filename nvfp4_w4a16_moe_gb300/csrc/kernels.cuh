@@ -163,6 +163,14 @@ cudaError_t launch_moe_prefill(const moe_layer_desc& d, const uint16_t* x, int T
 cudaError_t launch_grouped_tc(const GroupedParams& P, int mode, int tiles_max, WsHeader* hdr,
                               uint64_t wait_limit, cudaStream_t s);
 
+// Data read once (weights, the quantiser's input): past L1.
+__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
 // bf16 [B, R, K] -> E4M3 codes and fp32 scales of 1 x 128 (block_rows 1) or 128 x 128 blocks.
 cudaError_t launch_fp8_quantize(const uint16_t* x, int B, int R, int K, int block_rows, uint8_t* q, float* scales,
                                 cudaStream_t s);
@@ -185,12 +193,12 @@ struct RowsProduct {
 // Row of x and of y of list position r; -1 for an entry outside [0, R).
 __device__ __forceinline__ int x_row(const RowsProduct& P, int r) {
     if (!P.gather) return r;
-    const int entry = __ldg(P.list + r);
+    const int entry = P.list[r];
     return (unsigned)entry < (unsigned)P.R ? entry / P.k : -1;
 }
 __device__ __forceinline__ int y_row(const RowsProduct& P, int r) {
     if (!P.scatter) return r;
-    const int entry = __ldg(P.list + r);
+    const int entry = P.list[r];
     return (unsigned)entry < (unsigned)P.R ? entry : -1;
 }
 

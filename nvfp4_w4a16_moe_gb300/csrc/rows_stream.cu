@@ -53,8 +53,8 @@ __device__ __forceinline__ bool locate_pass(const RowsProduct& P, int p, int* e,
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int lo = 0, cnt = 0;
     if ((int)threadIdx.x < P.E) {   // NVFP4_MAX_EXPERTS = kSThreads
-        lo = min(max(__ldg(P.offsets + threadIdx.x), 0), P.R);
-        cnt = max(min(max(__ldg(P.offsets + threadIdx.x + 1), 0), P.R) - lo, 0);
+        lo = min(max(P.offsets[threadIdx.x], 0), P.R);
+        cnt = max(min(max(P.offsets[threadIdx.x + 1], 0), P.R) - lo, 0);
     }
     const int mine = (cnt + kRows - 1) / kRows;
     int incl = mine;
@@ -83,20 +83,24 @@ __device__ __forceinline__ bool locate_pass(const RowsProduct& P, int p, int* e,
 }
 
 template <bool FP8, int NB>
-__global__ void __launch_bounds__(kSThreads)
-rows_stream_kernel(const RowsProduct P, int n_tiles) {
+__global__ void __launch_bounds__(kSThreads, NB == 1 ? 3 : 2)
+rows_stream_kernel(const RowsProduct P, int n_tiles, int k_split) {
     constexpr int kRows = 8 * NB;
-    __shared__ float s_acc[kSWarps][16][kRows];
-    const int pass = blockIdx.x / n_tiles, n0 = (blockIdx.x - pass * n_tiles) * 16;
+    __shared__ float s_acc[kSWarps][16][kRows + 1];
+    // row tiles of this CTA: one for every k_split warps
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int k_part = warp & (k_split - 1), n_part = warp / k_split;
+    const int pass = blockIdx.x / n_tiles;
+    const int n0 = ((blockIdx.x - pass * n_tiles) * (kSWarps / k_split) + n_part) * 16;
     int e, r0, rows;
     if (!locate_pass<kRows>(P, pass, &e, &r0, &rows)) return;
 
     constexpr int kUnit = FP8 ? 16 : 8;            // elements of a 16-byte unit
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
     const int units = P.K / kUnit;                 // units of a row
     const int chunks = (units + 7) >> 3;
     const int KB = (P.K + 127) >> 7;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
 
     const uint4* w0 = nullptr;
     const uint4* w1 = nullptr;
@@ -105,6 +109,19 @@ rows_stream_kernel(const RowsProduct P, int n_tiles) {
         if (n0 + g < P.N) w0 = w + (size_t)g * units;
         if (n0 + g + 8 < P.N) w1 = w + (size_t)(g + 8) * units;
     }
+    uint4 a[kSAhead][2][2];
+    auto load_w = [&](int ch0) {
+#pragma unroll
+        for (int i = 0; i < kSAhead; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int u = (ch0 + i * k_split) * 8 + 4 * h + c;
+                a[i][h][0] = w0 != nullptr && u < units ? ld_once_v4(w0 + u) : zero;
+                a[i][h][1] = w1 != nullptr && u < units ? ld_once_v4(w1 + u) : zero;
+            }
+    };
+    load_w(k_part);                                // on its way while the list is read
+
     const uint4* xr[NB];
     const float* xs[NB][2];
 #pragma unroll
@@ -112,45 +129,35 @@ rows_stream_kernel(const RowsProduct P, int n_tiles) {
         const int row = 8 * b + g < rows ? x_row(P, r0 + 8 * b + g) : -1;
         xr[b] = row < 0 ? nullptr : static_cast<const uint4*>(P.x) + (size_t)row * units;
         if constexpr (FP8) {
+            // the rows of this lane's two columns are those of the lanes 4 * column
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int col = 8 * b + 2 * c + j;
-                const int cr = col < rows ? x_row(P, r0 + col) : -1;
+                const int cr = __shfl_sync(0xffffffffu, row, 4 * (2 * c + j));
                 xs[b][j] = cr < 0 ? nullptr : P.xs + (size_t)cr * KB;
             }
         }
     }
-    const float* wsc = FP8 ? P.ws + ((size_t)e * ((P.N + 127) >> 7) + (n0 >> 7)) * KB : nullptr;
+    const float* wsc = FP8 ? P.ws + ((size_t)e * ((P.N + 127) >> 7) + (min(n0, P.N - 1) >> 7)) * KB : nullptr;
 
-    const uint4 zero = make_uint4(0, 0, 0, 0);
     float acc[NB][4];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[b][i] = 0.f;
 
-    for (int ch0 = warp; ch0 < chunks; ch0 += kSWarps * kSAhead) {
-        uint4 a[kSAhead][2][2];
-#pragma unroll
-        for (int i = 0; i < kSAhead; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int u = (ch0 + i * kSWarps) * 8 + 4 * h + c;
-                a[i][h][0] = w0 != nullptr && u < units ? ld_stream_v4(w0 + u) : zero;
-                a[i][h][1] = w1 != nullptr && u < units ? ld_stream_v4(w1 + u) : zero;
-            }
+    for (int ch0 = k_part; ch0 < chunks; ch0 += k_split * kSAhead) {
 #pragma unroll
         for (int i = 0; i < kSAhead; ++i) {
-            const int ch = ch0 + i * kSWarps;
+            const int ch = ch0 + i * k_split;
             if (ch >= chunks) break;
-            const float sw = FP8 ? __ldg(wsc + ch) : 0.f;
+            const float sw = FP8 ? wsc[ch] : 0.f;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int u = ch * 8 + 4 * h + c;
-                    const uint4 x = xr[b] != nullptr && u < units ? __ldg(xr[b] + u) : zero;
+                    const uint4 x = xr[b] != nullptr && u < units ? xr[b][u] : zero;
                     const uint4 p = a[i][h][0], q = a[i][h][1];
                     if constexpr (FP8) {
                         mma_e4m3(part, p.x, q.x, p.y, q.y, x.x, x.y);
@@ -161,8 +168,8 @@ rows_stream_kernel(const RowsProduct P, int n_tiles) {
                     }
                 }
                 if constexpr (FP8) {
-                    const float s0 = xs[b][0] != nullptr ? __ldg(xs[b][0] + ch) * sw : 0.f;
-                    const float s1 = xs[b][1] != nullptr ? __ldg(xs[b][1] + ch) * sw : 0.f;
+                    const float s0 = xs[b][0] != nullptr ? xs[b][0][ch] * sw : 0.f;
+                    const float s1 = xs[b][1] != nullptr ? xs[b][1][ch] * sw : 0.f;
                     acc[b][0] = fmaf(part[0], s0, acc[b][0]);
                     acc[b][1] = fmaf(part[1], s1, acc[b][1]);
                     acc[b][2] = fmaf(part[2], s0, acc[b][2]);
@@ -170,6 +177,7 @@ rows_stream_kernel(const RowsProduct P, int n_tiles) {
                 }
             }
         }
+        if (ch0 + k_split * kSAhead < chunks) load_w(ch0 + k_split * kSAhead);
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -179,15 +187,16 @@ rows_stream_kernel(const RowsProduct P, int n_tiles) {
         s_acc[warp][g + 8][8 * b + 2 * c + 1] = acc[b][3];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * rows; i += kSThreads) {
-        const int col = i >> 4, m = i & 15;
-        if (n0 + m >= P.N) continue;
+    // the K parts of a tile are added in order; neighbouring threads write neighbouring outputs
+    const int span = kSWarps / k_split * 16, first = (blockIdx.x - pass * n_tiles) * span;
+    for (int i = threadIdx.x; i < span * rows; i += kSThreads) {
+        const int col = i / span, m = i - col * span;
+        if (first + m >= P.N) continue;
         float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < kSWarps; ++w) v += s_acc[w][m][col];
+        for (int w = 0; w < k_split; ++w) v += s_acc[(m >> 4) * k_split + w][m & 15][col];
         const int row = y_row(P, r0 + col);
         if (row < 0) continue;
-        const size_t at = (size_t)row * P.N + n0 + m;
+        const size_t at = (size_t)row * P.N + first + m;
         if (P.y_f32) static_cast<float*>(P.y)[at] = v;
         else static_cast<uint16_t*>(P.y)[at] = f32_to_bf16(v);
     }
@@ -195,13 +204,18 @@ rows_stream_kernel(const RowsProduct P, int n_tiles) {
 
 template <bool FP8, int NB>
 cudaError_t launch_stream(const RowsProduct& P, cudaStream_t s) {
-    const int n_tiles = (P.N + 15) / 16, rows = 8 * NB;
+    constexpr int rows = 8 * NB;
+    // warps to a row's K: as many as leave each two chunks, so that short rows share a CTA instead
+    const int chunks = (P.K * (FP8 ? 1 : 2) + 127) / 128;
+    int k_split = kSWarps;
+    while (k_split > 1 && chunks < 2 * k_split) k_split /= 2;
+    const int span = kSWarps / k_split * 16, n_tiles = (P.N + span - 1) / span;
     // every pass but an expert's last is full, and every pass has a row
     const long long full = (P.R + rows - 1) / rows;
     const long long passes = P.offsets == nullptr ? full : std::min<long long>(P.R, full + P.E);
     const long long grid = passes * n_tiles;
     if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-    rows_stream_kernel<FP8, NB><<<(unsigned)grid, kSThreads, 0, s>>>(P, n_tiles);
+    rows_stream_kernel<FP8, NB><<<(unsigned)grid, kSThreads, 0, s>>>(P, n_tiles, k_split);
     return cudaGetLastError();
 }
 

@@ -3,7 +3,7 @@
 //
 // A pair of CTAs (cluster of 2, cta_group::2) computes a tile of 256 weight rows of one expert times
 // up to NT of its list positions. The weights are the MMA's A operand (M = 256: 128 rows in each
-// CTA's shared memory) and the rows of x its B operand (N = the tile's rows, rounded up to 32; each
+// CTA's shared memory) and the rows of x its B operand (N = the tile's rows, rounded up to 64; each
 // CTA holds half of them), so an expert with few rows costs few MMA cycles, and any number of rows
 // per expert works without padding in memory. The pair is what feeds the tensor cores: one CTA alone
 // (128 x 256 tiles) needs 48 KB of operands per 64 columns of K from L2 where a CTA of a pair needs 32.
@@ -13,23 +13,23 @@
 // counts), and a persistent grid of pairs walks them.
 //
 // Warp roles of a CTA (both CTAs of a pair but where said):
-//   TMA warp: brings step s (128 bytes of K) of the CTA's weight rows (one box) and, for rows in list
-//     order, of its rows of x (boxes of 64 and 16) into a ring of 128-byte-swizzled stages. Coordinates
-//     past a matrix read zeros, which also pads K. (A box costs about as much as 64 rows however few it
-//     has: boxes of 16 alone ran the ring at half its rate.)
-//   Gather warps (rows read through the list): 16-byte cp.async from the tokens' rows straight into
-//     the swizzled stage, so no permuted copy of x is ever written. (TMA's own gather of four rows a
-//     copy measured 28 ns a copy, 4 times the MMA time of a step.)
-//   MMA warp: in the pair's first CTA, four MMAs a step for both. In the second CTA it tells the first
+//   TMA warp: brings step s (128 bytes of K) of the CTA's weight rows and, for rows in list order, of
+//     its rows of x into a ring of 128-byte-swizzled stages, each operand in one box: there is a tensor
+//     map for every height a tile's share can have. (Issuing a box costs about as much as 64 rows of it:
+//     boxes of 16 rows ran the ring at half its rate.) Coordinates past a matrix read zeros, which also
+//     pads K.
+//   Gather warps: rows read through the list, four tokens' rows a copy (tile::gather4), so no permuted
+//     copy of x is ever written.
+//   Scale warps (8-bit): x_scale * w_scale of every column of four steps, in a ring of their own.
+//   MMA warp: in the pair's first CTA, the MMAs of a step for both. In the second CTA it tells the first
 //     that the step's operands have landed here.
-//     bf16 sums a whole tile in one tensor-memory buffer. 8-bit operands carry a scale per 128 of K,
-//     so each step starts a buffer of its own from zero.
-//   Epilogue warps: bf16: read the finished tile. 8-bit: read every step's buffer, multiply each column
-//     with its scale and add it to the tile's sum in registers (fp32), while the MMAs fill the next
-//     buffer. Lane = weight row, column = row of x, so the stores of a warp are 32 neighbouring
-//     outputs of one row of y.
-//   Scale warps (8-bit): x_scale * w_scale of every column of a step, in a ring of their own.
-// The buffers of tensor memory (512 / NT) let the next tile's or step's MMAs run under the epilogue.
+//   Epilogue warps. bf16: a whole tile is summed in one tensor-memory buffer, then read and written out.
+//     8-bit: the operands carry a scale per 128 of K, so every step starts a buffer from zero; the warps
+//     read it, multiply each column with its scale and add it to the tile's sum in registers (fp32),
+//     while the MMAs fill the next buffer. That reading is what bounds 8-bit tiles, not the MMAs (512
+//     clocks for 256 x 256 x 128): sixteen warps share it, and each half of a tile's columns has buffers
+//     of its own, so that a buffer is busy for 256 clocks of MMA plus one reading.
+// Tensor memory holds 512 / NT buffers of a tile, so the next tile's or step's MMAs run under the epilogue.
 //
 // Every wait is bounded; one that runs out records NVFP4_ERR_DEVICE_TIMEOUT (where the caller passed a
 // workspace) and makes the pair fill its remaining tiles with NaN.
@@ -47,37 +47,48 @@ namespace {
 constexpr int kM = 128;                  // weight rows of a CTA's half of a tile
 constexpr int kStepBytes = 128;          // K bytes of a step: one row of the swizzle atom
 constexpr int kABytes = kM * kStepBytes;
-constexpr int kBigBox = 64, kSmallBox = 16;   // rows of x per box (rows in list order)
-constexpr int kMaxStages = 10;
-constexpr int kScaleSlots = 8;
+constexpr int kMaxStages = 9;
 constexpr int kMaxTiles = 1 << 30;
+constexpr unsigned long long kCopyDrainNs = 10000000ull;
+constexpr int kGroup = 4;                // steps whose scales are handed over together
+constexpr int kNRound = 64;              // a tile's columns are a multiple of this
 
-// Warps: two warpgroups of epilogue, one of TMA, MMA and scales, one of gather.
-constexpr int kEpiWarps = 8, kTmaWarp = 8, kMmaWarp = 9, kScaleWarp0 = 10, kGatherWarp0 = 12;
-constexpr int kScaleThreads = 64, kGatherThreads = 128;
-constexpr int kThreads = 512;
-// Registers of a thread, 8-bit kernel: 128 at launch (65536 / 512), then moved to the epilogue, which
-// keeps 128 sums a thread. 256 * 208 + 256 * 48 = 512 * 128.
-constexpr int kLaunchRegs = 128, kEpiRegs = 208, kOtherRegs = 48;
-static_assert(256 * kEpiRegs + 256 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
+// Warps: 16 of epilogue, TMA, MMA, two of scales, four of gather.
+constexpr int kEpiWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kScaleWarp0 = 18, kGatherWarp0 = 20;
+constexpr int kScaleThreads = 64, kGatherWarps = 4;
+constexpr int kThreads = 768;
+// Registers of a thread, 8-bit kernel: 80 at launch (65536 / 768 in steps of 8), then moved to the
+// epilogue, which keeps 64 sums a thread.
+constexpr int kLaunchRegs = 80, kEpiRegs = 96, kOtherRegs = 48;
+static_assert(512 * kEpiRegs + 256 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
+
+// Output staging of an epilogue warp (bf16): 16 rows of y, 32 neighbouring outputs of each. The pitch of
+// 80 bytes puts the eight 16-byte rows of a stmatrix on different banks.
+constexpr int kStgRows = 16, kStgPitch = 80;
 
 template <bool FP8, int NT>
 struct Cfg {
+    static constexpr int kUnits = FP8 ? 2 : 1;                   // column halves with buffers of their own
+    static constexpr int kUnitCols = NT / kUnits;
+    static constexpr int kBoxes = 4;                             // heights of a box of x: 1 .. 4 times
+    static constexpr int kBoxRows = kNRound / 2 / kUnits;        // ... this
+    static_assert(kBoxes * kBoxRows * 2 * kUnits >= NT, "the highest box holds a CTA's share of a unit");
     static constexpr int kStage = kABytes + NT / 2 * kStepBytes;
-    static constexpr int kStages = std::min(kMaxStages, (200 * 1024) / kStage);
-    static constexpr int kBufs = std::min(8, 512 / NT);          // tensor-memory buffers of NT columns
-    static constexpr int kCols = NT / 2;                         // columns of an epilogue warp
-    static constexpr int kOffScales = kStages * kStage;          // [kScaleSlots][NT] fp32
-    static constexpr int kOffBars = kOffScales + (FP8 ? kScaleSlots * NT * 4 : 0);
-    static constexpr int kNumBars = 4 * kStages + 2 * kBufs + 2 * kScaleSlots + 1;
+    static constexpr int kStages = std::min(kMaxStages, (192 * 1024) / kStage);
+    static constexpr int kBufs = 512 / NT;                       // tensor-memory buffers of a unit
+    static constexpr int kCols = NT / 4;                         // columns of an epilogue warp, at most
+    static constexpr int kOffScales = kStages * kStage;          // [2][kGroup][NT] fp32
+    static constexpr int kOffStg = kOffScales + (FP8 ? 2 * kGroup * NT * 4 : 0);
+    static constexpr int kOffBars = kOffStg + kEpiWarps * kStgRows * kStgPitch;
+    static constexpr int kNumBars = 4 * kStages + 2 * kUnits * kBufs + 4 + 1;
     static constexpr int kOffTab = kOffBars + kNumBars * 8 + 16; // tile prefix [E + 1], first position [E], rows [E]
     static constexpr int kSmem = 1024 + kOffTab + (3 * NVFP4_MAX_EXPERTS + 1) * 4;
-    static_assert(NT % 64 == 0 && NT <= 256 && kStage % 1024 == 0, "two column halves of 32s, swizzle atoms");
+    static_assert(NT % 64 == 0 && NT <= 256 && kStage % 1024 == 0 && kCols % 16 == 0, "swizzle atoms, fragments");
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
 struct TcRowMaps {
-    CUtensorMap w, x_big, x_small;
+    CUtensorMap w, x[4];   // x: boxes of one to four times Cfg::kBoxRows rows; x[0] single rows to gather
 };
 
 // ---------------------------------------------------------------- pair of CTAs
@@ -164,25 +175,24 @@ __device__ __forceinline__ uint32_t e4m3_idesc(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// 32 consecutive fp32 columns of this thread's tensor-memory lane; valid after tmem_wait32.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
-          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
-          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
-          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-        : "r"(taddr));
+// 32 lanes x 16 columns in fragments: v[8 L + 4 j + 2 u + b] is lane 16 L + 8 u + (thread / 4), column
+// 8 j + 2 (thread % 4) + b. Valid after tmem_wait16. A thread needs the scales of a quarter of the columns
+// this way; with a lane to a thread it needs all of them, 1024 clocks of shared-memory reads a step.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[16]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=f"(v[8 * h + 0]), "=f"(v[8 * h + 1]), "=f"(v[8 * h + 2]), "=f"(v[8 * h + 3]),
+                       "=f"(v[8 * h + 4]), "=f"(v[8 * h + 5]), "=f"(v[8 * h + 6]), "=f"(v[8 * h + 7])
+                     : "r"(taddr + ((uint32_t)(16 * h) << 16)));
 }
 // The loads so far are done; the values pass through, so that no use of them moves before the wait.
-__device__ __forceinline__ void tmem_wait32(float (&v)[32]) {
+__device__ __forceinline__ void tmem_wait16(float (&v)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-        : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
-          "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
-          "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
-          "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
-        :: "memory");
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
+                   "+f"(v[15])
+                 :: "memory");
 }
 
 // (a.x, a.y) += (v.x, v.y) * (s.x, s.y), each fused and rounded once: the packed fp32 pipe.
@@ -192,10 +202,20 @@ __device__ __forceinline__ void fma2(float2& a, float vx, float vy, float sx, fl
         : "+f"(a.x), "+f"(a.y) : "f"(vx), "f"(vy), "f"(sx), "f"(sy));
 }
 
+// Four rows of a 2D tensor (a map of single rows), bytes [x, x + 128) of each.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, int r0, int r1, int r2, int r3,
+                                            uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(su32(bar))
+        : "memory");
+}
+
 // ---------------------------------------------------------------- tiles
 struct Tile {
     int e, r0, n, m0;   // expert, first list position, rows, first weight row
-    __device__ __forceinline__ int mma_n() const { return (n + 31) & ~31; }
+    __device__ __forceinline__ int mma_n() const { return (n + kNRound - 1) & ~(kNRound - 1); }
 };
 
 // Tile i of the call, by all lanes of a warp. tab: tile prefix [E + 1], first position [E], rows [E].
@@ -207,14 +227,66 @@ __device__ __forceinline__ Tile tile_of(const int* tab, int E, int m_tiles, int 
         if (tab[mid] <= tt) lo = mid; else hi = mid;
     }
     const int cnt = tab[E + 1 + E + lo], parts = tab[lo + 1] - tab[lo], l = tt - tab[lo];
-    // nearly equal parts in multiples of 32: parts = ceil(cnt / NT), so none is empty
-    const int per = ((cnt + parts - 1) / parts + 31) & ~31;
+    // nearly equal parts in multiples of kNRound: parts = ceil(cnt / NT), so none is empty
+    const int per = ((cnt + parts - 1) / parts + kNRound - 1) & ~(kNRound - 1);
     Tile t;
     t.e = uniform(lo);
     t.r0 = uniform(tab[E + 1 + lo] + l * per);
     t.n = uniform(min(per, cnt - l * per));
     t.m0 = (i - tt * m_tiles) * (2 * kM);
     return t;
+}
+
+// Write 16 columns (rows of y) x 32 lanes (outputs n0 ..) of a tile, held as by tmem_ld_frag. `row`: lane j's
+// (j < 16) row of y for column j, or -1.
+__device__ __forceinline__ void store_frag(const RowsProduct& P, const float (&v)[16], int row, int n0, uint8_t* stg) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, p = lane & 3;
+    if (P.y_f32) {
+        // eight neighbouring outputs of a row are one 32-byte sector
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int r = __shfl_sync(0xffffffffu, row, 8 * j + 2 * p + b);
+                float* y = static_cast<float*>(P.y) + (size_t)max(r, 0) * P.N + n0 + g;
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    if (r >= 0 && n0 + g + 8 * h < P.N) y[8 * h] = v[8 * (h >> 1) + 4 * j + 2 * (h & 1) + b];
+            }
+        return;
+    }
+    // transposed through shared memory: rows of y with 32 neighbouring outputs
+    const uint32_t at = su32(stg) + (lane & 7) * kStgPitch + 16 * (lane >> 3);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const int i = 8 * (h >> 1) + 4 * j + 2 * (h & 1);
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[h]) : "f"(v[i + 1]), "f"(v[i]));
+        }
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                     :: "r"(at + 8 * j * kStgPitch), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    }
+    __syncwarp();
+    if ((P.N & 7) == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int c = 8 * i + g, r = __shfl_sync(0xffffffffu, row, c);
+            const uint4 u = *reinterpret_cast<const uint4*>(stg + c * kStgPitch + 16 * p);
+            if (r >= 0 && n0 + 8 * p < P.N)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.y) + (size_t)r * P.N + n0 + 8 * p) = u;
+        }
+    } else {
+        // rows of y start at any even address
+#pragma unroll 4
+        for (int c = 0; c < 16; ++c) {
+            const int r = __shfl_sync(0xffffffffu, row, c);
+            const uint16_t u = *reinterpret_cast<const uint16_t*>(stg + c * kStgPitch + 2 * lane);
+            if (r >= 0 && n0 + lane < P.N) static_cast<uint16_t*>(P.y)[(size_t)r * P.N + n0 + lane] = u;
+        }
+    }
+    __syncwarp();
 }
 
 template <bool FP8, int NT>
@@ -227,18 +299,18 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
     // pair have the same layout)
     uint8_t* sm = rows_smem_raw + ((1024u - (su32(rows_smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
-    const uint32_t rank = cluster_rank();
+    const int rank = (int)cluster_rank();
 
     float* scale_ring = reinterpret_cast<float*>(sm + C::kOffScales);
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::kOffBars);   // this CTA's TMA copies landed
     uint64_t* gath = full + C::kStages;                                // this CTA's gathered rows landed
     uint64_t* peer = gath + C::kStages;                                // first CTA: the second's operands landed
     uint64_t* empty = peer + C::kStages;                               // MMAs done with the step
-    uint64_t* acc_full = empty + C::kStages;                           // tensor-memory buffer summed
-    uint64_t* acc_empty = acc_full + C::kBufs;                         // first CTA: ... and read in both
-    uint64_t* sc_full = acc_empty + C::kBufs;                          // step's scales written
-    uint64_t* sc_empty = sc_full + kScaleSlots;                        // ... and read
-    uint64_t* done = sc_empty + kScaleSlots;                           // every MMA of the pair
+    uint64_t* acc_full = empty + C::kStages;                           // [unit][buffer] summed
+    uint64_t* acc_empty = acc_full + C::kUnits * C::kBufs;             // first CTA: ... and read in both
+    uint64_t* sc_full = acc_empty + C::kUnits * C::kBufs;              // [2] scales of a group of steps written
+    uint64_t* sc_empty = sc_full + 2;                                  // ... and read
+    uint64_t* done = sc_empty + 2;                                     // every MMA of the pair
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* tab = reinterpret_cast<int*>(sm + C::kOffTab);
@@ -247,15 +319,15 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
         if (lane == 0) {
             for (int i = 0; i < C::kStages; ++i) {
                 mbar_init(&full[i], 1);
-                mbar_init(&gath[i], kGatherThreads);
+                mbar_init(&gath[i], kGatherWarps);
                 mbar_init(&peer[i], 1);
                 mbar_init(&empty[i], 1);
             }
-            for (int i = 0; i < C::kBufs; ++i) {
+            for (int i = 0; i < C::kUnits * C::kBufs; ++i) {
                 mbar_init(&acc_full[i], 1);
-                mbar_init(&acc_empty[i], 2 * kEpiWarps);
+                mbar_init(&acc_empty[i], 2 * kEpiWarps / C::kUnits);
             }
-            for (int i = 0; i < kScaleSlots; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 mbar_init(&sc_full[i], kScaleThreads);
                 mbar_init(&sc_empty[i], kEpiWarps);
             }
@@ -279,8 +351,8 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                 if (P.offsets == nullptr) {
                     n = P.R;
                 } else {
-                    lo = min(max(__ldg(P.offsets + e), 0), P.R);
-                    n = max(min(max(__ldg(P.offsets + e + 1), 0), P.R) - lo, 0);
+                    lo = min(max(P.offsets[e], 0), P.R);
+                    n = max(min(max(P.offsets[e + 1], 0), P.R) - lo, 0);
                 }
                 tab[P.E + 1 + e] = lo;
                 tab[P.E + 1 + P.E + e] = n;
@@ -313,7 +385,7 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
     const int kStepK = FP8 ? 128 : 64;
     const int nk = (P.K + kStepK - 1) / kStepK;
     const int first_tile = blockIdx.x >> 1, tile_step = gridDim.x >> 1;
-    const Waiter wait{abort_flag, map_rank(su32(const_cast<int*>(abort_flag)), rank ^ 1u), hdr, wait_limit};
+    const Waiter wait{abort_flag, map_rank(su32(const_cast<int*>(abort_flag)), (uint32_t)rank ^ 1u), hdr, wait_limit};
 
     if (warp >= kEpiWarps) {
         if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
@@ -323,11 +395,10 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
 #pragma unroll 1
             for (int i = first_tile; i < total && ok; i += tile_step) {
                 const Tile t = tile_of(tab, P.E, m_tiles, i);
-                const int half = t.mma_n() / 2;
-                const int wy = t.e * P.N + t.m0 + (int)rank * kM;
-                const int xy = t.r0 + (int)rank * half;
-                const int big = half / kBigBox, small = (half - big * kBigBox) / kSmallBox;
-                const uint32_t bytes = kABytes + (P.gather ? 0 : half * kStepBytes);
+                const int unit_n = t.mma_n() / C::kUnits, share = unit_n / 2;   // rows of x: of a unit, here
+                const int wy = t.e * P.N + t.m0 + rank * kM;
+                const CUtensorMap* mx = &maps.x[share / C::kBoxRows - 1];
+                const uint32_t bytes = kABytes + (P.gather ? 0 : C::kUnits * share * kStepBytes);
 #pragma unroll 1
                 for (int s = 0; s < nk; ++s, ++step) {
                     const int st = step % C::kStages, u = step / C::kStages;
@@ -338,12 +409,10 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                         mbar_arrive_expect_tx(&full[st], bytes);
                         tma_load_2d(a, &maps.w, s * kStepK, wy, &full[st]);
                         if (!P.gather) {
-                            for (int j = 0; j < big; ++j)
-                                tma_load_2d(b + j * (kBigBox * kStepBytes), &maps.x_big, s * kStepK, xy + j * kBigBox,
-                                            &full[st]);
-                            for (int j = 0; j < small; ++j)
-                                tma_load_2d(b + (big * kBigBox + j * kSmallBox) * kStepBytes, &maps.x_small,
-                                            s * kStepK, xy + big * kBigBox + j * kSmallBox, &full[st]);
+#pragma unroll
+                            for (int h = 0; h < C::kUnits; ++h)
+                                tma_load_2d(b + h * share * kStepBytes, mx, s * kStepK,
+                                            t.r0 + h * unit_n + rank * share, &full[st]);
                         }
                     }
                 }
@@ -357,37 +426,40 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
             bool ok = true;
 #pragma unroll 1
             for (int i = first_tile; i < total && ok; i += tile_step) {
-                const int N = tile_of(tab, P.E, m_tiles, i).mma_n();
-                const uint32_t idesc = FP8 ? e4m3_idesc(2 * kM, N) : f16_idesc(2 * kM, N);
+                const int unit_n = tile_of(tab, P.E, m_tiles, i).mma_n() / C::kUnits;
+                const uint32_t idesc = FP8 ? e4m3_idesc(2 * kM, unit_n) : f16_idesc(2 * kM, unit_n);
 #pragma unroll 1
                 for (int s = 0; s < nk; ++s, ++step) {
                     const int st = step % C::kStages;
                     const uint32_t parity = (step / C::kStages) & 1;
                     ok = wait(&full[st], parity) && (!P.gather || wait(&gath[st], parity));
                     if (!ok) break;
-                    // gathered rows were written by cp.async (generic proxy): order them before the
-                    // tensor cores' reads
-                    if (P.gather) fence_proxy_async_smem();
                     if (rank != 0) {
                         if (elect_one()) arrive_cluster(map_rank(su32(&peer[st]), 0));
                         continue;
                     }
-                    const int buf = buf_use % C::kBufs, v = buf_use / C::kBufs;
-                    const bool first = FP8 || s == 0;
-                    ok = wait(&peer[st], parity) && (!first || v == 0 || wait(&acc_empty[buf], (v - 1) & 1));
+                    ok = wait(&peer[st], parity);
                     if (!ok) break;
-                    tc_fence_after();
+                    const int buf = buf_use % C::kBufs, v = buf_use / C::kBufs;
+                    const bool first = FP8 || s == 0, sum_done = FP8 || s == nk - 1;
                     const uint64_t a = sw128_desc(sm_base + st * C::kStage);
-                    const uint64_t b = sw128_desc(sm_base + st * C::kStage + kABytes);
-                    const uint32_t d = tmem + buf * NT;
-                    const bool sum_done = FP8 || s == nk - 1;
-                    if (elect_one()) {
 #pragma unroll
-                        for (int j = 0; j < kStepBytes / 32; ++j)      // 32 bytes of K an MMA: 2 address units
-                            mma_pair<FP8>(d, a + 2 * j, b + 2 * j, idesc, !first || j != 0);
-                        commit_pair(&empty[st]);
-                        if (sum_done) commit_pair(&acc_full[buf]);
+                    for (int h = 0; h < C::kUnits; ++h) {
+                        const int ub = h * C::kBufs + buf;
+                        if (first && v > 0) ok = wait(&acc_empty[ub], (v - 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t b = sw128_desc(sm_base + st * C::kStage + kABytes + h * (unit_n / 2) * kStepBytes);
+                        const uint32_t d = tmem + ub * C::kUnitCols;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int j = 0; j < kStepBytes / 32; ++j)      // 32 bytes of K an MMA: 2 address units
+                                mma_pair<FP8>(d, a + 2 * j, b + 2 * j, idesc, !first || j != 0);
+                            if (sum_done) commit_pair(&acc_full[ub]);
+                            if (h == C::kUnits - 1) commit_pair(&empty[st]);
+                        }
                     }
+                    if (!ok) break;
                     buf_use += sum_done;
                 }
             }
@@ -400,171 +472,174 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
             }
         } else if (warp >= kGatherWarp0) {
             if (P.gather) {
-                // thread: 16-byte unit `c` of every 16th row of this CTA's half
-                const int th = tid - kGatherWarp0 * 32, c = th & 7, row0 = th >> 3;
-                constexpr int kPer = NT / 2 / 16;
-                const size_t row_bytes = (size_t)P.K * (FP8 ? 1 : 2);
-                const uint8_t* x = static_cast<const uint8_t*>(P.x) + c * 16;
+                // copies of four rows, in turn over the warps: at most kPer a warp and step; lane 4 j + r has
+                // row r of this warp's copy j
+                constexpr int kPer = NT / 2 / 4 / kGatherWarps;
+                const int w = warp - kGatherWarp0;
                 int step = 0;
                 bool ok = true;
 #pragma unroll 1
                 for (int i = first_tile; i < total && ok; i += tile_step) {
                     const Tile t = tile_of(tab, P.E, m_tiles, i);
-                    const int half = t.mma_n() / 2;
-                    int src[kPer];
-#pragma unroll
-                    for (int j = 0; j < kPer; ++j) {
-                        const int r = (int)rank * half + row0 + 16 * j;
-                        src[j] = row0 + 16 * j < half && r < t.n ? x_row(P, t.r0 + r) : -1;
-                    }
+                    const int unit_n = t.mma_n() / C::kUnits, share = unit_n / 2;
+                    const int copies = C::kUnits * share / 4;
+                    const int l = 4 * (w + kGatherWarps * (lane >> 2)) + (lane & 3);
+                    const int h = C::kUnits == 2 && l >= share;
+                    const int col = h * unit_n + rank * share + l - h * share;
+                    int src = l < C::kUnits * share && col < t.n ? x_row(P, t.r0 + col) : -1;
+                    if (src < 0) src = P.x_rows;                     // past the last row: zeros
+                    const int mine = (copies - w + kGatherWarps - 1) / kGatherWarps;
 #pragma unroll 1
                     for (int s = 0; s < nk; ++s, ++step) {
                         const int st = step % C::kStages, u = step / C::kStages;
                         if (u > 0) ok = wait(&empty[st], (u - 1) & 1);
                         if (!ok) break;
-                        const uint32_t b = sm_base + st * C::kStage + kABytes;
-                        const size_t off = (size_t)s * kStepBytes;
-                        const bool in_k = off + c * 16 < row_bytes;
+                        const uint32_t b = sm_base + st * C::kStage + kABytes + w * 4 * kStepBytes;
+                        if (elect_one()) mbar_arrive_expect_tx(&gath[st], mine * 4 * kStepBytes);
 #pragma unroll
                         for (int j = 0; j < kPer; ++j) {
-                            const int row = row0 + 16 * j;
-                            if (row < half) {
-                                const bool in = in_k && src[j] >= 0;
-                                cp_async16_zfill(b + row * kStepBytes + ((c ^ (row & 7)) << 4),
-                                                 in ? x + src[j] * row_bytes + off : static_cast<const uint8_t*>(P.x),
-                                                 in ? 16u : 0u);
-                            }
+                            if (j >= mine) break;
+                            const int r0 = __shfl_sync(0xffffffffu, src, 4 * j);
+                            const int r1 = __shfl_sync(0xffffffffu, src, 4 * j + 1);
+                            const int r2 = __shfl_sync(0xffffffffu, src, 4 * j + 2);
+                            const int r3 = __shfl_sync(0xffffffffu, src, 4 * j + 3);
+                            if (elect_one())
+                                tma_gather4(b + j * (kGatherWarps * 4 * kStepBytes), &maps.x[0], s * kStepK, r0, r1, r2,
+                                            r3, &gath[st]);
                         }
-                        cp_async_arrive_noinc(&gath[st]);
                     }
                 }
-                asm volatile("cp.async.wait_all;" ::: "memory");
+                // this warp's copies have landed before the CTA may exit. (After an abort the other warps
+                // may not have issued theirs, so that the phase stays open: 10 ms is a thousand copies.)
+                if (lane == 0)
+                    for (int s = max(0, step - C::kStages); s < step; ++s)
+                        mbar_wait_bounded(&gath[s % C::kStages], (s / C::kStages) & 1, kCopyDrainNs);
             }
-        } else if (warp >= kScaleWarp0) {
-            if constexpr (FP8) {
-                const int th = tid - kScaleWarp0 * 32;
-                const int KB = nk, NB = (P.N + 127) >> 7;
-                constexpr int kPer = NT / kScaleThreads;
-                int step = 0;
-                bool ok = true;
+        } else if constexpr (FP8) {
+            const int th = tid - kScaleWarp0 * 32;           // columns th, th + 64, ...
+            constexpr int kPer = NT / kScaleThreads;
+            const int KB = nk, NB = (P.N + 127) >> 7;
+            int grp = 0;
+            bool ok = true;
 #pragma unroll 1
-                for (int i = first_tile; i < total && ok; i += tile_step) {
-                    const Tile t = tile_of(tab, P.E, m_tiles, i);
-                    const int nb = (t.m0 >> 7) + (int)rank;
-                    const bool any = nb < NB;           // else the half tile lies past the matrix
-                    const float* xs[kPer];
+            for (int i = first_tile; i < total && ok; i += tile_step) {
+                const Tile t = tile_of(tab, P.E, m_tiles, i);
+                const int nb = (t.m0 >> 7) + rank;           // past the matrix: scales 0
+                const float* wsc = nb < NB ? P.ws + ((size_t)t.e * NB + nb) * KB : P.ws;
+                int xs[kPer];
+                float next[kGroup][kPer];
+                auto load = [&](int s0) {
 #pragma unroll
-                    for (int j = 0; j < kPer; ++j) {
-                        const int c = th + kScaleThreads * j;
-                        const int row = any && c < t.n ? x_row(P, t.r0 + c) : -1;
-                        xs[j] = row < 0 ? nullptr : P.xs + (size_t)row * KB;
-                    }
-                    const float* wsc = any ? P.ws + ((size_t)t.e * NB + nb) * KB : P.ws;
-                    float next[kPer], wnext = __ldg(wsc);
+                    for (int d = 0; d < kGroup; ++d)
 #pragma unroll
-                    for (int j = 0; j < kPer; ++j) next[j] = xs[j] != nullptr ? __ldg(xs[j]) : 0.f;
+                        for (int j = 0; j < kPer; ++j)
+                            next[d][j] = xs[j] >= 0 && s0 + d < nk ? P.xs[(size_t)xs[j] * KB + s0 + d] : 0.f;
+                };
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    const int col = th + kScaleThreads * j;
+                    xs[j] = nb < NB && col < t.n ? x_row(P, t.r0 + col) : -1;
+                }
+                load(0);
 #pragma unroll 1
-                    for (int s = 0; s < nk; ++s, ++step) {
-                        const int slot = step % kScaleSlots, u = step / kScaleSlots;
-                        float now[kPer];
+                for (int s = 0; s < nk; s += kGroup, ++grp) {
+                    const int slot = grp & 1, u = grp >> 1;
+                    if (u > 0) ok = wait(&sc_empty[slot], (u - 1) & 1);
+                    if (!ok) break;
 #pragma unroll
-                        for (int j = 0; j < kPer; ++j) now[j] = xs[j] != nullptr ? next[j] * wnext : 0.f;
-                        if (s + 1 < nk) {
-                            wnext = __ldg(wsc + s + 1);
+                    for (int d = 0; d < kGroup; ++d) {
+                        const float sw = s + d < nk ? wsc[s + d] : 0.f;
 #pragma unroll
-                            for (int j = 0; j < kPer; ++j)
-                                if (xs[j] != nullptr) next[j] = __ldg(xs[j] + s + 1);
-                        }
-                        if (u > 0 && !wait(&sc_empty[slot], (u - 1) & 1)) {
-                            ok = false;
-                            break;
-                        }
-#pragma unroll
-                        for (int j = 0; j < kPer; ++j) scale_ring[slot * NT + th + kScaleThreads * j] = now[j];
-                        mbar_arrive(&sc_full[slot]);
+                        for (int j = 0; j < kPer; ++j)
+                            scale_ring[(slot * kGroup + d) * NT + th + kScaleThreads * j] =
+                                xs[j] >= 0 ? next[d][j] * sw : 0.f;
                     }
+                    mbar_arrive(&sc_full[slot]);
+                    if (s + kGroup < nk) load(s + kGroup);
                 }
             }
         }
     } else {
         if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kEpiRegs));
-        const int q = warp & 3, c0 = (warp >> 2) * C::kCols;
-        const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + c0;
-        int use = 0;          // tensor-memory buffers (8-bit: steps) read so far
+        const int q = warp & 3, part = warp >> 2;          // lanes 32 q .., a quarter of the columns
+        const int unit = FP8 ? part >> 1 : 0;
+        uint8_t* stg = sm + C::kOffStg + warp * (kStgRows * kStgPitch);
+        const int p = lane & 3;
+        int use = 0, grp = 0;      // buffers (8-bit: steps) and groups of scales read so far
         bool ok = true;
 #pragma unroll 1
         for (int i = first_tile; i < total; i += tile_step) {
             const Tile t = tile_of(tab, P.E, m_tiles, i);
-            const int n = t.m0 + (int)rank * kM + 32 * q + lane;      // output column of y
-            // write 32 columns of the tile
-            auto store32 = [&](int c, const float* v) {
-                const int row = c + lane < t.n ? y_row(P, t.r0 + c + lane) : -1;
-                const bool bad = *abort_flag != 0;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int rj = __shfl_sync(0xffffffffu, row, j);
-                    if (rj < 0 || n >= P.N) continue;
-                    const float out = bad ? __uint_as_float(0x7FC00000u) : v[j];
-                    const size_t at = (size_t)rj * P.N + n;
-                    if (P.y_f32) static_cast<float*>(P.y)[at] = out;
-                    else static_cast<uint16_t*>(P.y)[at] = f32_to_bf16(out);
-                }
-            };
+            const int width = t.mma_n() / 4, c0 = part * width;            // this warp's columns of the tile
+            const int uc0 = c0 - unit * (t.mma_n() / C::kUnits);           // ... and of its unit
+            const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + unit * C::kBufs * C::kUnitCols + uc0;
+            const int n0 = t.m0 + rank * kM + 32 * q;                      // first output
+            auto out_row = [&](int c) { return (lane & 15) + c < t.n ? y_row(P, t.r0 + c + (lane & 15)) : -1; };
             if constexpr (FP8) {
                 float2 acc[C::kCols / 2];
 #pragma unroll
                 for (int j = 0; j < C::kCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
 #pragma unroll 1
                 for (int s = 0; s < nk && ok; ++s, ++use) {
-                    const int buf = use % C::kBufs, slot = use % kScaleSlots;
-                    ok = wait(&sc_full[slot], (use / kScaleSlots) & 1) && wait(&acc_full[buf], (use / C::kBufs) & 1);
+                    const int buf = use % C::kBufs, slot = grp & 1;
+                    if (s % kGroup == 0) ok = wait(&sc_full[slot], (grp >> 1) & 1);
+                    if (ok) ok = wait(&acc_full[unit * C::kBufs + buf], (use / C::kBufs) & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    const float* sc = scale_ring + slot * NT + c0;
-                    float v[2][32];
-                    if (c0 < t.n) tmem_ld32(lane_base + buf * NT, v[0]);
+                    const float* sc = scale_ring + (slot * kGroup + s % kGroup) * NT + c0 + 2 * p;
 #pragma unroll
-                    for (int c = 0; c < C::kCols; c += 32) {
-                        if (c0 + c >= t.n) break;
-                        float (&now)[32] = v[(c / 32) & 1];
-                        tmem_wait32(now);
-                        if (c + 32 < C::kCols && c0 + c + 32 < t.n)
-                            tmem_ld32(lane_base + buf * NT + c + 32, v[(c / 32 + 1) & 1]);
+                    for (int c = 0; c < C::kCols; c += 16) {
+                        if (c >= width) break;
+                        float v[16];
+                        tmem_ld_frag(lanes + buf * C::kUnitCols + c, v);
+                        tmem_wait16(v);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float4 f = *reinterpret_cast<const float4*>(sc + c + j);
-                            fma2(acc[(c + j) / 2], now[j], now[j + 1], f.x, f.y);
-                            fma2(acc[(c + j) / 2 + 1], now[j + 2], now[j + 3], f.z, f.w);
+                        for (int j = 0; j < 2; ++j) {
+                            const float2 f = *reinterpret_cast<const float2*>(sc + c + 8 * j);
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) {
+                                const int k = 8 * (h >> 1) + 4 * j + 2 * (h & 1);
+                                fma2(acc[(c + k) / 2], v[k], v[k + 1], f.x, f.y);
+                            }
                         }
                     }
                     tc_fence_before();
                     __syncwarp();
+                    const bool last = s % kGroup == kGroup - 1 || s == nk - 1;
                     if (lane == 0) {
-                        arrive_cluster(map_rank(su32(&acc_empty[buf]), 0));
-                        mbar_arrive(&sc_empty[slot]);
+                        arrive_cluster(map_rank(su32(&acc_empty[unit * C::kBufs + buf]), 0));
+                        if (last) mbar_arrive(&sc_empty[slot]);
                     }
+                    grp += last;
                 }
+                const bool bad = *abort_flag != 0;
 #pragma unroll
-                for (int c = 0; c < C::kCols; c += 32) {
-                    if (c0 + c >= t.n) break;
-                    float v[32];
+                for (int c = 0; c < C::kCols; c += 16) {
+                    if (c >= width || c0 + c >= t.n) break;
+                    float v[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[2 * j] = acc[c / 2 + j].x, v[2 * j + 1] = acc[c / 2 + j].y;
-                    store32(c0 + c, v);
+                    for (int j = 0; j < 8; ++j) {
+                        v[2 * j] = bad ? __uint_as_float(0x7FC00000u) : acc[c / 2 + j].x;
+                        v[2 * j + 1] = bad ? __uint_as_float(0x7FC00000u) : acc[c / 2 + j].y;
+                    }
+                    store_frag(P, v, out_row(c0 + c), n0, stg);
                 }
             } else {
                 const int buf = use % C::kBufs;
                 if (ok) ok = wait(&acc_full[buf], (use / C::kBufs) & 1);
                 tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < C::kCols; c += 32) {
+                for (int c = 0; c < width; c += 16) {
                     if (c0 + c >= t.n) break;
-                    float v[32] = {};
+                    float v[16];
                     if (ok) {
-                        tmem_ld32(lane_base + buf * NT + c, v);
-                        tmem_wait32(v);
+                        tmem_ld_frag(lanes + buf * C::kUnitCols + c, v);
+                        tmem_wait16(v);
                     }
-                    store32(c0 + c, v);
+                    if (*abort_flag)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(0x7FC00000u);
+                    store_frag(P, v, out_row(c0 + c), n0, stg);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -613,10 +688,10 @@ cudaError_t launch_tc(const RowsProduct& P, WsHeader* hdr, const DeviceInfo& dev
     }
     PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
     TcRowMaps maps;
-    if (fn == nullptr || !encode_rows(fn, &maps.w, P.w, FP8, P.K, (uint64_t)P.E * P.N, kM) ||
-        !encode_rows(fn, &maps.x_big, P.x, FP8, P.K, P.x_rows, kBigBox) ||
-        !encode_rows(fn, &maps.x_small, P.x, FP8, P.K, P.x_rows, kSmallBox))
-        return cudaErrorInvalidValue;
+    if (fn == nullptr || !encode_rows(fn, &maps.w, P.w, FP8, P.K, (uint64_t)P.E * P.N, kM)) return cudaErrorInvalidValue;
+    for (int i = 0; i < (P.gather ? 1 : C::kBoxes); ++i)
+        if (!encode_rows(fn, &maps.x[i], P.x, FP8, P.K, P.x_rows, P.gather ? 1 : (i + 1) * C::kBoxRows))
+            return cudaErrorInvalidValue;
     const int m_tiles = (P.N + 2 * kM - 1) / (2 * kM);
     // tiles at most: every expert's last one is not full
     const long long tiles = (P.R / NT + std::min(P.R, P.E)) * (long long)m_tiles;
