@@ -202,7 +202,11 @@ __device__ __forceinline__ int y_row(const RowsProduct& P, int r) {
     return (unsigned)entry < (unsigned)P.R ? entry : -1;
 }
 
-// Few rows: weights streamed through warp-level MMAs. Many rows: tcgen05 tiles.
+// Up to kStreamRows rows in all: weights streamed through warp-level MMAs; more: tcgen05 tiles. Measured on
+// a GB300 (us a call, stream / tiles): one matrix 2048 x 8192 in 8 bits at 8 rows 12.6 / 23.1, at 16 12.9 /
+// 23.2, at 32 21.0 / 23.2; 8192 x 2048 at 16 rows 11.2 / 11.3, at 32 19.3 / 11.3; 256 experts of 1024 x 2048
+// at 8 rows 11.3 / 12.9, at 32 22.3 / 19.4.
+constexpr int kStreamRows = 16;
 cudaError_t launch_rows_stream(const RowsProduct& P, cudaStream_t s);
 cudaError_t launch_rows_tc(const RowsProduct& P, WsHeader* hdr, const DeviceInfo& dev, uint64_t wait_limit,
                            cudaStream_t s);

@@ -83,7 +83,7 @@ __device__ __forceinline__ bool locate_pass(const RowsProduct& P, int p, int* e,
 }
 
 template <bool FP8, int NB>
-__global__ void __launch_bounds__(kSThreads, NB == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kSThreads, 2)
 rows_stream_kernel(const RowsProduct P, int n_tiles, int k_split) {
     constexpr int kRows = 8 * NB;
     __shared__ float s_acc[kSWarps][16][kRows + 1];
@@ -222,7 +222,8 @@ cudaError_t launch_stream(const RowsProduct& P, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_rows_stream(const RowsProduct& P, cudaStream_t s) {
-    return P.xs != nullptr ? launch_stream<true, 1>(P, s) : launch_stream<false, 1>(P, s);
+    if (P.R <= 8) return P.xs != nullptr ? launch_stream<true, 1>(P, s) : launch_stream<false, 1>(P, s);
+    return P.xs != nullptr ? launch_stream<true, 2>(P, s) : launch_stream<false, 2>(P, s);
 }
 
 }  // namespace nvfp4

@@ -68,19 +68,17 @@ constexpr int kStgRows = 16, kStgPitch = 80;
 
 template <bool FP8, int NT>
 struct Cfg {
-    static constexpr int kUnits = FP8 ? 2 : 1;                   // column halves with buffers of their own
-    static constexpr int kUnitCols = NT / kUnits;
     static constexpr int kBoxes = 4;                             // heights of a box of x: 1 .. 4 times
-    static constexpr int kBoxRows = kNRound / 2 / kUnits;        // ... this
-    static_assert(kBoxes * kBoxRows * 2 * kUnits >= NT, "the highest box holds a CTA's share of a unit");
+    static constexpr int kBoxRows = kNRound / 2;                 // ... this
+    static_assert(kBoxes * kBoxRows * 2 >= NT, "the highest box holds a CTA's share of a tile");
     static constexpr int kStage = kABytes + NT / 2 * kStepBytes;
     static constexpr int kStages = std::min(kMaxStages, (192 * 1024) / kStage);
-    static constexpr int kBufs = 512 / NT;                       // tensor-memory buffers of a unit
+    static constexpr int kBufs = 512 / NT;                       // tensor-memory buffers of NT columns
     static constexpr int kCols = NT / 4;                         // columns of an epilogue warp, at most
     static constexpr int kOffScales = kStages * kStage;          // [2][kGroup][NT] fp32
     static constexpr int kOffStg = kOffScales + (FP8 ? 2 * kGroup * NT * 4 : 0);
     static constexpr int kOffBars = kOffStg + kEpiWarps * kStgRows * kStgPitch;
-    static constexpr int kNumBars = 4 * kStages + 2 * kUnits * kBufs + 4 + 1;
+    static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 4 + 1;
     static constexpr int kOffTab = kOffBars + kNumBars * 8 + 16; // tile prefix [E + 1], first position [E], rows [E]
     static constexpr int kSmem = 1024 + kOffTab + (3 * NVFP4_MAX_EXPERTS + 1) * 4;
     static_assert(NT % 64 == 0 && NT <= 256 && kStage % 1024 == 0 && kCols % 16 == 0, "swizzle atoms, fragments");
@@ -218,24 +216,38 @@ struct Tile {
     __device__ __forceinline__ int mma_n() const { return (n + kNRound - 1) & ~(kNRound - 1); }
 };
 
-// Tile i of the call, by all lanes of a warp. tab: tile prefix [E + 1], first position [E], rows [E].
-__device__ __forceinline__ Tile tile_of(const int* tab, int E, int m_tiles, int i) {
-    const int tt = i / m_tiles;
-    int lo = 0, hi = E;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (tab[mid] <= tt) lo = mid; else hi = mid;
+// The tiles of a pair: token tile tt (numbered over the experts) and weight tile mt of i = first, first +
+// step, ... below total. tab: token-tile prefix [E + 1], first position [E], rows [E].
+struct Walk {
+    const int* tab;
+    int E, m_tiles, i, step, total, tt, mt, dt, dm;
+
+    __device__ __forceinline__ Walk(const int* tab_, int E_, int m_tiles_, int first, int step_, int total_)
+        : tab(tab_), E(E_), m_tiles(m_tiles_), i(first), step(step_), total(total_), tt(first / m_tiles_),
+          mt(first - tt * m_tiles_), dt(step_ / m_tiles_), dm(step_ - dt * m_tiles_) {}
+    __device__ __forceinline__ bool more() const { return i < total; }
+    __device__ __forceinline__ void next() {
+        i += step, tt += dt, mt += dm;
+        if (mt >= m_tiles) mt -= m_tiles, ++tt;
     }
-    const int cnt = tab[E + 1 + E + lo], parts = tab[lo + 1] - tab[lo], l = tt - tab[lo];
-    // nearly equal parts in multiples of kNRound: parts = ceil(cnt / NT), so none is empty
-    const int per = ((cnt + parts - 1) / parts + kNRound - 1) & ~(kNRound - 1);
-    Tile t;
-    t.e = uniform(lo);
-    t.r0 = uniform(tab[E + 1 + lo] + l * per);
-    t.n = uniform(min(per, cnt - l * per));
-    t.m0 = (i - tt * m_tiles) * (2 * kM);
-    return t;
-}
+    // By all lanes of a warp: the last expert whose first token tile is at most tt (an empty one before it
+    // has the same first), found among every eighth and then among eight.
+    __device__ __forceinline__ Tile tile() const {
+        const int lane = threadIdx.x & 31;
+        const int b = __popc(__ballot_sync(0xffffffffu, 8 * lane < E && tab[min(8 * lane, E)] <= tt)) - 1;
+        const int e8 = 8 * b + (lane & 7);
+        const int e = 8 * b + __popc(__ballot_sync(0xffffffffu, lane < 8 && e8 < E && tab[min(e8, E)] <= tt)) - 1;
+        const int cnt = tab[E + 1 + E + e], parts = tab[e + 1] - tab[e], l = tt - tab[e];
+        // nearly equal parts in multiples of kNRound: parts = ceil(cnt / NT), so none is empty
+        const int per = parts == 1 ? cnt : ((cnt + parts - 1) / parts + kNRound - 1) & ~(kNRound - 1);
+        Tile t;
+        t.e = uniform(e);
+        t.r0 = uniform(tab[E + 1 + e] + l * per);
+        t.n = uniform(min(per, cnt - l * per));
+        t.m0 = mt * (2 * kM);
+        return t;
+    }
+};
 
 // Write 16 columns (rows of y) x 32 lanes (outputs n0 ..) of a tile, held as by tmem_ld_frag. `row`: lane j's
 // (j < 16) row of y for column j, or -1.
@@ -302,13 +314,11 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
     const int rank = (int)cluster_rank();
 
     float* scale_ring = reinterpret_cast<float*>(sm + C::kOffScales);
-    uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::kOffBars);   // this CTA's TMA copies landed
-    uint64_t* gath = full + C::kStages;                                // this CTA's gathered rows landed
-    uint64_t* peer = gath + C::kStages;                                // first CTA: the second's operands landed
-    uint64_t* empty = peer + C::kStages;                               // MMAs done with the step
-    uint64_t* acc_full = empty + C::kStages;                           // [unit][buffer] summed
-    uint64_t* acc_empty = acc_full + C::kUnits * C::kBufs;             // first CTA: ... and read in both
-    uint64_t* sc_full = acc_empty + C::kUnits * C::kBufs;              // [2] scales of a group of steps written
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::kOffBars);   // step landed (first CTA: in both)
+    uint64_t* empty = full + C::kStages;                               // MMAs done with the step
+    uint64_t* acc_full = empty + C::kStages;                           // tensor-memory buffer summed
+    uint64_t* acc_empty = acc_full + C::kBufs;                         // first CTA: ... and read in both
+    uint64_t* sc_full = acc_empty + C::kBufs;                          // [2] scales of a group of steps written
     uint64_t* sc_empty = sc_full + 2;                                  // ... and read
     uint64_t* done = sc_empty + 2;                                     // every MMA of the pair
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -318,14 +328,13 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
     if (warp == kMmaWarp) {
         if (lane == 0) {
             for (int i = 0; i < C::kStages; ++i) {
-                mbar_init(&full[i], 1);
-                mbar_init(&gath[i], kGatherWarps);
-                mbar_init(&peer[i], 1);
+                // the TMA warp, each gather warp, and in the first CTA the second's word
+                mbar_init(&full[i], 1 + (P.gather ? kGatherWarps : 0) + (rank == 0 ? 1 : 0));
                 mbar_init(&empty[i], 1);
             }
-            for (int i = 0; i < C::kUnits * C::kBufs; ++i) {
+            for (int i = 0; i < C::kBufs; ++i) {
                 mbar_init(&acc_full[i], 1);
-                mbar_init(&acc_empty[i], 2 * kEpiWarps / C::kUnits);
+                mbar_init(&acc_empty[i], 2 * kEpiWarps);
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&sc_full[i], kScaleThreads);
@@ -384,8 +393,16 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
     const int total = uniform((int)min((long long)tab[P.E] * m_tiles, (long long)kMaxTiles));
     const int kStepK = FP8 ? 128 : 64;
     const int nk = (P.K + kStepK - 1) / kStepK;
-    const int first_tile = blockIdx.x >> 1, tile_step = gridDim.x >> 1;
+    const Walk tiles(tab, P.E, m_tiles, blockIdx.x >> 1, gridDim.x >> 1, total);
     const Waiter wait{abort_flag, map_rank(su32(const_cast<int*>(abort_flag)), (uint32_t)rank ^ 1u), hdr, wait_limit};
+
+    // A warp that issued copies for `step` steps waits until the last fill of each stage has landed before
+    // the CTA may exit. (After an abort other warps may not have issued theirs, so that the phase stays
+    // open: 10 ms is a thousand copies.)
+    auto drain = [&](int step) {
+        for (int s = max(0, step - C::kStages); s < step; ++s)
+            mbar_wait_bounded(&full[s % C::kStages], (s / C::kStages) & 1, kCopyDrainNs);
+    };
 
     if (warp >= kEpiWarps) {
         if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
@@ -393,12 +410,12 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
             int step = 0;
             bool ok = true;
 #pragma unroll 1
-            for (int i = first_tile; i < total && ok; i += tile_step) {
-                const Tile t = tile_of(tab, P.E, m_tiles, i);
-                const int unit_n = t.mma_n() / C::kUnits, share = unit_n / 2;   // rows of x: of a unit, here
+            for (Walk at = tiles; at.more() && ok; at.next()) {
+                const Tile t = at.tile();
+                const int share = t.mma_n() / 2;                                // rows of x here
                 const int wy = t.e * P.N + t.m0 + rank * kM;
                 const CUtensorMap* mx = &maps.x[share / C::kBoxRows - 1];
-                const uint32_t bytes = kABytes + (P.gather ? 0 : C::kUnits * share * kStepBytes);
+                const uint32_t bytes = kABytes + (P.gather ? 0 : share * kStepBytes);
 #pragma unroll 1
                 for (int s = 0; s < nk; ++s, ++step) {
                     const int st = step % C::kStages, u = step / C::kStages;
@@ -408,59 +425,42 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                     if (elect_one()) {
                         mbar_arrive_expect_tx(&full[st], bytes);
                         tma_load_2d(a, &maps.w, s * kStepK, wy, &full[st]);
-                        if (!P.gather) {
-#pragma unroll
-                            for (int h = 0; h < C::kUnits; ++h)
-                                tma_load_2d(b + h * share * kStepBytes, mx, s * kStepK,
-                                            t.r0 + h * unit_n + rank * share, &full[st]);
-                        }
+                        if (!P.gather) tma_load_2d(b, mx, s * kStepK, t.r0 + rank * share, &full[st]);
                     }
                 }
             }
-            // every copy has landed before the CTA may exit (the last fill of each stage)
-            if (lane == 0)
-                for (int s = max(0, step - C::kStages); s < step; ++s)
-                    drain_wait(&full[s % C::kStages], (s / C::kStages) & 1);
+            if (lane == 0) drain(step);
         } else if (warp == kMmaWarp) {
-            int step = 0, buf_use = 0;
+            int st = 0, buf = 0;
+            uint32_t st_par = 0, buf_par = 1;          // an unused buffer's "empty" phase counts as over
             bool ok = true;
+            const uint64_t stage0 = sw128_desc(sm_base);
 #pragma unroll 1
-            for (int i = first_tile; i < total && ok; i += tile_step) {
-                const int unit_n = tile_of(tab, P.E, m_tiles, i).mma_n() / C::kUnits;
-                const uint32_t idesc = FP8 ? e4m3_idesc(2 * kM, unit_n) : f16_idesc(2 * kM, unit_n);
+            for (Walk at = tiles; at.more() && ok; at.next()) {
+                const int N = at.tile().mma_n();
+                const uint32_t idesc = FP8 ? e4m3_idesc(2 * kM, N) : f16_idesc(2 * kM, N);
 #pragma unroll 1
-                for (int s = 0; s < nk; ++s, ++step) {
-                    const int st = step % C::kStages;
-                    const uint32_t parity = (step / C::kStages) & 1;
-                    ok = wait(&full[st], parity) && (!P.gather || wait(&gath[st], parity));
+                for (int s = 0; s < nk; ++s) {
+                    const bool first = FP8 || s == 0, sum_done = FP8 || s == nk - 1;
+                    ok = wait(&full[st], st_par);
                     if (!ok) break;
                     if (rank != 0) {
-                        if (elect_one()) arrive_cluster(map_rank(su32(&peer[st]), 0));
-                        continue;
-                    }
-                    ok = wait(&peer[st], parity);
-                    if (!ok) break;
-                    const int buf = buf_use % C::kBufs, v = buf_use / C::kBufs;
-                    const bool first = FP8 || s == 0, sum_done = FP8 || s == nk - 1;
-                    const uint64_t a = sw128_desc(sm_base + st * C::kStage);
-#pragma unroll
-                    for (int h = 0; h < C::kUnits; ++h) {
-                        const int ub = h * C::kBufs + buf;
-                        if (first && v > 0) ok = wait(&acc_empty[ub], (v - 1) & 1);
+                        if (elect_one()) arrive_cluster(map_rank(su32(&full[st]), 0));
+                    } else {
+                        if (first) ok = wait(&acc_empty[buf], buf_par);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint64_t b = sw128_desc(sm_base + st * C::kStage + kABytes + h * (unit_n / 2) * kStepBytes);
-                        const uint32_t d = tmem + ub * C::kUnitCols;
+                        const uint64_t a = stage0 + st * (C::kStage / 16), b = a + kABytes / 16;
                         if (elect_one()) {
 #pragma unroll
                             for (int j = 0; j < kStepBytes / 32; ++j)      // 32 bytes of K an MMA: 2 address units
-                                mma_pair<FP8>(d, a + 2 * j, b + 2 * j, idesc, !first || j != 0);
-                            if (sum_done) commit_pair(&acc_full[ub]);
-                            if (h == C::kUnits - 1) commit_pair(&empty[st]);
+                                mma_pair<FP8>(tmem + buf * NT, a + 2 * j, b + 2 * j, idesc, !first || j != 0);
+                            commit_pair(&empty[st]);
+                            if (sum_done) commit_pair(&acc_full[buf]);
                         }
+                        if (sum_done && ++buf == C::kBufs) buf = 0, buf_par ^= 1;
                     }
-                    if (!ok) break;
-                    buf_use += sum_done;
+                    if (++st == C::kStages) st = 0, st_par ^= 1;
                 }
             }
             if (rank == 0) {
@@ -479,14 +479,12 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                 int step = 0;
                 bool ok = true;
 #pragma unroll 1
-                for (int i = first_tile; i < total && ok; i += tile_step) {
-                    const Tile t = tile_of(tab, P.E, m_tiles, i);
-                    const int unit_n = t.mma_n() / C::kUnits, share = unit_n / 2;
-                    const int copies = C::kUnits * share / 4;
+                for (Walk at = tiles; at.more() && ok; at.next()) {
+                    const Tile t = at.tile();
+                    const int share = t.mma_n() / 2, copies = share / 4;
                     const int l = 4 * (w + kGatherWarps * (lane >> 2)) + (lane & 3);
-                    const int h = C::kUnits == 2 && l >= share;
-                    const int col = h * unit_n + rank * share + l - h * share;
-                    int src = l < C::kUnits * share && col < t.n ? x_row(P, t.r0 + col) : -1;
+                    const int col = rank * share + l;
+                    int src = l < share && col < t.n ? x_row(P, t.r0 + col) : -1;
                     if (src < 0) src = P.x_rows;                     // past the last row: zeros
                     const int mine = (copies - w + kGatherWarps - 1) / kGatherWarps;
 #pragma unroll 1
@@ -495,7 +493,7 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                         if (u > 0) ok = wait(&empty[st], (u - 1) & 1);
                         if (!ok) break;
                         const uint32_t b = sm_base + st * C::kStage + kABytes + w * 4 * kStepBytes;
-                        if (elect_one()) mbar_arrive_expect_tx(&gath[st], mine * 4 * kStepBytes);
+                        if (elect_one()) mbar_arrive_expect_tx(&full[st], mine * 4 * kStepBytes);
 #pragma unroll
                         for (int j = 0; j < kPer; ++j) {
                             if (j >= mine) break;
@@ -505,15 +503,11 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                             const int r3 = __shfl_sync(0xffffffffu, src, 4 * j + 3);
                             if (elect_one())
                                 tma_gather4(b + j * (kGatherWarps * 4 * kStepBytes), &maps.x[0], s * kStepK, r0, r1, r2,
-                                            r3, &gath[st]);
+                                            r3, &full[st]);
                         }
                     }
                 }
-                // this warp's copies have landed before the CTA may exit. (After an abort the other warps
-                // may not have issued theirs, so that the phase stays open: 10 ms is a thousand copies.)
-                if (lane == 0)
-                    for (int s = max(0, step - C::kStages); s < step; ++s)
-                        mbar_wait_bounded(&gath[s % C::kStages], (s / C::kStages) & 1, kCopyDrainNs);
+                if (lane == 0) drain(step);
             }
         } else if constexpr (FP8) {
             const int th = tid - kScaleWarp0 * 32;           // columns th, th + 64, ...
@@ -522,8 +516,8 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
             int grp = 0;
             bool ok = true;
 #pragma unroll 1
-            for (int i = first_tile; i < total && ok; i += tile_step) {
-                const Tile t = tile_of(tab, P.E, m_tiles, i);
+            for (Walk at = tiles; at.more() && ok; at.next()) {
+                const Tile t = at.tile();
                 const int nb = (t.m0 >> 7) + rank;           // past the matrix: scales 0
                 const float* wsc = nb < NB ? P.ws + ((size_t)t.e * NB + nb) * KB : P.ws;
                 int xs[kPer];
@@ -562,19 +556,22 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
     } else {
         if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kEpiRegs));
         const int q = warp & 3, part = warp >> 2;          // lanes 32 q .., a quarter of the columns
-        const int unit = FP8 ? part >> 1 : 0;
         uint8_t* stg = sm + C::kOffStg + warp * (kStgRows * kStgPitch);
         const int p = lane & 3;
         int use = 0, grp = 0;      // buffers (8-bit: steps) and groups of scales read so far
         bool ok = true;
 #pragma unroll 1
-        for (int i = first_tile; i < total; i += tile_step) {
-            const Tile t = tile_of(tab, P.E, m_tiles, i);
+        for (Walk at = tiles; at.more(); at.next()) {
+            const Tile t = at.tile();
             const int width = t.mma_n() / 4, c0 = part * width;            // this warp's columns of the tile
-            const int uc0 = c0 - unit * (t.mma_n() / C::kUnits);           // ... and of its unit
-            const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + unit * C::kBufs * C::kUnitCols + uc0;
+            const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + c0;
             const int n0 = t.m0 + rank * kM + 32 * q;                      // first output
-            auto out_row = [&](int c) { return (lane & 15) + c < t.n ? y_row(P, t.r0 + c + (lane & 15)) : -1; };
+            int out[C::kCols / 16];        // lane j (< 16): row of y of column 16 i + j
+#pragma unroll
+            for (int c = 0; c < C::kCols; c += 16) {
+                const int col = c0 + c + (lane & 15);
+                out[c / 16] = c < width && col < t.n ? y_row(P, t.r0 + col) : -1;
+            }
             if constexpr (FP8) {
                 float2 acc[C::kCols / 2];
 #pragma unroll
@@ -583,15 +580,15 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                 for (int s = 0; s < nk && ok; ++s, ++use) {
                     const int buf = use % C::kBufs, slot = grp & 1;
                     if (s % kGroup == 0) ok = wait(&sc_full[slot], (grp >> 1) & 1);
-                    if (ok) ok = wait(&acc_full[unit * C::kBufs + buf], (use / C::kBufs) & 1);
+                    if (ok) ok = wait(&acc_full[buf], (use / C::kBufs) & 1);
                     if (!ok) break;
                     tc_fence_after();
                     const float* sc = scale_ring + (slot * kGroup + s % kGroup) * NT + c0 + 2 * p;
 #pragma unroll
                     for (int c = 0; c < C::kCols; c += 16) {
-                        if (c >= width) break;
+                        if (c >= width || c0 + c >= t.n) break;      // padding is neither read nor written
                         float v[16];
-                        tmem_ld_frag(lanes + buf * C::kUnitCols + c, v);
+                        tmem_ld_frag(lanes + buf * NT + c, v);
                         tmem_wait16(v);
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
@@ -607,7 +604,7 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                     __syncwarp();
                     const bool last = s % kGroup == kGroup - 1 || s == nk - 1;
                     if (lane == 0) {
-                        arrive_cluster(map_rank(su32(&acc_empty[unit * C::kBufs + buf]), 0));
+                        arrive_cluster(map_rank(su32(&acc_empty[buf]), 0));
                         if (last) mbar_arrive(&sc_empty[slot]);
                     }
                     grp += last;
@@ -622,24 +619,24 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                         v[2 * j] = bad ? __uint_as_float(0x7FC00000u) : acc[c / 2 + j].x;
                         v[2 * j + 1] = bad ? __uint_as_float(0x7FC00000u) : acc[c / 2 + j].y;
                     }
-                    store_frag(P, v, out_row(c0 + c), n0, stg);
+                    store_frag(P, v, out[c / 16], n0, stg);
                 }
             } else {
                 const int buf = use % C::kBufs;
                 if (ok) ok = wait(&acc_full[buf], (use / C::kBufs) & 1);
                 tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < width; c += 16) {
-                    if (c0 + c >= t.n) break;
+#pragma unroll
+                for (int c = 0; c < C::kCols; c += 16) {
+                    if (c >= width || c0 + c >= t.n) break;
                     float v[16];
                     if (ok) {
-                        tmem_ld_frag(lanes + buf * C::kUnitCols + c, v);
+                        tmem_ld_frag(lanes + buf * NT + c, v);
                         tmem_wait16(v);
                     }
                     if (*abort_flag)
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(0x7FC00000u);
-                    store_frag(P, v, out_row(c0 + c), n0, stg);
+                    store_frag(P, v, out[c / 16], n0, stg);
                 }
                 tc_fence_before();
                 __syncwarp();
