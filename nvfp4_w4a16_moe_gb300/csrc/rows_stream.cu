@@ -210,9 +210,9 @@ cudaError_t launch_stream(const RowsProduct& P, cudaStream_t s) {
     int k_split = kSWarps;
     while (k_split > 1 && chunks < 2 * k_split) k_split /= 2;
     const int span = kSWarps / k_split * 16, n_tiles = (P.N + span - 1) / span;
-    // every pass but an expert's last is full, and every pass has a row
-    const long long full = (P.R + rows - 1) / rows;
-    const long long passes = P.offsets == nullptr ? full : std::min<long long>(P.R, full + P.E);
+    // passes at most: every expert has rows, and its last pass one
+    const int groups = std::min(P.R, P.E);
+    const long long passes = (P.R - groups) / rows + groups;
     const long long grid = passes * n_tiles;
     if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
     rows_stream_kernel<FP8, NB><<<(unsigned)grid, kSThreads, 0, s>>>(P, n_tiles, k_split);

@@ -31,6 +31,10 @@
 //     of its own, so that a buffer is busy for 256 clocks of MMA plus one reading.
 // Tensor memory holds 512 / NT buffers of a tile, so the next tile's or step's MMAs run under the epilogue.
 //
+// Few tiles (a matrix of few rows of W, a small batch): a cluster of two or four pairs shares a tile's K,
+// and the pairs' sums are exchanged through distributed shared memory, each pair finishing a part of the
+// columns: the sums are added in the order of the pairs.
+//
 // Every wait is bounded; one that runs out records NVFP4_ERR_DEVICE_TIMEOUT (where the caller passed a
 // workspace) and makes the pair fill its remaining tiles with NaN.
 #include <atomic>
@@ -49,6 +53,7 @@ constexpr int kStepBytes = 128;          // K bytes of a step: one row of the sw
 constexpr int kABytes = kM * kStepBytes;
 constexpr int kMaxStages = 9;
 constexpr int kMaxTiles = 1 << 30;
+constexpr int kMinSteps = 4;             // steps of each pair that shares a tile's K, at least
 constexpr unsigned long long kCopyDrainNs = 10000000ull;
 constexpr int kGroup = 4;                // steps whose scales are handed over together
 constexpr int kNRound = 64;              // a tile's columns are a multiple of this
@@ -83,6 +88,7 @@ struct Cfg {
     static constexpr int kSmem = 1024 + kOffTab + (3 * NVFP4_MAX_EXPERTS + 1) * 4;
     static_assert(NT % 64 == 0 && NT <= 256 && kStage % 1024 == 0 && kCols % 16 == 0, "swizzle atoms, fragments");
     static_assert(kSmem <= 227 * 1024, "shared memory");
+    static_assert(4 * NT / 16 * 2048 <= kOffScales, "exchanged sums fit in the ring");
 };
 
 struct TcRowMaps {
@@ -162,11 +168,11 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
             " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}"
             :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
-// Arrive on this barrier in both CTAs once every MMA issued so far by this thread has completed.
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+// Arrive on this barrier in both CTAs (cluster mask) once every MMA issued so far by this thread has completed.
+__device__ __forceinline__ void commit_pair(uint64_t* bar, uint16_t mask) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-        :: "r"(su32(bar)), "h"((uint16_t)3) : "memory");
+        :: "r"(su32(bar)), "h"(mask) : "memory");
 }
 // Instruction descriptor of kind::f8f6f4: E4M3 A and B (format 0, both K-major), fp32 D, M x N.
 __device__ __forceinline__ uint32_t e4m3_idesc(int M, int N) {
@@ -290,19 +296,94 @@ __device__ __forceinline__ void store_frag(const RowsProduct& P, const float (&v
                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.y) + (size_t)r * P.N + n0 + 8 * p) = u;
         }
     } else {
-        // rows of y start at any even address
-#pragma unroll 4
-        for (int c = 0; c < 16; ++c) {
-            const int r = __shfl_sync(0xffffffffu, row, c);
-            const uint16_t u = *reinterpret_cast<const uint16_t*>(stg + c * kStgPitch + 2 * lane);
-            if (r >= 0 && n0 + lane < P.N) static_cast<uint16_t*>(P.y)[(size_t)r * P.N + n0 + lane] = u;
+        // Rows of y start at any even address: two rows at a time as 32-bit words from the row's first whole
+        // word on, then the single outputs before and after the words of all rows at once.
+        uint16_t* y = static_cast<uint16_t*>(P.y);
+        const int i = lane & 15;
+#pragma unroll
+        for (int c = 0; c < 16; c += 2) {
+            const int cc = c + (lane >> 4), r = __shfl_sync(0xffffffffu, row, cc);
+            const size_t at = (size_t)max(r, 0) * P.N + n0;
+            const int odd = (int)(at & 1), e = odd + 2 * i;         // outputs e, e + 1
+            const uint32_t* words = reinterpret_cast<const uint32_t*>(stg + cc * kStgPitch) + i;
+            const uint32_t w = odd ? __byte_perm(words[0], words[1], 0x5432) : words[0];
+            if (r >= 0 && e + 1 < 32 && n0 + e + 1 < P.N) *reinterpret_cast<uint32_t*>(y + at + e) = w;
+        }
+        {
+            const int r = __shfl_sync(0xffffffffu, row, i);
+            const size_t at = (size_t)max(r, 0) * P.N + n0;
+            const int odd = (int)(at & 1), in = min(32, P.N - n0);  // outputs of this row here
+            const int e = lane < 16 ? 0 : in - 1;
+            const bool single = lane < 16 ? odd != 0 : ((in - odd) & 1) != 0 && in - 1 >= odd;
+            if (r >= 0 && single && in > 0)
+                y[at + e] = *reinterpret_cast<const uint16_t*>(stg + i * kStgPitch + 2 * e);
         }
     }
     __syncwarp();
 }
 
-template <bool FP8, int NT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+// The pairs of a cluster add up their sums of a tile. Columns go in chunks of 16, chunk g of the tile to
+// pair g % pairs; a pair's CTA sends the chunks that are not its own to the CTA that has the same weight
+// rows there, into that one's ring of stages (every MMA and copy of the cluster is over by then).
+// kCols: columns of a warp at most.
+template <int kCols, int pairs>
+struct Exchange {
+    uint8_t* ring;
+    int pair, rank;
+
+    // [source pair][lane quadrant][own chunk][4][32 lanes] float4
+    __device__ __forceinline__ uint32_t place(int src, int q, int g, int width) const {
+        return (uint32_t)(((src * 4 + q) * (width / 4 / pairs) + g / pairs) * 2048) + (threadIdx.x & 31) * 16;
+    }
+    // Called by all epilogue warps (the CTA's other warps call join). `width` columns a warp from c0 on;
+    // sums(c, v) gives the sums of columns c0 + c ...
+    template <typename Sums>
+    __device__ __forceinline__ void send(const Sums& sums, const Tile& t, int width, int c0, int part, int q) const {
+        cluster_sync_all();      // everyone's MMAs are done
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16) {
+            if (c >= width || c0 + c >= t.n) break;
+            const int g = (part * width + c) / 16, owner = g % pairs;
+            float v[16];
+            sums(c, v);
+            if (owner == pair) continue;
+            const uint32_t to = map_rank(su32(ring) + place(pair, q, g, width), (uint32_t)(2 * owner + rank));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};"
+                             :: "r"(to + 512 * j), "f"(v[4 * j]), "f"(v[4 * j + 1]), "f"(v[4 * j + 2]),
+                                "f"(v[4 * j + 3]) : "memory");
+        }
+        cluster_sync_all();      // everyone's sums have arrived
+    }
+    static __device__ __forceinline__ void join() {
+        cluster_sync_all();
+        cluster_sync_all();
+    }
+    // Adds the other pairs' sums to this pair's own chunk at c, in the order of the pairs; false: not its own.
+    __device__ __forceinline__ bool finish(float (&v)[16], int c, int width, int part, int q) const {
+        const int g = (part * width + c) / 16;
+        if (g % pairs != pair) return false;
+        float own[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) own[j] = v[j], v[j] = 0.f;
+#pragma unroll
+        for (int src = 0; src < pairs; ++src) {
+            const float4* from = reinterpret_cast<const float4*>(ring + place(src, q, g, width));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 f = src == pair ? make_float4(own[4 * j], own[4 * j + 1], own[4 * j + 2], own[4 * j + 3])
+                                             : from[32 * j];
+                v[4 * j] += f.x, v[4 * j + 1] += f.y, v[4 * j + 2] += f.z, v[4 * j + 3] += f.w;
+            }
+        }
+        return true;
+    }
+};
+
+// SPLITS: pairs of a cluster, which share a tile's K.
+template <bool FP8, int NT, int SPLITS>
+__global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(kThreads, 1)
 rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int m_tiles, WsHeader* hdr,
                unsigned long long wait_limit) {
     using C = Cfg<FP8, NT>;
@@ -311,7 +392,9 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
     // pair have the same layout)
     uint8_t* sm = rows_smem_raw + ((1024u - (su32(rows_smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
-    const int rank = (int)cluster_rank();
+    // CTA of its pair, pair of its cluster
+    const int crank = (int)cluster_rank(), rank = crank & 1, pair = SPLITS == 1 ? 0 : crank >> 1, first_rank = 2 * pair;
+    const uint16_t pair_mask = (uint16_t)(3u << first_rank);
 
     float* scale_ring = reinterpret_cast<float*>(sm + C::kOffScales);
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::kOffBars);   // step landed (first CTA: in both)
@@ -389,12 +472,19 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
     cluster_sync_all();       // barriers are ready in both CTAs
     tc_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot), sm_base = su32(sm);
-    // overlapping groups of a malformed list could add up to more tiles than the host allows
-    const int total = uniform((int)min((long long)tab[P.E] * m_tiles, (long long)kMaxTiles));
+    // overlapping groups of a malformed list could add up to more tiles than the host counted: those are left
+    // out, in particular a second tile of a cluster of several pairs
+    constexpr int kCluster = 2 * SPLITS;
+    const int total = uniform((int)min((long long)tab[P.E] * m_tiles,
+                                       SPLITS > 1 ? (long long)(gridDim.x / kCluster) : (long long)kMaxTiles));
     const int kStepK = FP8 ? 128 : 64;
     const int nk = (P.K + kStepK - 1) / kStepK;
-    const Walk tiles(tab, P.E, m_tiles, blockIdx.x >> 1, gridDim.x >> 1, total);
-    const Waiter wait{abort_flag, map_rank(su32(const_cast<int*>(abort_flag)), (uint32_t)rank ^ 1u), hdr, wait_limit};
+    const int s_begin = nk * pair / SPLITS, s_end = nk * (pair + 1) / SPLITS;      // this pair's steps
+    const Walk tiles(tab, P.E, m_tiles, blockIdx.x / kCluster, gridDim.x / kCluster, total);
+    const Waiter wait{abort_flag, map_rank(su32(const_cast<int*>(abort_flag)), (uint32_t)crank ^ 1u), hdr, wait_limit};
+
+    // one tile at most to a cluster of several pairs
+    const Exchange<C::kCols, SPLITS> exchange{sm, pair, rank};
 
     // A warp that issued copies for `step` steps waits until the last fill of each stage has landed before
     // the CTA may exit. (After an abort other warps may not have issued theirs, so that the phase stays
@@ -417,7 +507,7 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                 const CUtensorMap* mx = &maps.x[share / C::kBoxRows - 1];
                 const uint32_t bytes = kABytes + (P.gather ? 0 : share * kStepBytes);
 #pragma unroll 1
-                for (int s = 0; s < nk; ++s, ++step) {
+                for (int s = s_begin; s < s_end; ++s, ++step) {
                     const int st = step % C::kStages, u = step / C::kStages;
                     if (u > 0) ok = wait(&empty[st], (u - 1) & 1);
                     if (!ok) break;
@@ -440,12 +530,12 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                 const int N = at.tile().mma_n();
                 const uint32_t idesc = FP8 ? e4m3_idesc(2 * kM, N) : f16_idesc(2 * kM, N);
 #pragma unroll 1
-                for (int s = 0; s < nk; ++s) {
-                    const bool first = FP8 || s == 0, sum_done = FP8 || s == nk - 1;
+                for (int s = s_begin; s < s_end; ++s) {
+                    const bool first = FP8 || s == s_begin, sum_done = FP8 || s == s_end - 1;
                     ok = wait(&full[st], st_par);
                     if (!ok) break;
                     if (rank != 0) {
-                        if (elect_one()) arrive_cluster(map_rank(su32(&full[st]), 0));
+                        if (elect_one()) arrive_cluster(map_rank(su32(&full[st]), first_rank));
                     } else {
                         if (first) ok = wait(&acc_empty[buf], buf_par);
                         if (!ok) break;
@@ -455,8 +545,8 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
 #pragma unroll
                             for (int j = 0; j < kStepBytes / 32; ++j)      // 32 bytes of K an MMA: 2 address units
                                 mma_pair<FP8>(tmem + buf * NT, a + 2 * j, b + 2 * j, idesc, !first || j != 0);
-                            commit_pair(&empty[st]);
-                            if (sum_done) commit_pair(&acc_full[buf]);
+                            commit_pair(&empty[st], pair_mask);
+                            if (sum_done) commit_pair(&acc_full[buf], pair_mask);
                         }
                         if (sum_done && ++buf == C::kBufs) buf = 0, buf_par ^= 1;
                     }
@@ -466,7 +556,7 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
             if (rank == 0) {
                 // no MMA still reads or writes either CTA's memory when it is freed
                 if (elect_one()) {
-                    commit_pair(done);
+                    commit_pair(done, pair_mask);
                     drain_wait(done, 0);
                 }
             }
@@ -488,7 +578,7 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                     if (src < 0) src = P.x_rows;                     // past the last row: zeros
                     const int mine = (copies - w + kGatherWarps - 1) / kGatherWarps;
 #pragma unroll 1
-                    for (int s = 0; s < nk; ++s, ++step) {
+                    for (int s = s_begin; s < s_end; ++s, ++step) {
                         const int st = step % C::kStages, u = step / C::kStages;
                         if (u > 0) ok = wait(&empty[st], (u - 1) & 1);
                         if (!ok) break;
@@ -527,32 +617,33 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                     for (int d = 0; d < kGroup; ++d)
 #pragma unroll
                         for (int j = 0; j < kPer; ++j)
-                            next[d][j] = xs[j] >= 0 && s0 + d < nk ? P.xs[(size_t)xs[j] * KB + s0 + d] : 0.f;
+                            next[d][j] = xs[j] >= 0 && s0 + d < s_end ? P.xs[(size_t)xs[j] * KB + s0 + d] : 0.f;
                 };
 #pragma unroll
                 for (int j = 0; j < kPer; ++j) {
                     const int col = th + kScaleThreads * j;
                     xs[j] = nb < NB && col < t.n ? x_row(P, t.r0 + col) : -1;
                 }
-                load(0);
+                load(s_begin);
 #pragma unroll 1
-                for (int s = 0; s < nk; s += kGroup, ++grp) {
+                for (int s = s_begin; s < s_end; s += kGroup, ++grp) {
                     const int slot = grp & 1, u = grp >> 1;
                     if (u > 0) ok = wait(&sc_empty[slot], (u - 1) & 1);
                     if (!ok) break;
 #pragma unroll
                     for (int d = 0; d < kGroup; ++d) {
-                        const float sw = s + d < nk ? wsc[s + d] : 0.f;
+                        const float sw = s + d < s_end ? wsc[s + d] : 0.f;
 #pragma unroll
                         for (int j = 0; j < kPer; ++j)
                             scale_ring[(slot * kGroup + d) * NT + th + kScaleThreads * j] =
                                 xs[j] >= 0 ? next[d][j] * sw : 0.f;
                     }
                     mbar_arrive(&sc_full[slot]);
-                    if (s + kGroup < nk) load(s + kGroup);
+                    if (s + kGroup < s_end) load(s + kGroup);
                 }
             }
         }
+        if (SPLITS > 1 && tiles.more()) exchange.join();
     } else {
         if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kEpiRegs));
         const int q = warp & 3, part = warp >> 2;          // lanes 32 q .., a quarter of the columns
@@ -577,7 +668,7 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
 #pragma unroll
                 for (int j = 0; j < C::kCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
 #pragma unroll 1
-                for (int s = 0; s < nk && ok; ++s, ++use) {
+                for (int s = 0; s < s_end - s_begin && ok; ++s, ++use) {
                     const int buf = use % C::kBufs, slot = grp & 1;
                     if (s % kGroup == 0) ok = wait(&sc_full[slot], (grp >> 1) & 1);
                     if (ok) ok = wait(&acc_full[buf], (use / C::kBufs) & 1);
@@ -602,33 +693,35 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                     }
                     tc_fence_before();
                     __syncwarp();
-                    const bool last = s % kGroup == kGroup - 1 || s == nk - 1;
+                    const bool last = s % kGroup == kGroup - 1 || s == s_end - s_begin - 1;
                     if (lane == 0) {
-                        arrive_cluster(map_rank(su32(&acc_empty[buf]), 0));
+                        arrive_cluster(map_rank(su32(&acc_empty[buf]), first_rank));
                         if (last) mbar_arrive(&sc_empty[slot]);
                     }
                     grp += last;
                 }
-                const bool bad = *abort_flag != 0;
-#pragma unroll
-                for (int c = 0; c < C::kCols; c += 16) {
-                    if (c >= width || c0 + c >= t.n) break;
-                    float v[16];
+                const auto sums = [&](int c, float (&v)[16]) {
+                    const bool bad = *abort_flag != 0;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         v[2 * j] = bad ? __uint_as_float(0x7FC00000u) : acc[c / 2 + j].x;
                         v[2 * j + 1] = bad ? __uint_as_float(0x7FC00000u) : acc[c / 2 + j].y;
                     }
+                };
+                if constexpr (SPLITS > 1) exchange.send(sums, t, width, c0, part, q);
+#pragma unroll
+                for (int c = 0; c < C::kCols; c += 16) {
+                    if (c >= width || c0 + c >= t.n) break;
+                    float v[16];
+                    sums(c, v);
+                    if (SPLITS > 1 && !exchange.finish(v, c, width, part, q)) continue;
                     store_frag(P, v, out[c / 16], n0, stg);
                 }
             } else {
                 const int buf = use % C::kBufs;
                 if (ok) ok = wait(&acc_full[buf], (use / C::kBufs) & 1);
                 tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < C::kCols; c += 16) {
-                    if (c >= width || c0 + c >= t.n) break;
-                    float v[16];
+                const auto sums = [&](int c, float (&v)[16]) {
                     if (ok) {
                         tmem_ld_frag(lanes + buf * NT + c, v);
                         tmem_wait16(v);
@@ -636,11 +729,19 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                     if (*abort_flag)
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(0x7FC00000u);
+                };
+                if constexpr (SPLITS > 1) exchange.send(sums, t, width, c0, part, q);
+#pragma unroll
+                for (int c = 0; c < C::kCols; c += 16) {
+                    if (c >= width || c0 + c >= t.n) break;
+                    float v[16];
+                    sums(c, v);
+                    if (SPLITS > 1 && !exchange.finish(v, c, width, part, q)) continue;
                     store_frag(P, v, out[c / 16], n0, stg);
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (ok && lane == 0) arrive_cluster(map_rank(su32(&acc_empty[buf]), 0));
+                if (ok && lane == 0) arrive_cluster(map_rank(su32(&acc_empty[buf]), first_rank));
                 ++use;
             }
         }
@@ -668,34 +769,47 @@ bool encode_rows(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* m, const voi
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <bool FP8, int NT, int SPLITS>
+cudaError_t launch_clusters(const RowsProduct& P, const TcRowMaps& maps, int m_tiles, int clusters, WsHeader* hdr,
+                            const DeviceInfo& dev, uint64_t wait_limit, cudaStream_t s) {
+    using C = Cfg<FP8, NT>;
+    static std::atomic<uint64_t> ready{0};      // one bit per device
+    if (!(ready.load(std::memory_order_acquire) >> dev.device & 1)) {
+        cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<FP8, NT, SPLITS>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e != cudaSuccess) return e;
+        // the register split waits forever for registers that the launch did not bring
+        cudaFuncAttributes a;
+        if ((e = cudaFuncGetAttributes(&a, rows_tc_kernel<FP8, NT, SPLITS>)) != cudaSuccess) return e;
+        if (FP8 && a.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+        ready.fetch_or(1ull << dev.device, std::memory_order_release);
+    }
+    rows_tc_kernel<FP8, NT, SPLITS><<<2 * SPLITS * clusters, kThreads, C::kSmem, s>>>(P, maps, m_tiles, hdr, wait_limit);
+    return cudaGetLastError();
+}
+
 template <bool FP8, int NT>
 cudaError_t launch_tc(const RowsProduct& P, WsHeader* hdr, const DeviceInfo& dev, uint64_t wait_limit,
                       cudaStream_t s) {
     using C = Cfg<FP8, NT>;
-    static std::atomic<uint64_t> ready{0};      // one bit per device
-    if (!(ready.load(std::memory_order_acquire) >> dev.device & 1)) {
-        cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<FP8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             C::kSmem);
-        if (e != cudaSuccess) return e;
-        // the register split waits forever for registers that the launch did not bring
-        cudaFuncAttributes a;
-        if ((e = cudaFuncGetAttributes(&a, rows_tc_kernel<FP8, NT>)) != cudaSuccess) return e;
-        if (FP8 && a.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-        ready.fetch_or(1ull << dev.device, std::memory_order_release);
-    }
     PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
     TcRowMaps maps;
     if (fn == nullptr || !encode_rows(fn, &maps.w, P.w, FP8, P.K, (uint64_t)P.E * P.N, kM)) return cudaErrorInvalidValue;
     for (int i = 0; i < (P.gather ? 1 : C::kBoxes); ++i)
         if (!encode_rows(fn, &maps.x[i], P.x, FP8, P.K, P.x_rows, P.gather ? 1 : (i + 1) * C::kBoxRows))
             return cudaErrorInvalidValue;
-    const int m_tiles = (P.N + 2 * kM - 1) / (2 * kM);
-    // tiles at most: every expert's last one is not full
-    const long long tiles = (P.R / NT + std::min(P.R, P.E)) * (long long)m_tiles;
+    const int m_tiles = (P.N + 2 * kM - 1) / (2 * kM), nk = (P.K * (FP8 ? 1 : 2) + kStepBytes - 1) / kStepBytes;
+    // tiles at most: every expert has rows, and its last tile one
+    const int groups = std::min(P.R, P.E);
+    const long long tiles = ((P.R - groups) / NT + groups) * (long long)m_tiles;
     if (tiles > kMaxTiles) return cudaErrorInvalidConfiguration;
-    const unsigned pairs = (unsigned)std::min<long long>(tiles, dev.num_sms / 2);
-    rows_tc_kernel<FP8, NT><<<2 * pairs, kThreads, C::kSmem, s>>>(P, maps, m_tiles, hdr, wait_limit);
-    return cudaGetLastError();
+    const int pairs = dev.num_sms / 2;
+    const int one = (int)std::min<long long>(tiles, pairs);
+    if (4 * tiles <= pairs && nk >= 4 * kMinSteps)
+        return launch_clusters<FP8, NT, 4>(P, maps, m_tiles, one, hdr, dev, wait_limit, s);
+    if (2 * tiles <= pairs && nk >= 2 * kMinSteps)
+        return launch_clusters<FP8, NT, 2>(P, maps, m_tiles, one, hdr, dev, wait_limit, s);
+    return launch_clusters<FP8, NT, 1>(P, maps, m_tiles, one, hdr, dev, wait_limit, s);
 }
 
 template <bool FP8>

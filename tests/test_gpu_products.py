@@ -293,11 +293,12 @@ def test_grouped_both_maps_and_unwritten_rows(nv, T, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
-@pytest.mark.parametrize("T", [3, 180])
-def test_grouped_bad_offsets_and_entries_stay_in_bounds(nv, T, fp8):
-    """Offsets outside [0, R] and groups that run backwards, entries outside [0, R): as documented."""
+@pytest.mark.parametrize("T,K", [(3, 144), (180, 144), (180, 2048)])
+def test_grouped_bad_offsets_and_entries_stay_in_bounds(nv, T, K, fp8):
+    """Offsets outside [0, R] and groups that run backwards, entries outside [0, R): as documented. (The
+    last case has few tiles and a long K, which several pairs of CTAs share.)"""
     for rows in ("gather", "scatter"):
-        a, xd, wd, off, lst, R = _grouped_case(T, 2, 5, 130, 144, "even", rows, fp8, 21)
+        a, xd, wd, off, lst, R = _grouped_case(T, 2, 5, 130, K, "even", rows, fp8, 21)
         off = torch.tensor([-5, 2, 1, 3, R, R + 100], dtype=torch.int32)
         lst[2], lst[0], lst[R - 1] = -1, R, 2 ** 31 - 1
         a["offsets"], a["token_list"] = off.cuda(), lst.cuda()
@@ -314,6 +315,34 @@ def test_grouped_bad_offsets_and_entries_stay_in_bounds(nv, T, fp8):
             touched = {int(v) for v in lst if 0 <= int(v) < R}
             for r in set(range(R)) - touched:
                 assert (got[r] == -77.0).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("K", [144, 1024])
+def test_grouped_groups_that_all_overlap(nv, K, fp8):
+    """Every group is the whole list: far more tiles than the host counts. The call stays in bounds and
+    returns, and the next one is right."""
+    a, xd, wd, off, lst, R = _grouped_case(130, 2, 40, 130, K, "even", "list", fp8, 3)
+    good = a["offsets"]
+    bad = torch.tensor([0, R] * 20 + [0], dtype=torch.int32).cuda()
+    y = torch.full((R + 1, 130), -77.0, device="cuda")
+    _call(nv, dict(a, offsets=bad), y=y[:R])
+    assert (y[R] == -77.0).all()
+    _check_exact(_call(nv, dict(a, offsets=good), out_dtype=torch.float32), _want(a, xd, wd, off, lst, R)[0])
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("N", [1, 3, 33, 250, 255, 257, 1022])
+def test_grouped_output_widths(nv, N, fp8):
+    """Rows of y that start at every alignment, ends inside a 32-output piece and a 128-row half; the
+    element after the last row is left alone."""
+    a, xd, wd, off, lst, R = _grouped_case(60, 2, 3, N, 160, "skew", "scatter", fp8, N)
+    want = _want(a, xd, wd, off, lst, R)[0]
+    for dt in (torch.bfloat16, torch.float32):
+        buf = torch.full((R * N + 64,), -77.0, dtype=dt, device="cuda")
+        _call(nv, a, y=buf[:R * N].view(R, N))
+        _check_exact(buf[:R * N].view(R, N), want, dt)
+        assert (buf[R * N:] == -77.0).all()
 
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
