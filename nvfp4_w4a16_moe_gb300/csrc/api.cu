@@ -150,7 +150,7 @@ nvfp4_status run_product(RowsProduct P, bool fp8, int32_t y_type, void* workspac
     DeviceInfo dev;
     if (nvfp4_status st = device_info(&dev); st != NVFP4_OK) return st;
     if (P.R == 0) return NVFP4_OK;
-    if (P.R <= kStreamRows) return from_cuda(launch_rows_stream(P, static_cast<cudaStream_t>(stream)));
+    if (P.R <= kStreamRows) return from_cuda(launch_rows_stream(P, dev, static_cast<cudaStream_t>(stream)));
     return from_cuda(launch_rows_tc(P, static_cast<WsHeader*>(workspace), dev, g_wait_limit.load(),
                                     static_cast<cudaStream_t>(stream)));
 }

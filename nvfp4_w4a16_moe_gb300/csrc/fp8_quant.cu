@@ -14,6 +14,8 @@
 //
 // Bound: HBM, 2 bytes read and 1 written per element, one pass: each block stays in registers
 // between its maximum and its codes.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -23,6 +25,10 @@ namespace {
 
 constexpr int kQThreads = 256;
 constexpr float kE4m3Max = 448.0f;
+// Fewer blocks than this: one pair of blocks a warp and short latency (us, 1 against 4 pairs: 1 x 2048 1.6 / 1.9,
+// 512 x 2048 2.3 / 2.4); more: four pairs, whose divisions are done together (4096 x 2048 6.3 / 5.3, 262144 x 2048
+// 351 / 251, 6.4 TB/s).
+constexpr size_t kFewBlocks = 1u << 14;
 
 // Larger of two |x| as fp32 bits: NaN above infinity above every number, so a NaN is kept.
 __device__ __forceinline__ uint32_t absmax8(const uint4 v) {
@@ -36,25 +42,20 @@ __device__ __forceinline__ uint32_t absmax8(const uint4 v) {
     return m;
 }
 
-struct BlockScale {
-    float pre;    // power of two that brings a tiny amax into range
-    float inv;    // 448 / (amax * pre)
-    float scale;  // amax / 448, or 1
-    uint32_t half;  // half a unit of the 16th significant bit; 0 for a block that holds infinity or NaN
-};
+// Below this amax 448 / amax could overflow: the block is first brought up by 2^64, exactly.
+constexpr float kTinyAmax = 0x1p-100f;
 
-__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
+__device__ __forceinline__ float block_scale(uint32_t amax_bits) {
+    return amax_bits == 0u ? 1.0f : __uint_as_float(amax_bits) / kE4m3Max;
+}
+// 448 / amax, of a tiny block 448 / (2^64 amax).
+__device__ __forceinline__ float block_inverse(uint32_t amax_bits) {
     const float a = __uint_as_float(amax_bits);
-    BlockScale b;
-    b.pre = a < 0x1p-64f ? 0x1p64f : 1.0f;   // 448 / a stays below fp32's largest
-    b.scale = amax_bits == 0u ? 1.0f : a / kE4m3Max;
-    b.inv = amax_bits == 0u ? 1.0f : kE4m3Max / (a * b.pre);
-    b.half = amax_bits < 0x7F800000u ? 0x80u : 0u;
-    return b;
+    return amax_bits == 0u ? 1.0f : kE4m3Max / (a < kTinyAmax ? a * 0x1p64f : a);
 }
 
-// p rounded to 16 significant bits. In a block with infinities or NaN nothing is added, so that
-// the quotient's NaN does not wrap into a number.
+// p rounded to 16 significant bits. In a block with infinities or NaN nothing is added (half 0), so
+// that the quotient's NaN does not wrap into a number.
 __device__ __forceinline__ float snap16(float p, uint32_t half) {
     return __uint_as_float((__float_as_uint(p) + half) & 0xFFFFFF00u);
 }
@@ -65,23 +66,26 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-// Eight bf16 -> eight codes.
-__device__ __forceinline__ uint2 quantize8(const uint4 v, const BlockScale b) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// Eight bf16 of a block with this amax -> eight codes.
+__device__ __forceinline__ uint2 quantize8(const uint4 v, uint32_t amax_bits, float inv) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (__uint_as_float(amax_bits) < kTinyAmax) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = (uint32_t)f32_to_bf16(bf16lo(w[i]) * 0x1p64f) | ((uint32_t)f32_to_bf16(bf16hi(w[i]) * 0x1p64f) << 16);
+    }
+    const uint32_t half = amax_bits < 0x7F800000u ? 0x80u : 0u;
     uint32_t h[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        h[i] = e4m3x2(snap16(bf16lo(w[i]) * b.pre * b.inv, b.half), snap16(bf16hi(w[i]) * b.pre * b.inv, b.half));
+    for (int i = 0; i < 4; ++i) h[i] = e4m3x2(snap16(bf16lo(w[i]) * inv, half), snap16(bf16hi(w[i]) * inv, half));
     return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
-// 1 x 128 blocks: 16 lanes hold one block, a warp takes kUnroll pairs of neighbouring blocks so
-// that it has kUnroll 16-byte loads a lane in flight.
-constexpr int kUnroll = 4;
-
+// 1 x 128 blocks: 16 lanes hold one block, a warp takes kUnroll pairs of neighbouring blocks.
+// WHOLE: K is a multiple of 128, the blocks follow one another without a gap.
+template <int kUnroll, bool WHOLE>
 __global__ void __launch_bounds__(kQThreads)
-quantize_rows_kernel(const uint16_t* x, size_t blocks, int K, int KB, uint8_t* q,
-                     float* scales) {
+quantize_rows_kernel(const uint16_t* x, size_t blocks, int K, unsigned KB, uint8_t* q, float* scales) {
     const int lane = threadIdx.x & 31, unit = lane & 15, half = lane >> 4;
     const size_t warp = (size_t)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
     const size_t first = warp * (2 * kUnroll) + half;
@@ -93,22 +97,32 @@ quantize_rows_kernel(const uint16_t* x, size_t blocks, int K, int KB, uint8_t* q
         v[u] = make_uint4(0, 0, 0, 0);
         at[u] = ~size_t(0);
         if (blk < blocks) {
-            const size_t row = blk / KB;
-            const int col = (int)(blk - row * KB) * 128 + unit * 8;
-            if (col < K) {
-                at[u] = row * K + col;
-                v[u] = ld_once_v4(x + at[u]);
+            if (WHOLE) {
+                at[u] = blk * 128 + unit * 8;
+            } else {
+                // 32-bit division where the numbers allow it
+                const size_t row = blocks >> 32 ? blk / KB : (size_t)((unsigned)blk / KB);
+                const int col = (int)(blk - row * KB) * 128 + unit * 8;
+                if (col < K) at[u] = row * K + col;
             }
+            if (at[u] != ~size_t(0)) v[u] = ld_once_v4(x + at[u]);
         }
     }
+    // lane u of a half warp keeps the maximum of block u, so that the divisions are done once for all blocks
+    uint32_t m[kUnroll], mine = 0;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-        uint32_t m = absmax8(v[u]);
+        m[u] = absmax8(v[u]);
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const BlockScale b = block_scale(m);
-        if (at[u] != ~size_t(0)) *reinterpret_cast<uint2*>(q + at[u]) = quantize8(v[u], b);
-        if (unit == 0 && first + 2 * u < blocks) scales[first + 2 * u] = b.scale;
+        for (int o = 8; o > 0; o >>= 1) m[u] = max(m[u], __shfl_xor_sync(0xffffffffu, m[u], o));
+        if (unit == u) mine = m[u];
+    }
+    const float inv = block_inverse(mine);
+    if (unit < kUnroll && first + 2 * unit < blocks) scales[first + 2 * unit] = block_scale(mine);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        const float iu = __shfl_sync(0xffffffffu, inv, u, 16);
+        if (at[u] != ~size_t(0)) *reinterpret_cast<uint2*>(q + at[u]) = quantize8(v[u], m[u], iu);
     }
 }
 
@@ -138,12 +152,12 @@ quantize_tiles_kernel(const uint16_t* x, int R, int K, int RB, int KB, uint8_t* 
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kQThreads / 32; ++i) m = max(m, s_max[i]);
-    const BlockScale b = block_scale(m);
+    const float inv = block_inverse(m);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (col < K && row0 + 16 * i < R)
-            *reinterpret_cast<uint2*>(q + base + (size_t)16 * i * K) = quantize8(v[i], b);
-    if (threadIdx.x == 0) scales[blk] = b.scale;
+            *reinterpret_cast<uint2*>(q + base + (size_t)16 * i * K) = quantize8(v[i], m, inv);
+    if (threadIdx.x == 0) scales[blk] = block_scale(m);
 }
 
 }  // namespace
@@ -152,8 +166,18 @@ cudaError_t launch_fp8_quantize(const uint16_t* x, int B, int R, int K, int bloc
                                 cudaStream_t s) {
     const int KB = (K + 127) / 128;
     if (block_rows == 1) {
-        const size_t blocks = (size_t)B * R * KB, per = (kQThreads / 32) * 2 * kUnroll;
-        quantize_rows_kernel<<<(unsigned)((blocks + per - 1) / per), kQThreads, 0, s>>>(x, blocks, K, KB, q, scales);
+        const size_t blocks = (size_t)B * R * KB;
+        auto run = [&](auto unroll) {
+            constexpr int kUnroll = decltype(unroll)::value;
+            const size_t per = (kQThreads / 32) * 2 * kUnroll;
+            const unsigned grid = (unsigned)((blocks + per - 1) / per);
+            if (K % 128 == 0)
+                quantize_rows_kernel<kUnroll, true><<<grid, kQThreads, 0, s>>>(x, blocks, K, KB, q, scales);
+            else
+                quantize_rows_kernel<kUnroll, false><<<grid, kQThreads, 0, s>>>(x, blocks, K, KB, q, scales);
+        };
+        if (blocks < kFewBlocks) run(std::integral_constant<int, 1>{});
+        else run(std::integral_constant<int, 4>{});
     } else {
         const int RB = (R + 127) / 128;
         quantize_tiles_kernel<<<(unsigned)((size_t)B * RB * KB), kQThreads, 0, s>>>(x, R, K, RB, KB, q, scales);

@@ -203,11 +203,11 @@ __device__ __forceinline__ int y_row(const RowsProduct& P, int r) {
 }
 
 // Up to kStreamRows rows in all: weights streamed through warp-level MMAs; more: tcgen05 tiles. Measured on
-// a GB300 (us a call, stream / tiles): one matrix 2048 x 8192 in 8 bits at 8 rows 12.6 / 23.1, at 16 12.9 /
-// 23.2, at 32 21.0 / 23.2; 8192 x 2048 at 16 rows 11.2 / 11.3, at 32 19.3 / 11.3; 256 experts of 1024 x 2048
-// at 8 rows 11.3 / 12.9, at 32 22.3 / 19.4.
-constexpr int kStreamRows = 16;
-cudaError_t launch_rows_stream(const RowsProduct& P, cudaStream_t s);
+// a GB300 (us on the device, stream / tiles): 8192 x 2048 in 8 bits at 8 rows 6.2 / 7.9, at 16 rows (two blocks
+// of columns in the streaming kernel) 8.2 / 8.0; 2048 x 8192 at 8 rows 7.4 / 9.9; 8 bf16 experts of 1024 x 2048
+// with a row each 7.2 / 10.6, 15 with 16 rows 19.3 / 13.7.
+constexpr int kStreamRows = 8;
+cudaError_t launch_rows_stream(const RowsProduct& P, const DeviceInfo& dev, cudaStream_t s);
 cudaError_t launch_rows_tc(const RowsProduct& P, WsHeader* hdr, const DeviceInfo& dev, uint64_t wait_limit,
                            cudaStream_t s);
 

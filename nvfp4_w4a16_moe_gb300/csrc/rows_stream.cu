@@ -2,16 +2,24 @@
 // cores: y[o(r), n] = sum_k W[e(r)][n, k] x[i(r), k].
 //
 // With few rows a call is bound by the bytes of W, so the kernel only has to keep them coming:
-//  - A CTA owns 16 rows of one expert's W and up to 8 * NB of the expert's list positions; its
-//    warps split K in chunks of 128 bytes of a row. A lane reads whole 16-byte units of W and x
-//    straight from global memory into the fragment registers of mma.sync m16n8: the lane in
-//    column group c takes units c and 4 + c of a chunk, and the four words of a unit feed two
-//    MMAs. This permutes K inside a chunk, in the same way for both operands, so the sum is
+//  - A CTA owns 16 or more rows of one expert's W (below) and up to 8 of the expert's list positions;
+//    its warps split K in chunks of 128 bytes of a row. A lane reads whole 16-byte units of W and x
+//    straight from global memory into the fragment registers of mma.sync m16n8k16: the lane in
+//    column group c takes units c and 4 + c of a chunk, and the words of a unit feed two (bf16) or
+//    four MMAs (8-bit). This permutes K inside a chunk, in the same way for both operands, so the sum is
 //    over the same products; no shared memory or transposition is needed.
+//  - One chunk a warp at a time and four CTAs on an SM: 64 KB of W in flight. (Two chunks a warp and two
+//    CTAs: 9.3 us for the gate/up of one token over 8 bf16 experts of 1024 x 2048, this way 6.9.) A grid
+//    that fills the device less than that requests the next chunk before it uses this one (AHEAD: 80
+//    registers, three CTAs: 2048 x 8192 in bf16 7.4 us against 9.3; on the larger grid above 8.4 against 6.7).
 //  - The warps' fp32 partial sums are added in warp order in shared memory: the same bits on
 //    every run.
-//  - 8-bit operands: a chunk is one block of 128, summed from zero in fp32 and added to the
-//    running sum times the block's two scales.
+//  - Rows so short that eight warps would not have two chunks each share a CTA instead: with K = 512 in
+//    8 bits a 64-token batch over 256 experts fell from 147 to 58 us.
+//  - 8-bit operands are converted to f16, exactly, in registers (as fast as the 8-bit form of mma.sync, or
+//    faster: 109 against 113 us for one token and 248320 x 2048, where the conversions bound it at
+//    4.7 TB/s; bf16 streams the same matrix at 6.5 TB/s, 96 % of the measured copy rate). A chunk is one
+//    block of 128, summed from zero in fp32 and added to the running sum times the block's two scales.
 // Widths that are no multiple of a chunk read zero units past the end.
 #include "common.cuh"
 #include "kernels.cuh"
@@ -22,7 +30,8 @@ namespace {
 
 constexpr int kSWarps = 8;
 constexpr int kSThreads = kSWarps * 32;
-constexpr int kSAhead = 2;      // chunks of W a lane requests before it uses them
+constexpr int kAheadCtas = 3;        // CTAs on an SM that request a chunk ahead
+constexpr int kRows = 8;             // list positions of a pass: the columns of an MMA
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -31,17 +40,29 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
+// Two E4M3 pairs of a word -> two f16x2 (exact).
+__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Four k of a lane of two rows of W and one of x, in E4M3.
+__device__ __forceinline__ void mma_e4m3_word(float (&d)[4], uint32_t p, uint32_t q, uint32_t x) {
+    uint32_t p0, p1, q0, q1, x0, x1;
+    e4m3x4_f16(p, p0, p1);
+    e4m3x4_f16(q, q0, q1);
+    e4m3x4_f16(x, x0, x1);
+    mma_f16(d, p0, q0, p1, q1, x0, x1);
 }
 
 // Pass `p` of the call -> its expert, first list position and rows. Passes are numbered over the
 // experts in order, up to kRows positions each. Returns false past the last pass.
-template <int kRows>
 __device__ __forceinline__ bool locate_pass(const RowsProduct& P, int p, int* e, int* r0, int* n) {
     if (P.offsets == nullptr) {
         *e = 0;
@@ -82,10 +103,9 @@ __device__ __forceinline__ bool locate_pass(const RowsProduct& P, int p, int* e,
     return s_n > 0;
 }
 
-template <bool FP8, int NB>
-__global__ void __launch_bounds__(kSThreads, 2)
+template <bool FP8, bool AHEAD>
+__global__ void __launch_bounds__(kSThreads, AHEAD ? kAheadCtas : kAheadCtas + 1)
 rows_stream_kernel(const RowsProduct P, int n_tiles, int k_split) {
-    constexpr int kRows = 8 * NB;
     __shared__ float s_acc[kSWarps][16][kRows + 1];
     // row tiles of this CTA: one for every k_split warps
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -93,7 +113,7 @@ rows_stream_kernel(const RowsProduct P, int n_tiles, int k_split) {
     const int pass = blockIdx.x / n_tiles;
     const int n0 = ((blockIdx.x - pass * n_tiles) * (kSWarps / k_split) + n_part) * 16;
     int e, r0, rows;
-    if (!locate_pass<kRows>(P, pass, &e, &r0, &rows)) return;
+    if (!locate_pass(P, pass, &e, &r0, &rows)) return;
 
     constexpr int kUnit = FP8 ? 16 : 8;            // elements of a 16-byte unit
     const int g = lane >> 2, c = lane & 3;
@@ -109,83 +129,70 @@ rows_stream_kernel(const RowsProduct P, int n_tiles, int k_split) {
         if (n0 + g < P.N) w0 = w + (size_t)g * units;
         if (n0 + g + 8 < P.N) w1 = w + (size_t)(g + 8) * units;
     }
-    uint4 a[kSAhead][2][2];
-    auto load_w = [&](int ch0) {
+    uint4 a[2][2];
+    auto load_w = [&](int ch, uint4 (&v)[2][2]) {
 #pragma unroll
-        for (int i = 0; i < kSAhead; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int u = (ch0 + i * k_split) * 8 + 4 * h + c;
-                a[i][h][0] = w0 != nullptr && u < units ? ld_once_v4(w0 + u) : zero;
-                a[i][h][1] = w1 != nullptr && u < units ? ld_once_v4(w1 + u) : zero;
-            }
+        for (int h = 0; h < 2; ++h) {
+            const int u = ch * 8 + 4 * h + c;
+            v[h][0] = w0 != nullptr && u < units ? ld_once_v4(w0 + u) : zero;
+            v[h][1] = w1 != nullptr && u < units ? ld_once_v4(w1 + u) : zero;
+        }
     };
-    load_w(k_part);                                // on its way while the list is read
+    load_w(k_part, a);                             // on its way while the list is read
 
-    const uint4* xr[NB];
-    const float* xs[NB][2];
+    const int row = g < rows ? x_row(P, r0 + g) : -1;
+    const uint4* xr = row < 0 ? nullptr : static_cast<const uint4*>(P.x) + (size_t)row * units;
+    const float* xs[2] = {nullptr, nullptr};
+    if constexpr (FP8) {
+        // the rows of this lane's two columns are those of the lanes 4 * column
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        const int row = 8 * b + g < rows ? x_row(P, r0 + 8 * b + g) : -1;
-        xr[b] = row < 0 ? nullptr : static_cast<const uint4*>(P.x) + (size_t)row * units;
-        if constexpr (FP8) {
-            // the rows of this lane's two columns are those of the lanes 4 * column
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int cr = __shfl_sync(0xffffffffu, row, 4 * (2 * c + j));
-                xs[b][j] = cr < 0 ? nullptr : P.xs + (size_t)cr * KB;
-            }
+        for (int j = 0; j < 2; ++j) {
+            const int cr = __shfl_sync(0xffffffffu, row, 4 * (2 * c + j));
+            if (cr >= 0) xs[j] = P.xs + (size_t)cr * KB;
         }
     }
     const float* wsc = FP8 ? P.ws + ((size_t)e * ((P.N + 127) >> 7) + (min(n0, P.N - 1) >> 7)) * KB : nullptr;
 
-    float acc[NB][4];
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int ch = k_part; ch < chunks; ch += k_split) {
+        uint4 next[2][2];
+        if (AHEAD) load_w(ch + k_split, next);
+        const float sw = FP8 ? wsc[ch] : 0.f;
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[b][i] = 0.f;
-
-    for (int ch0 = k_part; ch0 < chunks; ch0 += k_split * kSAhead) {
-#pragma unroll
-        for (int i = 0; i < kSAhead; ++i) {
-            const int ch = ch0 + i * k_split;
-            if (ch >= chunks) break;
-            const float sw = FP8 ? wsc[ch] : 0.f;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int u = ch * 8 + 4 * h + c;
-                    const uint4 x = xr[b] != nullptr && u < units ? xr[b][u] : zero;
-                    const uint4 p = a[i][h][0], q = a[i][h][1];
-                    if constexpr (FP8) {
-                        mma_e4m3(part, p.x, q.x, p.y, q.y, x.x, x.y);
-                        mma_e4m3(part, p.z, q.z, p.w, q.w, x.z, x.w);
-                    } else {
-                        mma_bf16(acc[b], p.x, q.x, p.y, q.y, x.x, x.y);
-                        mma_bf16(acc[b], p.z, q.z, p.w, q.w, x.z, x.w);
-                    }
-                }
-                if constexpr (FP8) {
-                    const float s0 = xs[b][0] != nullptr ? xs[b][0][ch] * sw : 0.f;
-                    const float s1 = xs[b][1] != nullptr ? xs[b][1][ch] * sw : 0.f;
-                    acc[b][0] = fmaf(part[0], s0, acc[b][0]);
-                    acc[b][1] = fmaf(part[1], s1, acc[b][1]);
-                    acc[b][2] = fmaf(part[2], s0, acc[b][2]);
-                    acc[b][3] = fmaf(part[3], s1, acc[b][3]);
-                }
+        for (int h = 0; h < 2; ++h) {
+            const int u = ch * 8 + 4 * h + c;
+            const uint4 x = xr != nullptr && u < units ? xr[u] : zero;
+            const uint4 p = a[h][0], q = a[h][1];
+            if constexpr (FP8) {
+                mma_e4m3_word(part, p.x, q.x, x.x);
+                mma_e4m3_word(part, p.y, q.y, x.y);
+                mma_e4m3_word(part, p.z, q.z, x.z);
+                mma_e4m3_word(part, p.w, q.w, x.w);
+            } else {
+                mma_bf16(acc, p.x, q.x, p.y, q.y, x.x, x.y);
+                mma_bf16(acc, p.z, q.z, p.w, q.w, x.z, x.w);
             }
         }
-        if (ch0 + k_split * kSAhead < chunks) load_w(ch0 + k_split * kSAhead);
-    }
+        if constexpr (FP8) {
+            const float s0 = xs[0] != nullptr ? xs[0][ch] * sw : 0.f;
+            const float s1 = xs[1] != nullptr ? xs[1][ch] * sw : 0.f;
+            acc[0] = fmaf(part[0], s0, acc[0]);
+            acc[1] = fmaf(part[1], s1, acc[1]);
+            acc[2] = fmaf(part[2], s0, acc[2]);
+            acc[3] = fmaf(part[3], s1, acc[3]);
+        }
+        if (AHEAD) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        s_acc[warp][g][8 * b + 2 * c] = acc[b][0];
-        s_acc[warp][g][8 * b + 2 * c + 1] = acc[b][1];
-        s_acc[warp][g + 8][8 * b + 2 * c] = acc[b][2];
-        s_acc[warp][g + 8][8 * b + 2 * c + 1] = acc[b][3];
+            for (int h = 0; h < 2; ++h) a[h][0] = next[h][0], a[h][1] = next[h][1];
+        } else if (ch + k_split < chunks) {
+            load_w(ch + k_split, a);
+        }
     }
+    s_acc[warp][g][2 * c] = acc[0];
+    s_acc[warp][g][2 * c + 1] = acc[1];
+    s_acc[warp][g + 8][2 * c] = acc[2];
+    s_acc[warp][g + 8][2 * c + 1] = acc[3];
     __syncthreads();
     // the K parts of a tile are added in order; neighbouring threads write neighbouring outputs
     const int span = kSWarps / k_split * 16, first = (blockIdx.x - pass * n_tiles) * span;
@@ -202,9 +209,8 @@ rows_stream_kernel(const RowsProduct P, int n_tiles, int k_split) {
     }
 }
 
-template <bool FP8, int NB>
-cudaError_t launch_stream(const RowsProduct& P, cudaStream_t s) {
-    constexpr int rows = 8 * NB;
+template <bool FP8>
+cudaError_t launch_stream(const RowsProduct& P, const DeviceInfo& dev, cudaStream_t s) {
     // warps to a row's K: as many as leave each two chunks, so that short rows share a CTA instead
     const int chunks = (P.K * (FP8 ? 1 : 2) + 127) / 128;
     int k_split = kSWarps;
@@ -212,18 +218,20 @@ cudaError_t launch_stream(const RowsProduct& P, cudaStream_t s) {
     const int span = kSWarps / k_split * 16, n_tiles = (P.N + span - 1) / span;
     // passes at most: every expert has rows, and its last pass one
     const int groups = std::min(P.R, P.E);
-    const long long passes = (P.R - groups) / rows + groups;
+    const long long passes = (P.R - groups) / kRows + groups;
     const long long grid = passes * n_tiles;
     if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-    rows_stream_kernel<FP8, NB><<<(unsigned)grid, kSThreads, 0, s>>>(P, n_tiles, k_split);
+    if (grid <= kAheadCtas * dev.num_sms)
+        rows_stream_kernel<FP8, true><<<(unsigned)grid, kSThreads, 0, s>>>(P, n_tiles, k_split);
+    else
+        rows_stream_kernel<FP8, false><<<(unsigned)grid, kSThreads, 0, s>>>(P, n_tiles, k_split);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_rows_stream(const RowsProduct& P, cudaStream_t s) {
-    if (P.R <= 8) return P.xs != nullptr ? launch_stream<true, 1>(P, s) : launch_stream<false, 1>(P, s);
-    return P.xs != nullptr ? launch_stream<true, 2>(P, s) : launch_stream<false, 2>(P, s);
+cudaError_t launch_rows_stream(const RowsProduct& P, const DeviceInfo& dev, cudaStream_t s) {
+    return P.xs != nullptr ? launch_stream<true>(P, dev, s) : launch_stream<false>(P, dev, s);
 }
 
 }  // namespace nvfp4
