@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -101,11 +102,6 @@ class MoELayerDescC(ctypes.Structure):
                 ("sh_gate_w", _P)]
 
 
-class MoEGroupsC(ctypes.Structure):
-    _fields_ = [("R", _i32), ("E", _i32), ("k", _i32), ("gather", _i32), ("scatter", _i32),
-                ("expert_offsets", _P), ("token_list", _P)]
-
-
 lib = ctypes.CDLL(LIB_PATH)
 lib.nvfp4_pack.restype = _i32
 lib.nvfp4_pack.argtypes = [_P, _i32, _i32, _i32, _P, _P, _P, _P, _sz, _P]
@@ -147,9 +143,9 @@ lib.fp8_quantize_block128.argtypes = [_P, _i32, _i32, _i32, _i32, _P, _P, _P]
 lib.fp8_gemm_block128.restype = _i32
 lib.fp8_gemm_block128.argtypes = [_P, _P, _i32, _P, _P, _i32, _i32, _P, _i32, _P, _sz, _P]
 lib.moe_grouped_gemm_bf16.restype = _i32
-lib.moe_grouped_gemm_bf16.argtypes = [ctypes.POINTER(MoEGroupsC), _P, _P, _i32, _i32, _P, _i32, _P, _sz, _P]
+lib.moe_grouped_gemm_bf16.argtypes = [_P, _P, _P, _i32, _i32, _P, _i32, _P, _sz, _P]
 lib.moe_grouped_gemm_fp8.restype = _i32
-lib.moe_grouped_gemm_fp8.argtypes = [ctypes.POINTER(MoEGroupsC), _P, _P, _P, _P, _i32, _i32, _P, _i32, _P, _sz, _P]
+lib.moe_grouped_gemm_fp8.argtypes = [_P, _P, _P, _P, _P, _i32, _i32, _P, _i32, _P, _sz, _P]
 lib.moe_layer_forward_noalloc.restype = _i32
 lib.moe_layer_forward_noalloc.argtypes = [ctypes.POINTER(MoELayerDescC), _P, _i32, _P, _P, _P, _P]
 lib.nvfp4_noalloc_status.restype = _i32
@@ -292,6 +288,7 @@ def moe_route_topk(logits: torch.Tensor, k: int, stream=None):
 # ---------------------------------------------------------------- 8-bit and grouped products
 
 _OUT_TYPE = {torch.bfloat16: 0, torch.float32: 1}
+_GROUPS = struct.Struct("@5iPP")     # moe_groups; packing it costs half of filling a ctypes structure
 
 
 def _refuse(where: str, why: str, status: int = NVFP4_ERR_INVALID_ARG):
@@ -300,13 +297,13 @@ def _refuse(where: str, why: str, status: int = NVFP4_ERR_INVALID_ARG):
 
 def _first(t: torch.Tensor, dtype, where: str, dims=(2,)):
     """(address, shape, device index) of x, the operand that names the device of a call."""
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.dim() not in dims:
+    shape, index = t.shape, t.get_device()
+    if t.dtype is not dtype or index < 0 or len(shape) not in dims or not t.is_contiguous():
         _refuse(where, "x must be a contiguous CUDA tensor of %s with %s dimensions" % (
             dtype, " or ".join(map(str, dims))))
-    shape = t.shape
     if max(shape) > 0x7FFFFFFF:          # the C ABI takes int32
         _refuse(where, "x has shape %s" % (tuple(shape),), NVFP4_ERR_UNSUPPORTED_SHAPE)
-    return t.data_ptr(), shape, t.get_device()
+    return t.data_ptr(), shape, index
 
 
 def _operand(t: torch.Tensor, dtype, shape, index: int, where: str, name: str):
@@ -401,9 +398,9 @@ def _grouped(where, fn, x, x_scales, w, w_scales, dtype, offsets, token_list, k,
     elif gather or scatter:
         _refuse(where, "gather and scatter need token_list")
     else:
-        pl = None
-    g = MoEGroupsC(R, E, k, 1 if gather else 0, 1 if scatter else 0,
-                   _operand(offsets, torch.int32, (E + 1,), dev, where, "offsets"), pl)
+        pl = 0
+    groups = _GROUPS.pack(R, E, k, 1 if gather else 0, 1 if scatter else 0,
+                          _operand(offsets, torch.int32, (E + 1,), dev, where, "offsets"), pl)
     if y is None:
         y = _output((R, N), out_dtype, x.device, stream)
     if y.dtype not in _OUT_TYPE:
@@ -415,7 +412,7 @@ def _grouped(where, fn, x, x_scales, w, w_scales, dtype, offsets, token_list, k,
         KB = (K + 127) // 128
         operands = (px, _operand(x_scales, torch.float32, (rows, KB), dev, where, "x_scales"), pw,
                     _operand(w_scales, torch.float32, (E, (N + 127) // 128, KB), dev, where, "w_scales"))
-    _enqueue(fn, where, dev, stream, ctypes.byref(g), *operands, N, K, _operand(y, y.dtype, (R, N), dev, where, "y"),
+    _enqueue(fn, where, dev, stream, groups, *operands, N, K, _operand(y, y.dtype, (R, N), dev, where, "y"),
              _OUT_TYPE[y.dtype], None if ws is None else ws.buf.data_ptr(), 0 if ws is None else ws.nbytes)
     return y
 

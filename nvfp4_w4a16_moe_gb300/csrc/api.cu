@@ -1,6 +1,7 @@
 // C ABI of the library (declared in include/nvfp4moe.h): host-side argument
 // checks, workspace carving and dispatch to the sm_103a kernels. Nothing here
 // allocates memory; nothing falls back to another implementation.
+#include <algorithm>
 #include <atomic>
 #include <cstring>
 
@@ -150,7 +151,8 @@ nvfp4_status run_product(RowsProduct P, bool fp8, int32_t y_type, void* workspac
     DeviceInfo dev;
     if (nvfp4_status st = device_info(&dev); st != NVFP4_OK) return st;
     if (P.R == 0) return NVFP4_OK;
-    if (P.R <= kStreamRows) return from_cuda(launch_rows_stream(P, dev, static_cast<cudaStream_t>(stream)));
+    const long long bytes8 = fp8 ? (long long)std::min(P.R, P.E) * P.N * P.K : 0;
+    if (P.R <= kStreamRows && bytes8 <= kStreamBytes8) return from_cuda(launch_rows_stream(P, dev, static_cast<cudaStream_t>(stream)));
     return from_cuda(launch_rows_tc(P, static_cast<WsHeader*>(workspace), dev, g_wait_limit.load(),
                                     static_cast<cudaStream_t>(stream)));
 }

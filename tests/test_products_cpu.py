@@ -56,6 +56,16 @@ def test_ratio_of_bf16_significands_stays_off_the_rounding_points():
     assert nearest >= 2.0 ** -13
 
 
+class Groups(ctypes.Structure):         # moe_groups of the C header
+    _fields_ = [("R", ctypes.c_int32), ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("gather", ctypes.c_int32),
+                ("scatter", ctypes.c_int32), ("expert_offsets", ctypes.c_void_p), ("token_list", ctypes.c_void_p)]
+
+
+def test_python_packs_the_groups_like_c(nv):
+    g = Groups(1, 2, 3, 4, 5, 6, 7)
+    assert bytes(g) == nv._GROUPS.pack(1, 2, 3, 4, 5, 6, 7)
+
+
 FAKE = 0x100000        # never dereferenced: the checks fail first
 
 
@@ -94,8 +104,8 @@ def test_dense_refusals(nv):
 def test_grouped_refusals(nv, fp8):
     def call(R=8, E=4, k=2, gather=0, scatter=0, off=FAKE, lst=FAKE, x=FAKE, w=FAKE, N=16, K=64, y=FAKE, yt=0,
              wk=None, wb=0, xs=FAKE, ws=FAKE, null=False):
-        g = nv.MoEGroupsC(R, E, k, gather, scatter, off, lst)
-        p = None if null else ctypes.byref(g)
+        g = Groups(R, E, k, gather, scatter, off, lst)
+        p = None if null else ctypes.addressof(g)
         if fp8:
             return _status(nv, "moe_grouped_gemm_fp8", p, x, xs, w, ws, N, K, y, yt, wk, wb, None)
         return _status(nv, "moe_grouped_gemm_bf16", p, x, w, N, K, y, yt, wk, wb, None)
