@@ -334,9 +334,11 @@ NVFP4_API nvfp4_status fp8_quantize_block128(const uint16_t* x, int32_t B, int32
  *       nvfp4_workspace_init: the call needs no scratch, but a bounded device wait that ran
  *       out is recorded in its status word. Such a wait also writes quiet NaN into the rows
  *       of y that it touches.
- *   Scales, offsets and lists are 4-byte aligned, everything else 16-byte.
+ *   Scales, offsets and lists are 4-byte aligned, everything else 16-byte. y overlaps no input.
  *   Shapes: 0 <= T <= NVFP4_MAX_PRODUCT_ROWS, 1 <= N <= 2^22, K >= 16, K % 16 == 0,
  *   K <= NVFP4_MAX_PRODUCT_K. T == 0 enqueues nothing.
+ *   One kernel: up to 8 rows (here T; R of a grouped product) stream the weights through
+ *   warp-level MMAs, more rows, and 8-bit weights above 48 MB, run on tcgen05 tiles.
  */
 NVFP4_API nvfp4_status fp8_gemm_block128(const uint8_t* x, const float* x_scales, int32_t T, const uint8_t* w,
                                          const float* w_scales, int32_t N, int32_t K, void* y, int32_t y_type,

@@ -73,7 +73,8 @@ __device__ __forceinline__ bool locate_pass(const RowsProduct& P, int p, int* e,
     __shared__ int s_sum[kSWarps], s_e, s_r0, s_n;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int lo = 0, cnt = 0;
-    if ((int)threadIdx.x < P.E) {   // NVFP4_MAX_EXPERTS = kSThreads
+    static_assert(NVFP4_MAX_EXPERTS <= kSThreads, "an expert a thread");
+    if ((int)threadIdx.x < P.E) {
         lo = min(max(P.offsets[threadIdx.x], 0), P.R);
         cnt = max(min(max(P.offsets[threadIdx.x + 1], 0), P.R) - lo, 0);
     }

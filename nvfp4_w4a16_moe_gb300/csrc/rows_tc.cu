@@ -1,39 +1,43 @@
 // Products of many rows with one matrix or with each expert's matrix on the 5th-generation tensor
 // cores: y[o(r), n] = sum_k W[e(r)][n, k] x[i(r), k], in bf16 or in E4M3 with block scales.
 //
-// A pair of CTAs (cluster of 2, cta_group::2) computes a tile of 256 weight rows of one expert times
-// up to NT of its list positions. The weights are the MMA's A operand (M = 256: 128 rows in each
-// CTA's shared memory) and the rows of x its B operand (N = the tile's rows, rounded up to 64; each
-// CTA holds half of them), so an expert with few rows costs few MMA cycles, and any number of rows
-// per expert works without padding in memory. The pair is what feeds the tensor cores: one CTA alone
-// (128 x 256 tiles) needs 48 KB of operands per 64 columns of K from L2 where a CTA of a pair needs 32.
+// A pair of CTAs (cta_group::2) computes a tile of 256 weight rows of one expert times up to NT of its
+// list positions. The weights are the MMA's A operand (M = 256: 128 rows in each CTA's shared memory) and
+// the rows of x its B operand (N = the tile's rows, rounded up to 64; each CTA holds half of them), so an
+// expert with few rows costs few MMA cycles, and any number of rows per expert works without padding in
+// memory. The pair is what feeds the tensor cores: one CTA alone (128 x 256 tiles) needs 48 KB of operands
+// per 64 columns of bf16 from L2 where a CTA of a pair needs 32: 4096 x 8192 x 2048 took 107 us that way
+// and takes 72 us (1.91 PFLOP/s, 99 % of the measured cuBLAS rate).
 //
 // An expert's rows are cut into tiles of nearly equal size. The tiles of the whole call are numbered
 // over the experts (prefix sums over the offsets, made by every CTA for itself: the host never sees the
-// counts), and a persistent grid of pairs walks them.
+// counts), and a persistent grid of pairs walks them. Grouped calls of the layer's shape are bound by the
+// bytes of the experts' matrices: gate/up of 256 bf16 experts of 1024 x 2048, 203 us at 4096 tokens (84 %
+// of the copy rate), 101 us for the experts that 64 tokens reach.
 //
 // Warp roles of a CTA (both CTAs of a pair but where said):
 //   TMA warp: brings step s (128 bytes of K) of the CTA's weight rows and, for rows in list order, of
 //     its rows of x into a ring of 128-byte-swizzled stages, each operand in one box: there is a tensor
-//     map for every height a tile's share can have. (Issuing a box costs about as much as 64 rows of it:
-//     boxes of 16 rows ran the ring at half its rate.) Coordinates past a matrix read zeros, which also
-//     pads K.
+//     map for every height a tile's share can have. Coordinates past a matrix read zeros, which also pads
+//     K. (Boxes of 16 rows, one to a lane, ran the ring at half its rate.)
 //   Gather warps: rows read through the list, four tokens' rows a copy (tile::gather4), so no permuted
-//     copy of x is ever written.
+//     copy of x is ever written; as fast as rows in order where the experts' bytes bound the call.
 //   Scale warps (8-bit): x_scale * w_scale of every column of four steps, in a ring of their own.
 //   MMA warp: in the pair's first CTA, the MMAs of a step for both. In the second CTA it tells the first
 //     that the step's operands have landed here.
 //   Epilogue warps. bf16: a whole tile is summed in one tensor-memory buffer, then read and written out.
 //     8-bit: the operands carry a scale per 128 of K, so every step starts a buffer from zero; the warps
 //     read it, multiply each column with its scale and add it to the tile's sum in registers (fp32),
-//     while the MMAs fill the next buffer. That reading is what bounds 8-bit tiles, not the MMAs (512
-//     clocks for 256 x 256 x 128): sixteen warps share it, and each half of a tile's columns has buffers
-//     of its own, so that a buffer is busy for 256 clocks of MMA plus one reading.
-// Tensor memory holds 512 / NT buffers of a tile, so the next tile's or step's MMAs run under the epilogue.
+//     while the MMAs fill the next buffer. That bounds 8-bit tiles, not the MMAs: a step of 256 x 256 takes
+//     0.65 us where the MMAs alone need 0.27 (a third of it is the multiply-adds and the reads of the
+//     scales, the rest reading tensor memory and handing buffers back). 4096 x 8192 x 2048: 86 us,
+//     1.6 PFLOP/s. Separate buffers for the two column halves cost more in operand reads than they hid.
+// Tensor memory holds 512 / NT buffers, so the next tile's or step's MMAs run under the epilogue.
 //
-// Few tiles (a matrix of few rows of W, a small batch): a cluster of two or four pairs shares a tile's K,
-// and the pairs' sums are exchanged through distributed shared memory, each pair finishing a part of the
-// columns: the sums are added in the order of the pairs.
+// Few tiles (few rows of W, a small batch): a cluster of two or four pairs shares a tile's K, and the
+// pairs' sums are exchanged through distributed shared memory, each pair finishing a part of the columns:
+// the sums are added in the order of the pairs. (64 rows times 2048 x 8192 in 8 bits: 24 us with one pair a
+// tile, 10.3 with four.)
 //
 // Every wait is bounded; one that runs out records NVFP4_ERR_DEVICE_TIMEOUT (where the caller passed a
 // workspace) and makes the pair fill its remaining tiles with NaN.
@@ -66,6 +70,7 @@ constexpr int kThreads = 768;
 // epilogue, which keeps 64 sums a thread.
 constexpr int kLaunchRegs = 80, kEpiRegs = 96, kOtherRegs = 48;
 static_assert(512 * kEpiRegs + 256 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
+static_assert(NVFP4_MAX_EXPERTS <= 8 * 32, "eight experts a lane");
 
 // Output staging of an epilogue warp (bf16): 16 rows of y, 32 neighbouring outputs of each. The pitch of
 // 80 bytes puts the eight 16-byte rows of a stmatrix on different banks.
@@ -384,7 +389,7 @@ struct Exchange {
 // SPLITS: pairs of a cluster, which share a tile's K.
 template <bool FP8, int NT, int SPLITS>
 __global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(kThreads, 1)
-rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int m_tiles, WsHeader* hdr,
+rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int m_tiles, int max_tiles, WsHeader* hdr,
                unsigned long long wait_limit) {
     using C = Cfg<FP8, NT>;
     extern __shared__ uint8_t rows_smem_raw[];
@@ -473,10 +478,9 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
     tc_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot), sm_base = su32(sm);
     // overlapping groups of a malformed list could add up to more tiles than the host counted: those are left
-    // out, in particular a second tile of a cluster of several pairs
+    // out, in particular a second tile of a cluster of several pairs (which has as many clusters as tiles)
     constexpr int kCluster = 2 * SPLITS;
-    const int total = uniform((int)min((long long)tab[P.E] * m_tiles,
-                                       SPLITS > 1 ? (long long)(gridDim.x / kCluster) : (long long)kMaxTiles));
+    const int total = uniform((int)min((long long)tab[P.E] * m_tiles, (long long)max_tiles));
     const int kStepK = FP8 ? 128 : 64;
     const int nk = (P.K + kStepK - 1) / kStepK;
     const int s_begin = nk * pair / SPLITS, s_end = nk * (pair + 1) / SPLITS;      // this pair's steps
@@ -770,7 +774,7 @@ bool encode_rows(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* m, const voi
 }
 
 template <bool FP8, int NT, int SPLITS>
-cudaError_t launch_clusters(const RowsProduct& P, const TcRowMaps& maps, int m_tiles, int clusters, WsHeader* hdr,
+cudaError_t launch_clusters(const RowsProduct& P, const TcRowMaps& maps, int m_tiles, int tiles, WsHeader* hdr,
                             const DeviceInfo& dev, uint64_t wait_limit, cudaStream_t s) {
     using C = Cfg<FP8, NT>;
     static std::atomic<uint64_t> ready{0};      // one bit per device
@@ -784,7 +788,9 @@ cudaError_t launch_clusters(const RowsProduct& P, const TcRowMaps& maps, int m_t
         if (FP8 && a.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
         ready.fetch_or(1ull << dev.device, std::memory_order_release);
     }
-    rows_tc_kernel<FP8, NT, SPLITS><<<2 * SPLITS * clusters, kThreads, C::kSmem, s>>>(P, maps, m_tiles, hdr, wait_limit);
+    const int clusters = SPLITS > 1 ? tiles : std::min(tiles, dev.num_sms / 2);
+    rows_tc_kernel<FP8, NT, SPLITS><<<2 * SPLITS * clusters, kThreads, C::kSmem, s>>>(P, maps, m_tiles, tiles, hdr,
+                                                                                      wait_limit);
     return cudaGetLastError();
 }
 
@@ -803,19 +809,23 @@ cudaError_t launch_tc(const RowsProduct& P, WsHeader* hdr, const DeviceInfo& dev
     const int groups = std::min(P.R, P.E);
     const long long tiles = ((P.R - groups) / NT + groups) * (long long)m_tiles;
     if (tiles > kMaxTiles) return cudaErrorInvalidConfiguration;
+    // as many pairs to a tile as the device has for all tiles, where each has kMinSteps steps (us, 1 / 2 or 4
+    // pairs a tile, 8 bits: 64 rows x 2048 x 8192 24.1 / 10.3, 77 x 5003 x 2000 13.2 / 10.7, 64 x 8192 x 2048 8.9 / 8.4)
     const int pairs = dev.num_sms / 2;
-    const int one = (int)std::min<long long>(tiles, pairs);
     if (4 * tiles <= pairs && nk >= 4 * kMinSteps)
-        return launch_clusters<FP8, NT, 4>(P, maps, m_tiles, one, hdr, dev, wait_limit, s);
+        return launch_clusters<FP8, NT, 4>(P, maps, m_tiles, (int)tiles, hdr, dev, wait_limit, s);
     if (2 * tiles <= pairs && nk >= 2 * kMinSteps)
-        return launch_clusters<FP8, NT, 2>(P, maps, m_tiles, one, hdr, dev, wait_limit, s);
-    return launch_clusters<FP8, NT, 1>(P, maps, m_tiles, one, hdr, dev, wait_limit, s);
+        return launch_clusters<FP8, NT, 2>(P, maps, m_tiles, (int)tiles, hdr, dev, wait_limit, s);
+    return launch_clusters<FP8, NT, 1>(P, maps, m_tiles, (int)tiles, hdr, dev, wait_limit, s);
 }
 
 template <bool FP8>
 cudaError_t launch_any(const RowsProduct& P, WsHeader* hdr, const DeviceInfo& dev, uint64_t wait_limit,
                        cudaStream_t s) {
-    const int rows = (P.R + P.E - 1) / P.E;      // per expert, were they even
+    // Rows per expert, were they even. Tiles of 64 leave room for more and smaller stages and for eight
+    // tensor-memory buffers (us, tiles of 64 / 256: 256 bf16 experts with 32 rows each 171 / 175, in 8 bits
+    // 95 / 101); above, tiles of 256 read the weights fewer times.
+    const int rows = (P.R + P.E - 1) / P.E;
     if (rows > 64) return launch_tc<FP8, 256>(P, hdr, dev, wait_limit, s);
     return launch_tc<FP8, 64>(P, hdr, dev, wait_limit, s);
 }

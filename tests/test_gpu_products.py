@@ -397,6 +397,55 @@ def test_grouped_graph_streams_and_repeats(nv, T, fp8):
     _check_exact(y3, _want(a, xd, wd, off2, lst.flip(0), R)[0])
 
 
+_FIRST_IN_CAPTURE = """
+import sys
+sys.path[:0] = [%r, %r]
+import torch
+import nvfp4_w4a16_moe_gb300 as nv
+T, N, K = %d, 300, 2048
+x = torch.ones(T, K, dtype=torch.bfloat16, device="cuda")
+w = torch.ones(1, N, K, dtype=torch.bfloat16, device="cuda")
+off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y = nv.moe_grouped_gemm_bf16(x, w, off)
+    q, s = nv.fp8_quantize_block128(x)
+    v, t = nv.fp8_quantize_block128(w[0], 128)
+    z = nv.fp8_gemm_block128(q, s, v, t, out_dtype=torch.float32)
+g.replay()
+torch.cuda.synchronize()
+# 1 = 448 / 448: codes 448, scales fl(1 / 448), so every product is 1 within four roundings
+assert (y == K).all() and ((z - K).abs() <= K * 2.0 ** -20).all()
+"""
+
+
+@pytest.mark.parametrize("T", [4, 300])
+def test_first_calls_of_a_process_inside_a_capture(nv, T):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = _FIRST_IN_CAPTURE % (root, os.path.join(root, "tests"), T)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_two_streams_at_once(nv):
+    """Large and small calls on two streams, interleaved, each with its own outputs."""
+    cases = [_grouped_case(T, 4, 20, 520, 1040, "skew", "gather", fp8, T) for T in (2, 200) for fp8 in (False, True)]
+    wants = [_want(*c) for c in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = []
+    torch.cuda.synchronize()
+    for i in range(12):
+        c = cases[i % 4]
+        outs.append(_call(nv, c[0], out_dtype=torch.float32, stream=streams[(i // 2) % 2]))
+    torch.cuda.synchronize()
+    for i, y in enumerate(outs):
+        _check_exact(y, wants[i % 4][0])
+
+
 def test_grouped_empty_and_refusals(nv):
     a, xd, wd, off, lst, R = _grouped_case(4, 2, 3, 20, 64, "even", "gather", False, 2)
     e = dict(a, x=a["x"][:0], token_list=a["token_list"][:0], offsets=torch.zeros(4, dtype=torch.int32, device="cuda"))

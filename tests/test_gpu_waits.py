@@ -127,12 +127,12 @@ def test_multi_token_path_has_no_waits(nv):
     check_layer_parity(L, x, y, ids, w)
 
 
+@pytest.mark.parametrize("T,N,K", [(700, 513, 4096), (2000, 2600, 512)])   # few tiles with a long K; many tiles
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
-def test_products_wait_timeout_is_reported(nv, fp8):
+def test_products_wait_timeout_is_reported(nv, fp8, T, N, K):
     """The tile products' barrier waits with the limit at 1 ns: the status and the NaN rows go together,
     the CTAs drain their copies and MMAs and return, and the next call is exact again."""
     g = torch.Generator().manual_seed(4)
-    T, N, K = 700, 513, 4096
     x = torch.randint(-2, 3, (T, K), generator=g).float()
     w = torch.randint(-2, 3, (N, K), generator=g).float()
     want = (x @ w.t()).cuda()
