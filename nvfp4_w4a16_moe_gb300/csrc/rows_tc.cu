@@ -200,8 +200,7 @@ __device__ __forceinline__ void tmem_wait16(float (&v)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
                    "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
-                   "+f"(v[15])
-                 :: "memory");
+                   "+f"(v[15]));
 }
 
 // (a.x, a.y) += (v.x, v.y) * (s.x, s.y), each fused and rounded once: the packed fp32 pipe.
@@ -365,20 +364,17 @@ struct Exchange {
         cluster_sync_all();
         cluster_sync_all();
     }
-    // Adds the other pairs' sums to this pair's own chunk at c, in the order of the pairs; false: not its own.
+    // Adds the other pairs' sums, in their order, to this pair's own chunk at c; false: not its own.
     __device__ __forceinline__ bool finish(float (&v)[16], int c, int width, int part, int q) const {
         const int g = (part * width + c) / 16;
         if (g % pairs != pair) return false;
-        float own[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) own[j] = v[j], v[j] = 0.f;
-#pragma unroll
+#pragma unroll 1
         for (int src = 0; src < pairs; ++src) {
+            if (src == pair) continue;
             const float4* from = reinterpret_cast<const float4*>(ring + place(src, q, g, width));
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float4 f = src == pair ? make_float4(own[4 * j], own[4 * j + 1], own[4 * j + 2], own[4 * j + 3])
-                                             : from[32 * j];
+                const float4 f = from[32 * j];
                 v[4 * j] += f.x, v[4 * j + 1] += f.y, v[4 * j + 2] += f.z, v[4 * j + 3] += f.w;
             }
         }
@@ -653,6 +649,7 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
         const int q = warp & 3, part = warp >> 2;          // lanes 32 q .., a quarter of the columns
         uint8_t* stg = sm + C::kOffStg + warp * (kStgRows * kStgPitch);
         const int p = lane & 3;
+        const uint32_t first_acc_empty = map_rank(su32(acc_empty), first_rank);
         int use = 0, grp = 0;      // buffers (8-bit: steps) and groups of scales read so far
         bool ok = true;
 #pragma unroll 1
@@ -661,56 +658,58 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
             const int width = t.mma_n() / 4, c0 = part * width;            // this warp's columns of the tile
             const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + c0;
             const int n0 = t.m0 + rank * kM + 32 * q;                      // first output
-            int out[C::kCols / 16];        // lane j (< 16): row of y of column 16 i + j
-#pragma unroll
-            for (int c = 0; c < C::kCols; c += 16) {
+            // lane j (< 16): row of y of column c0 + c + j
+            auto out_row = [&](int c) {
                 const int col = c0 + c + (lane & 15);
-                out[c / 16] = c < width && col < t.n ? y_row(P, t.r0 + col) : -1;
-            }
+                return c < width && col < t.n ? y_row(P, t.r0 + col) : -1;
+            };
             if constexpr (FP8) {
                 float2 acc[C::kCols / 2];
 #pragma unroll
                 for (int j = 0; j < C::kCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
 #pragma unroll 1
-                for (int s = 0; s < s_end - s_begin && ok; ++s, ++use) {
-                    const int buf = use % C::kBufs, slot = grp & 1;
-                    if (s % kGroup == 0) ok = wait(&sc_full[slot], (grp >> 1) & 1);
-                    if (ok) ok = wait(&acc_full[buf], (use / C::kBufs) & 1);
+                for (int s0 = s_begin; s0 < s_end && ok; s0 += kGroup, ++grp) {
+                    const int slot = grp & 1;
+                    ok = wait(&sc_full[slot], (grp >> 1) & 1);
                     if (!ok) break;
-                    tc_fence_after();
-                    const float* sc = scale_ring + (slot * kGroup + s % kGroup) * NT + c0 + 2 * p;
+                    const float* sc = scale_ring + slot * (kGroup * NT) + c0 + 2 * p;
+#pragma unroll 1
+                    for (int s = s0; s < min(s0 + kGroup, s_end); ++s, ++use, sc += NT) {
+                        const int buf = use % C::kBufs;
+                        ok = wait(&acc_full[buf], (use / C::kBufs) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll
-                    for (int c = 0; c < C::kCols; c += 16) {
-                        if (c >= width || c0 + c >= t.n) break;      // padding is neither read nor written
-                        float v[16];
-                        tmem_ld_frag(lanes + buf * NT + c, v);
-                        tmem_wait16(v);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const float2 f = *reinterpret_cast<const float2*>(sc + c + 8 * j);
+                        for (int c = 0; c < C::kCols; c += 16) {
+                            if (c >= width || c0 + c >= t.n) break;      // padding is neither read nor written
+                            float v[16];
+                            tmem_ld_frag(lanes + buf * NT + c, v);
+                            const float2 f0 = *reinterpret_cast<const float2*>(sc + c);
+                            const float2 f1 = *reinterpret_cast<const float2*>(sc + c + 8);
+                            tmem_wait16(v);
 #pragma unroll
                             for (int h = 0; h < 4; ++h) {
-                                const int k = 8 * (h >> 1) + 4 * j + 2 * (h & 1);
-                                fma2(acc[(c + k) / 2], v[k], v[k + 1], f.x, f.y);
+                                const int k = 8 * (h >> 1) + 2 * (h & 1);
+                                fma2(acc[c / 2 + h], v[k], v[k + 1], f0.x, f0.y);
+                                fma2(acc[c / 2 + 4 + h], v[k + 4], v[k + 5], f1.x, f1.y);
                             }
                         }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_cluster(first_acc_empty + 8 * buf);
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    const bool last = s % kGroup == kGroup - 1 || s == s_end - s_begin - 1;
-                    if (lane == 0) {
-                        arrive_cluster(map_rank(su32(&acc_empty[buf]), first_rank));
-                        if (last) mbar_arrive(&sc_empty[slot]);
-                    }
-                    grp += last;
+                    if (ok && lane == 0) mbar_arrive(&sc_empty[slot]);
                 }
                 const auto sums = [&](int c, float (&v)[16]) {
                     const bool bad = *abort_flag != 0;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        v[2 * j] = bad ? __uint_as_float(0x7FC00000u) : acc[c / 2 + j].x;
-                        v[2 * j + 1] = bad ? __uint_as_float(0x7FC00000u) : acc[c / 2 + j].y;
-                    }
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            const int k = 8 * (h >> 1) + 4 * j + 2 * (h & 1);
+                            v[k] = bad ? __uint_as_float(0x7FC00000u) : acc[c / 2 + 4 * j + h].x;
+                            v[k + 1] = bad ? __uint_as_float(0x7FC00000u) : acc[c / 2 + 4 * j + h].y;
+                        }
                 };
                 if constexpr (SPLITS > 1) exchange.send(sums, t, width, c0, part, q);
 #pragma unroll
@@ -719,7 +718,7 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                     float v[16];
                     sums(c, v);
                     if (SPLITS > 1 && !exchange.finish(v, c, width, part, q)) continue;
-                    store_frag(P, v, out[c / 16], n0, stg);
+                    store_frag(P, v, out_row(c), n0, stg);
                 }
             } else {
                 const int buf = use % C::kBufs;
@@ -741,11 +740,11 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                     float v[16];
                     sums(c, v);
                     if (SPLITS > 1 && !exchange.finish(v, c, width, part, q)) continue;
-                    store_frag(P, v, out[c / 16], n0, stg);
+                    store_frag(P, v, out_row(c), n0, stg);
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (ok && lane == 0) arrive_cluster(map_rank(su32(&acc_empty[buf]), first_rank));
+                if (ok && lane == 0) arrive_cluster(first_acc_empty + 8 * buf);
                 ++use;
             }
         }
