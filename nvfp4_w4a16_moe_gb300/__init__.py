@@ -287,7 +287,11 @@ def moe_route_topk(logits: torch.Tensor, k: int, stream=None):
 
 # ---------------------------------------------------------------- 8-bit and grouped products
 
-_OUT_TYPE = {torch.bfloat16: 0, torch.float32: 1}
+# names looked up once: a call spends as long on attributes of torch as on its launch otherwise
+_BF16, _F32, _F8, _I32 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream      # torch.cuda.current_stream builds an object: 2 us
+_OUT_TYPE = {_BF16: 0, _F32: 1}
 _GROUPS = struct.Struct("@5iPP")     # moe_groups; packing it costs half of filling a ctypes structure
 
 
@@ -322,15 +326,24 @@ def _output(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _status_word(ws: Optional[Workspace], index: int, where: str):
+    """(address, bytes) of the optional workspace, which has to be on the call's device."""
+    if ws is None:
+        return None, 0
+    if ws.buf.get_device() != index:
+        _refuse(where, "the workspace is on %s, x on cuda:%d" % (ws.buf.device, index))
+    return ws.buf.data_ptr(), ws.nbytes
+
+
 def _enqueue(fn, where: str, index: int, stream, *args):
     """Call a library entry point with device ``index`` current, on ``stream`` or the device's current one."""
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(index)     # torch.cuda.current_stream builds an object: 2 us
+        raw = _raw_stream(index)
     elif stream.device.index != index:
         _refuse(where, "the stream is on %s, x on cuda:%d" % (stream.device, index))
     else:
         raw = stream.cuda_stream
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = fn(*args, raw)
     else:
         with torch.cuda.device(index):
@@ -346,17 +359,17 @@ def fp8_quantize_block128(x: torch.Tensor, block_rows: int = 1, q: Optional[torc
     where = "fp8_quantize_block128"
     if block_rows != 1 and block_rows != 128:
         _refuse(where, "block_rows must be 1 or 128")
-    px, shape, dev = _first(x, torch.bfloat16, where, (2, 3))
+    px, shape, dev = _first(x, _BF16, where, (2, 3))
     R, K = shape[-2:]
     B = shape[0] if len(shape) == 3 else 1
     sshape = (*shape[:-2], R if block_rows == 1 else (R + 127) // 128, (K + 127) // 128)
     if q is None:
-        q = _output(shape, torch.float8_e4m3fn, x.device, stream)
+        q = _output(shape, _F8, x.device, stream)
     if scales is None:
-        scales = _output(sshape, torch.float32, x.device, stream)
+        scales = _output(sshape, _F32, x.device, stream)
     _enqueue(lib.fp8_quantize_block128, where, dev, stream, px, B, R, K, block_rows,
-             _operand(q, torch.float8_e4m3fn, shape, dev, where, "q"),
-             _operand(scales, torch.float32, sshape, dev, where, "scales"))
+             _operand(q, _F8, shape, dev, where, "q"),
+             _operand(scales, _F32, sshape, dev, where, "scales"))
     return q, scales
 
 
@@ -367,18 +380,18 @@ def fp8_gemm_block128(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, 
     ``fp8_quantize_block128``: x_scales [T, ceil(K/128)], w_scales [ceil(N/128), ceil(K/128)].
     ``ws`` (optional) receives a device wait that ran out in its status word."""
     where = "fp8_gemm_block128"
-    px, (T, K), dev = _first(x, torch.float8_e4m3fn, where)
+    px, (T, K), dev = _first(x, _F8, where)
     N, KB = w.shape[0], (K + 127) // 128
     if y is None:
         y = _output((T, N), out_dtype, x.device, stream)
     if y.dtype not in _OUT_TYPE:
         _refuse(where, "the output is bfloat16 or float32, not %s" % y.dtype)
     _enqueue(lib.fp8_gemm_block128, where, dev, stream, px,
-             _operand(x_scales, torch.float32, (T, KB), dev, where, "x_scales"), T,
-             _operand(w, torch.float8_e4m3fn, (N, K), dev, where, "w"),
-             _operand(w_scales, torch.float32, ((N + 127) // 128, KB), dev, where, "w_scales"), N, K,
+             _operand(x_scales, _F32, (T, KB), dev, where, "x_scales"), T,
+             _operand(w, _F8, (N, K), dev, where, "w"),
+             _operand(w_scales, _F32, ((N + 127) // 128, KB), dev, where, "w_scales"), N, K,
              _operand(y, y.dtype, (T, N), dev, where, "y"), _OUT_TYPE[y.dtype],
-             None if ws is None else ws.buf.data_ptr(), 0 if ws is None else ws.nbytes)
+             *_status_word(ws, dev, where))
     return y
 
 
@@ -394,13 +407,13 @@ def _grouped(where, fn, x, x_scales, w, w_scales, dtype, offsets, token_list, k,
     if R > 0x7FFFFFFF or k > 0x7FFFFFFF:
         _refuse(where, "%d list positions" % R, NVFP4_ERR_UNSUPPORTED_SHAPE)
     if token_list is not None:
-        pl = _operand(token_list, torch.int32, (R,), dev, where, "token_list")
+        pl = _operand(token_list, _I32, (R,), dev, where, "token_list")
     elif gather or scatter:
         _refuse(where, "gather and scatter need token_list")
     else:
         pl = 0
     groups = _GROUPS.pack(R, E, k, 1 if gather else 0, 1 if scatter else 0,
-                          _operand(offsets, torch.int32, (E + 1,), dev, where, "offsets"), pl)
+                          _operand(offsets, _I32, (E + 1,), dev, where, "offsets"), pl)
     if y is None:
         y = _output((R, N), out_dtype, x.device, stream)
     if y.dtype not in _OUT_TYPE:
@@ -410,10 +423,10 @@ def _grouped(where, fn, x, x_scales, w, w_scales, dtype, offsets, token_list, k,
         operands = (px, pw)
     else:
         KB = (K + 127) // 128
-        operands = (px, _operand(x_scales, torch.float32, (rows, KB), dev, where, "x_scales"), pw,
-                    _operand(w_scales, torch.float32, (E, (N + 127) // 128, KB), dev, where, "w_scales"))
+        operands = (px, _operand(x_scales, _F32, (rows, KB), dev, where, "x_scales"), pw,
+                    _operand(w_scales, _F32, (E, (N + 127) // 128, KB), dev, where, "w_scales"))
     _enqueue(fn, where, dev, stream, groups, *operands, N, K, _operand(y, y.dtype, (R, N), dev, where, "y"),
-             _OUT_TYPE[y.dtype], None if ws is None else ws.buf.data_ptr(), 0 if ws is None else ws.nbytes)
+             _OUT_TYPE[y.dtype], *_status_word(ws, dev, where))
     return y
 
 
@@ -436,7 +449,7 @@ def moe_grouped_gemm_fp8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tenso
                          out_dtype=torch.bfloat16, ws: Optional[Workspace] = None, stream=None):
     """``moe_grouped_gemm_bf16`` with E4M3 x and w [E, N, K] and their block scales: x_scales
     [rows of x, ceil(K/128)], w_scales [E, ceil(N/128), ceil(K/128)]."""
-    return _grouped("moe_grouped_gemm_fp8", lib.moe_grouped_gemm_fp8, x, x_scales, w, w_scales, torch.float8_e4m3fn,
+    return _grouped("moe_grouped_gemm_fp8", lib.moe_grouped_gemm_fp8, x, x_scales, w, w_scales, _F8,
                     offsets, token_list, k, gather, scatter, y, out_dtype, ws, stream)
 
 

@@ -29,9 +29,10 @@
 //     8-bit: the operands carry a scale per 128 of K, so every step starts a buffer from zero; the warps
 //     read it, multiply each column with its scale and add it to the tile's sum in registers (fp32),
 //     while the MMAs fill the next buffer. That bounds 8-bit tiles, not the MMAs: a step of 256 x 256 takes
-//     0.65 us where the MMAs alone need 0.27 (a third of it is the multiply-adds and the reads of the
-//     scales, the rest reading tensor memory and handing buffers back). 4096 x 8192 x 2048: 86 us,
-//     1.6 PFLOP/s. Separate buffers for the two column halves cost more in operand reads than they hid.
+//     0.58 us where the MMAs alone need 0.27 (over a quarter of it are the multiply-adds; sixteen warps
+//     issue half of their scheduler's slots, eight warps with twice the sums each took 0.82 us). 4096 x 8192
+//     x 2048: 80 us, 1.7 PFLOP/s; gate/up of 4096 tokens over 256 experts of 1024 x 2048: 144 us. Separate
+//     buffers for the two column halves cost more in operand reads than they hid.
 // Tensor memory holds 512 / NT buffers, so the next tile's or step's MMAs run under the epilogue.
 //
 // Few tiles (few rows of W, a small batch): a cluster of two or four pairs shares a tile's K, and the
@@ -664,6 +665,7 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                 return c < width && col < t.n ? y_row(P, t.r0 + col) : -1;
             };
             if constexpr (FP8) {
+                const int cols = uniform(min(width, t.n - c0));
                 float2 acc[C::kCols / 2];
 #pragma unroll
                 for (int j = 0; j < C::kCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
@@ -681,7 +683,7 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                         tc_fence_after();
 #pragma unroll
                         for (int c = 0; c < C::kCols; c += 16) {
-                            if (c >= width || c0 + c >= t.n) break;      // padding is neither read nor written
+                            if (c >= cols) break;                       // padding is neither read nor written
                             float v[16];
                             tmem_ld_frag(lanes + buf * NT + c, v);
                             const float2 f0 = *reinterpret_cast<const float2*>(sc + c);
@@ -696,7 +698,7 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                         }
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) arrive_cluster(first_acc_empty + 8 * buf);
+                        if (elect_one()) arrive_cluster(first_acc_empty + 8 * buf);
                     }
                     if (ok && lane == 0) mbar_arrive(&sc_empty[slot]);
                 }
