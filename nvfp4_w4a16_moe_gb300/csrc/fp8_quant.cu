@@ -167,19 +167,21 @@ cudaError_t launch_fp8_quantize(const uint16_t* x, int B, int R, int K, int bloc
     const int KB = (K + 127) / 128;
     if (block_rows == 1) {
         const size_t blocks = (size_t)B * R * KB;
-        auto run = [&](auto unroll) {
+        auto run = [&](auto unroll) -> cudaError_t {
             constexpr int kUnroll = decltype(unroll)::value;
             const size_t per = (kQThreads / 32) * 2 * kUnroll;
+            if ((blocks + per - 1) / per > 0x7FFFFFFFu) return cudaErrorInvalidConfiguration;
             const unsigned grid = (unsigned)((blocks + per - 1) / per);
             if (K % 128 == 0)
                 quantize_rows_kernel<kUnroll, true><<<grid, kQThreads, 0, s>>>(x, blocks, K, KB, q, scales);
             else
                 quantize_rows_kernel<kUnroll, false><<<grid, kQThreads, 0, s>>>(x, blocks, K, KB, q, scales);
+            return cudaGetLastError();
         };
-        if (blocks < kFewBlocks) run(std::integral_constant<int, 1>{});
-        else run(std::integral_constant<int, 4>{});
+        return blocks < kFewBlocks ? run(std::integral_constant<int, 1>{}) : run(std::integral_constant<int, 4>{});
     } else {
         const int RB = (R + 127) / 128;
+        if ((size_t)B * RB * KB > 0x7FFFFFFFu) return cudaErrorInvalidConfiguration;
         quantize_tiles_kernel<<<(unsigned)((size_t)B * RB * KB), kQThreads, 0, s>>>(x, R, K, RB, KB, q, scales);
     }
     return cudaGetLastError();

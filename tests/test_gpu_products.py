@@ -41,7 +41,7 @@ def _check_exact(y, want, what=""):
 # ---------------------------------------------------------------- quantiser
 
 @pytest.mark.parametrize("B,R,K", [(1, 1, 16), (1, 1, 128), (1, 3, 144), (1, 129, 2048), (2, 130, 272), (3, 1, 1040),
-                                   (1, 1000, 64)])
+                                   (1, 1000, 64), (1, 1100, 2048), (2, 1050, 1040)])
 @pytest.mark.parametrize("block_rows", [1, 128])
 def test_quantize(nv, B, R, K, block_rows):
     g = _gen(R * K + block_rows)
@@ -92,9 +92,9 @@ def test_quantize_extremes(nv):
     x[0, 6, :3] = torch.tensor([float("nan"), float("-inf"), 3.0])
     x[0, 7] = 5.0
     x = x.to(torch.bfloat16)
-    for br in (1, 128):
-        q, s = nv.fp8_quantize_block128(x.cuda(), br)
-        qw, sw = ref.quantize(x, br)
+    for br, times in ((1, 1), (1, 2500), (128, 1), (128, 40)):      # few blocks and many
+        q, s = nv.fp8_quantize_block128(x.repeat(times, 1, 1).cuda(), br)
+        qw, sw = (np.repeat(v, times, axis=0) for v in ref.quantize(x, br))
         assert np.array_equal(s.cpu().numpy(), sw, equal_nan=True)
         got = q.cpu().view(torch.uint8).numpy()
         nan = (qw & 0x7F) == 0x7F
@@ -455,6 +455,70 @@ def test_grouped_empty_and_refusals(nv):
                dict(out_dtype=torch.float16), dict(x=a["x"][:, :32])):
         with pytest.raises(nv.NVFP4Error):
             _call(nv, dict(a, **kw))
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("rows", ["gather", "scatter", "list"])
+@pytest.mark.parametrize("T", [2, 90])
+def test_grouped_neighbours_do_not_leak(nv, T, rows, fp8):
+    """Tiles reach past an expert's weight rows and list positions: NaN in the matrices of experts without
+    rows, and in rows of x that no position reads, stays there."""
+    E, N, K = 9, 130, 272
+    a, xd, wd, off, lst, R = _grouped_case(T, 4, E, N, K, "holes", rows, fp8, 44)
+    off = off.clone()
+    last = int(off[-1]) - 3                      # the last three positions belong to no expert
+    off = torch.minimum(off, torch.tensor(last, dtype=torch.int32))
+    a["offsets"] = off.cuda()
+    bits = lambda t: t.view(torch.uint8 if fp8 else torch.int16)
+    nan = 0x7F if fp8 else 0x7FC0
+    empty = (off[1:] == off[:-1]).nonzero().flatten()
+    bits(a["w"])[empty.cuda()] = nan
+    if rows == "gather":
+        used = {int(e) // 4 for e in lst[:last]}
+    else:
+        used = set(range(last))
+    idle = [r for r in range(a["x"].shape[0]) if r not in used]
+    if idle:
+        bits(a["x"])[torch.tensor(idle).cuda()] = nan
+    want, _, written = _want(a, np.nan_to_num(xd), wd, off, lst, R)
+    y = torch.full((R, N), -77.0, device="cuda")
+    _call(nv, a, y=y)
+    want[~written] = -77.0
+    _check_exact(y, want)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_grouped_outputs_and_weights_past_32_bits(nv, fp8):
+    """2.3e9 outputs, and 2^33 weight elements: the last rows and the last expert are where they should be."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    dt = F8 if fp8 else torch.bfloat16
+
+    def small(*shape):
+        return torch.randint(-2, 3, shape, generator=g, device="cuda", dtype=torch.int8).to(torch.bfloat16).to(dt)
+
+    def check(x, w, off, rows, R, N):
+        kw = {}
+        if fp8:
+            kw = dict(x_scales=torch.ones(x.shape[0], -(-x.shape[1] // 128), device="cuda"),
+                      w_scales=torch.ones(w.shape[0], -(-N // 128), -(-x.shape[1] // 128), device="cuda"))
+        y = _call(nv, dict(x=x, w=w, offsets=off, **kw))
+        for r in rows:
+            e = int((off[1:] <= r).sum())
+            want = (w[e].float() @ x[r].float()).to(torch.bfloat16)
+            assert torch.equal(y[r], want), r
+
+    R, N, K = 280000, 8200, 64
+    off = torch.tensor([0, 100, R], dtype=torch.int32, device="cuda")
+    check(small(R, K), small(2, N, K), off, (0, 99, 100, 262143, R - 1), R, N)
+    E, N, K = 128, 8192, 8192
+    w = torch.empty(E, N, K, dtype=dt, device="cuda")
+    for e in range(E):
+        w[e] = small(N, K)
+    for R in (4, 70):
+        off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+        off[1:] = R // 2
+        off[-1] = R
+        check(small(R, K), w, off, (0, R // 2 - 1, R // 2, R - 1), R, N)
 
 
 # ---------------------------------------------------------------- together
