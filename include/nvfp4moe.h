@@ -337,6 +337,8 @@ NVFP4_API nvfp4_status fp8_quantize_block128(const uint16_t* x, int32_t B, int32
  *   Scales, offsets and lists are 4-byte aligned, everything else 16-byte. y overlaps no input.
  *   Shapes: 0 <= T <= NVFP4_MAX_PRODUCT_ROWS, 1 <= N <= 2^22, K >= 16, K % 16 == 0,
  *   K <= NVFP4_MAX_PRODUCT_K. T == 0 enqueues nothing.
+ *   Launched with programmatic stream serialisation; it waits for the kernel before it on the
+ *   stream before it reads or writes anything (so do the quantiser and the grouped products).
  *   One kernel: up to 8 rows (here T; R of a grouped product) stream the weights through
  *   warp-level MMAs, more rows, and 8-bit weights above 48 MB, run on tcgen05 tiles.
  */

@@ -86,6 +86,7 @@ __device__ __forceinline__ uint2 quantize8(const uint4 v, uint32_t amax_bits, fl
 template <int kUnroll, bool WHOLE>
 __global__ void __launch_bounds__(kQThreads)
 quantize_rows_kernel(const uint16_t* x, size_t blocks, int K, unsigned KB, uint8_t* q, float* scales) {
+    pdl_wait_then_trigger();
     const int lane = threadIdx.x & 31, unit = lane & 15, half = lane >> 4;
     const size_t warp = (size_t)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
     const size_t first = warp * (2 * kUnroll) + half;
@@ -131,6 +132,7 @@ __global__ void __launch_bounds__(kQThreads)
 quantize_tiles_kernel(const uint16_t* x, int R, int K, int RB, int KB, uint8_t* q,
                       float* scales) {
     __shared__ uint32_t s_max[kQThreads / 32];
+    pdl_wait_then_trigger();
     const size_t blk = blockIdx.x;
     const size_t mat = blk / ((size_t)RB * KB);
     const int in = (int)(blk - mat * ((size_t)RB * KB));
@@ -173,16 +175,14 @@ cudaError_t launch_fp8_quantize(const uint16_t* x, int B, int R, int K, int bloc
             if ((blocks + per - 1) / per > 0x7FFFFFFFu) return cudaErrorInvalidConfiguration;
             const unsigned grid = (unsigned)((blocks + per - 1) / per);
             if (K % 128 == 0)
-                quantize_rows_kernel<kUnroll, true><<<grid, kQThreads, 0, s>>>(x, blocks, K, KB, q, scales);
-            else
-                quantize_rows_kernel<kUnroll, false><<<grid, kQThreads, 0, s>>>(x, blocks, K, KB, q, scales);
-            return cudaGetLastError();
+                return launch_pdl(quantize_rows_kernel<kUnroll, true>, grid, kQThreads, 0, s, x, blocks, K, KB, q, scales);
+            return launch_pdl(quantize_rows_kernel<kUnroll, false>, grid, kQThreads, 0, s, x, blocks, K, KB, q, scales);
         };
         return blocks < kFewBlocks ? run(std::integral_constant<int, 1>{}) : run(std::integral_constant<int, 4>{});
     } else {
         const int RB = (R + 127) / 128;
         if ((size_t)B * RB * KB > 0x7FFFFFFFu) return cudaErrorInvalidConfiguration;
-        quantize_tiles_kernel<<<(unsigned)((size_t)B * RB * KB), kQThreads, 0, s>>>(x, R, K, RB, KB, q, scales);
+        return launch_pdl(quantize_tiles_kernel, (unsigned)((size_t)B * RB * KB), kQThreads, 0, s, x, R, K, RB, KB, q, scales);
     }
     return cudaGetLastError();
 }

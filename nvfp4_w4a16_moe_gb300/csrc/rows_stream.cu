@@ -108,6 +108,7 @@ template <bool FP8, bool AHEAD>
 __global__ void __launch_bounds__(kSThreads, AHEAD ? kAheadCtas : kAheadCtas + 1)
 rows_stream_kernel(const RowsProduct P, int n_tiles, int k_split) {
     __shared__ float s_acc[kSWarps][16][kRows + 1];
+    pdl_wait_then_trigger();
     // row tiles of this CTA: one for every k_split warps
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int k_part = warp & (k_split - 1), n_part = warp / k_split;
@@ -223,10 +224,8 @@ cudaError_t launch_stream(const RowsProduct& P, const DeviceInfo& dev, cudaStrea
     const long long grid = passes * n_tiles;
     if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
     if (grid <= kAheadCtas * dev.num_sms)
-        rows_stream_kernel<FP8, true><<<(unsigned)grid, kSThreads, 0, s>>>(P, n_tiles, k_split);
-    else
-        rows_stream_kernel<FP8, false><<<(unsigned)grid, kSThreads, 0, s>>>(P, n_tiles, k_split);
-    return cudaGetLastError();
+        return launch_pdl(rows_stream_kernel<FP8, true>, (unsigned)grid, kSThreads, 0, s, P, n_tiles, k_split);
+    return launch_pdl(rows_stream_kernel<FP8, false>, (unsigned)grid, kSThreads, 0, s, P, n_tiles, k_split);
 }
 
 }  // namespace

@@ -434,6 +434,7 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    pdl_wait_then_trigger();       // barriers and tensor memory are set up under the kernel before
     if (warp == 0) {
         // tiles of every expert: eight experts a lane, then a prefix sum over the lanes
         int cnt[8], sum = 0;
@@ -790,9 +791,8 @@ cudaError_t launch_clusters(const RowsProduct& P, const TcRowMaps& maps, int m_t
         ready.fetch_or(1ull << dev.device, std::memory_order_release);
     }
     const int clusters = SPLITS > 1 ? tiles : std::min(tiles, dev.num_sms / 2);
-    rows_tc_kernel<FP8, NT, SPLITS><<<2 * SPLITS * clusters, kThreads, C::kSmem, s>>>(P, maps, m_tiles, tiles, hdr,
-                                                                                      wait_limit);
-    return cudaGetLastError();
+    return launch_pdl(rows_tc_kernel<FP8, NT, SPLITS>, 2 * SPLITS * clusters, kThreads, C::kSmem, s, P, maps, m_tiles,
+                      tiles, hdr, (unsigned long long)wait_limit);
 }
 
 template <bool FP8, int NT>

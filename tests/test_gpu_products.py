@@ -521,6 +521,87 @@ def test_grouped_outputs_and_weights_past_32_bits(nv, fp8):
         check(small(R, K), w, off, (0, R // 2 - 1, R // 2, R - 1), R, N)
 
 
+def _run_twice(step, n):
+    """The outputs of n steps in a row, and of the same steps with the device idle between all calls."""
+    outs = []
+    for wait in (False, True):
+        torch.cuda.synchronize()
+        outs.append([[o.clone() for o in step(i, torch.cuda.synchronize if wait else (lambda: None))] for i in range(n)])
+    torch.cuda.synchronize()
+    return outs
+
+
+def test_chains_over_reused_buffers(nv):
+    """Quantise, multiply, round, quantise again in the same buffers, few and many rows in turn: a call that
+    started before the one ahead of it was done, or read a stale line, would differ from the slow run."""
+    g = _gen(8)
+    E, N = 4, 512
+    w = (torch.randn(E, N, N, generator=g) * 0.06).to(torch.bfloat16).cuda()
+    wq, ws = nv.fp8_quantize_block128(w, 128)
+    xs = [torch.randn(r, N, generator=g).to(torch.bfloat16).cuda() for r in (6, 700)]
+    offs = [torch.tensor([0, r // 4, r // 2, r // 2, r], dtype=torch.int32, device="cuda") for r in (6, 700)]
+    bufs = [(torch.empty_like(x), torch.empty(x.shape, dtype=F8, device="cuda"),
+             torch.empty(x.shape[0], N // 128, device="cuda")) for x in xs]
+
+    def step(i, wait):
+        b = i % 2
+        (y, q, s), off = bufs[b], offs[b]
+        y.copy_(xs[b] * (1 + i % 3))
+        for _ in range(4):
+            wait()
+            nv.fp8_quantize_block128(y, q=q, scales=s)
+            wait()
+            nv.moe_grouped_gemm_fp8(q, s, wq, ws, off, y=y)
+            wait()
+            nv.fp8_quantize_block128(y, q=q, scales=s)
+            wait()
+            nv.fp8_gemm_block128(q, s, wq[1], ws[1], y=y)
+        wait()
+        return y, q.view(torch.uint8), s
+
+    fast, slow = _run_twice(step, 30)
+    for a, b in zip(fast, slow):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_chains_with_the_nvfp4_kernels(nv):
+    """The NVFP4 packer, GEMV and single-token layer read weights before they wait for the kernel ahead of
+    them: with the new kernels in between, freshly written weights and workspaces are still seen."""
+    import workload as wl
+    from harness import gpu_layer
+    layer = gpu_layer(wl.LayerInputs(wl.SMALL256, seed=3))
+    H = wl.SMALL256.H
+    g = _gen(12)
+    masters = [torch.randn(512, H, generator=g).cuda() * 0.1 for _ in range(3)]
+    x = torch.randn(1, H, generator=g).to(torch.bfloat16).cuda()
+    w = (torch.randn(1, H, H, generator=g) * 0.1).to(torch.bfloat16).cuda()
+    off = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    W = nv.nvfp4_pack(masters[0])
+    wk = nv.Workspace(nv.moe_layer_workspace_size(layer, 1))
+    q, s = nv.fp8_quantize_block128(x)
+
+    def step(i, wait):
+        wait()
+        nv.nvfp4_pack(masters[i % 3], out=W)
+        wait()
+        nv.fp8_quantize_block128(x, q=q, scales=s)
+        wait()
+        a = nv.nvfp4_gemv_w4a16(W, x)
+        wait()
+        b = nv.moe_layer_forward(layer, x, ws=wk)
+        wait()
+        c = nv.moe_grouped_gemm_bf16(b, w, off)
+        wait()
+        d = nv.moe_layer_forward(layer, c, ws=wk)
+        wait()
+        return a, b, c, d
+
+    fast, slow = _run_twice(step, 40)
+    assert wk.status() == nv.NVFP4_OK
+    for a, b in zip(fast, slow):
+        assert all(torch.equal(p.view(torch.int16), r.view(torch.int16)) for p, r in zip(a, b))
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
