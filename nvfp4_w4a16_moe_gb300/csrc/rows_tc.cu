@@ -31,14 +31,14 @@
 //     while the MMAs fill the next buffer. That bounds 8-bit tiles, not the MMAs: a step of 256 x 256 takes
 //     0.58 us where the MMAs alone need 0.27 (over a quarter of it are the multiply-adds; sixteen warps
 //     issue half of their scheduler's slots, eight warps with twice the sums each took 0.82 us). 4096 x 8192
-//     x 2048: 80 us, 1.7 PFLOP/s; gate/up of 4096 tokens over 256 experts of 1024 x 2048: 144 us. Separate
+//     x 2048: 80 us, 1.7 PFLOP/s; gate/up of 4096 tokens over 256 experts of 1024 x 2048: 135 us. Separate
 //     buffers for the two column halves cost more in operand reads than they hid.
 // Tensor memory holds 512 / NT buffers, so the next tile's or step's MMAs run under the epilogue.
 //
 // Few tiles (few rows of W, a small batch): a cluster of two or four pairs shares a tile's K, and the
 // pairs' sums are exchanged through distributed shared memory, each pair finishing a part of the columns:
 // the sums are added in the order of the pairs. (64 rows times 2048 x 8192 in 8 bits: 24 us with one pair a
-// tile, 10.3 with four.)
+// tile, 9.4 with four.)
 //
 // Every wait is bounded; one that runs out records NVFP4_ERR_DEVICE_TIMEOUT (where the caller passed a
 // workspace) and makes the pair fill its remaining tiles with NaN.
@@ -775,28 +775,85 @@ bool encode_rows(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* m, const voi
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Sets the kernel up on the current device, once, and says how many of its clusters run there at a time
+// (clusters of eight CTAs do not fill every GPC).
 template <bool FP8, int NT, int SPLITS>
-cudaError_t launch_clusters(const RowsProduct& P, const TcRowMaps& maps, int m_tiles, int tiles, WsHeader* hdr,
-                            const DeviceInfo& dev, uint64_t wait_limit, cudaStream_t s) {
+cudaError_t resident_clusters(const DeviceInfo& dev, int* clusters) {
     using C = Cfg<FP8, NT>;
-    static std::atomic<uint64_t> ready{0};      // one bit per device
-    if (!(ready.load(std::memory_order_acquire) >> dev.device & 1)) {
-        cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<FP8, NT, SPLITS>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static std::atomic<int> known[64];           // by device: one more than the clusters
+    int n = known[dev.device].load(std::memory_order_acquire) - 1;
+    if (n < 0) {
+        const auto kernel = rows_tc_kernel<FP8, NT, SPLITS>;
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (e != cudaSuccess) return e;
         // the register split waits forever for registers that the launch did not bring
         cudaFuncAttributes a;
-        if ((e = cudaFuncGetAttributes(&a, rows_tc_kernel<FP8, NT, SPLITS>)) != cudaSuccess) return e;
+        if ((e = cudaFuncGetAttributes(&a, kernel)) != cudaSuccess) return e;
         if (FP8 && a.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-        ready.fetch_or(1ull << dev.device, std::memory_order_release);
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2 * SPLITS;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(2 * SPLITS * dev.num_sms);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = C::kSmem;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess) return e;
+        known[dev.device].store(n + 1, std::memory_order_release);
     }
-    const int clusters = SPLITS > 1 ? tiles : std::min(tiles, dev.num_sms / 2);
-    return launch_pdl(rows_tc_kernel<FP8, NT, SPLITS>, 2 * SPLITS * clusters, kThreads, C::kSmem, s, P, maps, m_tiles,
-                      tiles, hdr, (unsigned long long)wait_limit);
+    *clusters = n;
+    return cudaSuccess;
+}
+
+// How a product runs: columns of a tile, pairs to a tile, tiles at most, and an estimate of its time.
+struct Plan {
+    int nt, splits;
+    long long tiles;
+    float us;
+};
+
+// Tiles of NT columns. The estimate takes the rows to be even over the experts; its figures (us) are fitted to
+// calls of one to three rounds of tiles: a step of N columns 0.08 + 0.00195 N in 8 bits, 0.05 + 0.0007 N in bf16;
+// 2 to write a tile out, 0.5 + 0.009 N to exchange its sums.
+template <bool FP8, int NT>
+cudaError_t plan_tiles(const RowsProduct& P, const DeviceInfo& dev, Plan* best) {
+    const int m_tiles = (P.N + 2 * kM - 1) / (2 * kM), nk = (P.K * (FP8 ? 1 : 2) + kStepBytes - 1) / kStepBytes;
+    const int groups = std::min(P.R, P.E), rows = (P.R + groups - 1) / groups;
+    Plan p;
+    p.nt = NT;
+    // tiles at most: every expert has rows, and its last tile one
+    p.tiles = ((P.R - groups) / NT + groups) * (long long)m_tiles;
+    // as many pairs to a tile as the device runs at a time, where each has kMinSteps steps (us, 1 / 2 or 4 pairs a
+    // tile, 8 bits: 64 rows x 2048 x 8192 24.1 / 9.8, 77 x 5003 x 2000 13.2 / 10.7, 64 x 8192 x 2048 8.9 / 8.4)
+    int c2 = 0, c4 = 0;
+    if (nk >= 2 * kMinSteps && 2 * p.tiles <= dev.num_sms / 2)
+        if (cudaError_t e = resident_clusters<FP8, NT, 2>(dev, &c2); e != cudaSuccess) return e;
+    if (nk >= 4 * kMinSteps && 4 * p.tiles <= dev.num_sms / 2)
+        if (cudaError_t e = resident_clusters<FP8, NT, 4>(dev, &c4); e != cudaSuccess) return e;
+    p.splits = p.tiles <= c4 ? 4 : p.tiles <= c2 ? 2 : 1;
+    const int parts = (rows + NT - 1) / NT, n = ((rows + parts - 1) / parts + kNRound - 1) / kNRound * kNRound;
+    const long long even = (long long)groups * parts * m_tiles, rounds = (even + dev.num_sms / 2 - 1) / (dev.num_sms / 2);
+    const float step = FP8 ? 0.08f + 0.00195f * n : 0.05f + 0.0007f * n;
+    p.us = rounds * ((nk + p.splits - 1) / p.splits * step + 2.0f + (p.splits > 1 ? 0.5f + 0.009f * n : 0.0f));
+    if (p.us < best->us) *best = p;
+    return cudaSuccess;
+}
+
+template <bool FP8, int NT, int SPLITS>
+cudaError_t launch_clusters(const RowsProduct& P, const TcRowMaps& maps, int tiles, WsHeader* hdr,
+                            const DeviceInfo& dev, uint64_t wait_limit, cudaStream_t s) {
+    int resident = 0;
+    if (cudaError_t e = resident_clusters<FP8, NT, SPLITS>(dev, &resident); e != cudaSuccess) return e;
+    if (resident < 1) return cudaErrorInvalidConfiguration;
+    const int clusters = SPLITS > 1 ? tiles : std::min(tiles, resident), m_tiles = (P.N + 2 * kM - 1) / (2 * kM);
+    return launch_pdl(rows_tc_kernel<FP8, NT, SPLITS>, 2 * SPLITS * clusters, kThreads, Cfg<FP8, NT>::kSmem, s, P, maps,
+                      m_tiles, tiles, hdr, (unsigned long long)wait_limit);
 }
 
 template <bool FP8, int NT>
-cudaError_t launch_tc(const RowsProduct& P, WsHeader* hdr, const DeviceInfo& dev, uint64_t wait_limit,
+cudaError_t launch_tc(const RowsProduct& P, const Plan& plan, WsHeader* hdr, const DeviceInfo& dev, uint64_t wait_limit,
                       cudaStream_t s) {
     using C = Cfg<FP8, NT>;
     PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
@@ -805,30 +862,35 @@ cudaError_t launch_tc(const RowsProduct& P, WsHeader* hdr, const DeviceInfo& dev
     for (int i = 0; i < (P.gather ? 1 : C::kBoxes); ++i)
         if (!encode_rows(fn, &maps.x[i], P.x, FP8, P.K, P.x_rows, P.gather ? 1 : (i + 1) * C::kBoxRows))
             return cudaErrorInvalidValue;
-    const int m_tiles = (P.N + 2 * kM - 1) / (2 * kM), nk = (P.K * (FP8 ? 1 : 2) + kStepBytes - 1) / kStepBytes;
-    // tiles at most: every expert has rows, and its last tile one
-    const int groups = std::min(P.R, P.E);
-    const long long tiles = ((P.R - groups) / NT + groups) * (long long)m_tiles;
-    if (tiles > kMaxTiles) return cudaErrorInvalidConfiguration;
-    // as many pairs to a tile as the device has for all tiles, where each has kMinSteps steps (us, 1 / 2 or 4
-    // pairs a tile, 8 bits: 64 rows x 2048 x 8192 24.1 / 10.3, 77 x 5003 x 2000 13.2 / 10.7, 64 x 8192 x 2048 8.9 / 8.4)
-    const int pairs = dev.num_sms / 2;
-    if (4 * tiles <= pairs && nk >= 4 * kMinSteps)
-        return launch_clusters<FP8, NT, 4>(P, maps, m_tiles, (int)tiles, hdr, dev, wait_limit, s);
-    if (2 * tiles <= pairs && nk >= 2 * kMinSteps)
-        return launch_clusters<FP8, NT, 2>(P, maps, m_tiles, (int)tiles, hdr, dev, wait_limit, s);
-    return launch_clusters<FP8, NT, 1>(P, maps, m_tiles, (int)tiles, hdr, dev, wait_limit, s);
+    const int tiles = (int)plan.tiles;
+    if (plan.splits == 4) return launch_clusters<FP8, NT, 4>(P, maps, tiles, hdr, dev, wait_limit, s);
+    if (plan.splits == 2) return launch_clusters<FP8, NT, 2>(P, maps, tiles, hdr, dev, wait_limit, s);
+    return launch_clusters<FP8, NT, 1>(P, maps, tiles, hdr, dev, wait_limit, s);
 }
 
+// Small tiles have more and smaller stages and more tensor-memory buffers, and there are more of them to go round;
+// large ones read the weights fewer times. Measured (us, tiles of 64 / 256 columns): 256 bf16 experts with 32 rows
+// each 171 / 175, in 8 bits 95 / 101. Tiles of 128 / 256: 128 rows x 8192 x 2048 in 8 bits 9.2 / 10.8, 256 rows 9.8
+// / 13.9, 1024 rows 26.6 / 25.6; 256 8-bit experts of 1024 x 2048 with 128 uneven rows on average 134 / 154, with
+// 160 even ones 139 / 125. So: 64 where the experts' rows, were they even, fit; otherwise what the estimate says,
+// and 128 where it is the same for both.
 template <bool FP8>
 cudaError_t launch_any(const RowsProduct& P, WsHeader* hdr, const DeviceInfo& dev, uint64_t wait_limit,
                        cudaStream_t s) {
-    // Rows per expert, were they even. Tiles of 64 leave room for more and smaller stages and for eight
-    // tensor-memory buffers (us, tiles of 64 / 256: 256 bf16 experts with 32 rows each 171 / 175, in 8 bits
-    // 95 / 101); above, tiles of 256 read the weights fewer times.
-    const int rows = (P.R + P.E - 1) / P.E;
-    if (rows > 64) return launch_tc<FP8, 256>(P, hdr, dev, wait_limit, s);
-    return launch_tc<FP8, 64>(P, hdr, dev, wait_limit, s);
+    Plan plan{};
+    plan.us = 3.0e38f;
+    const int groups = std::min(P.R, P.E), rows = (P.R + groups - 1) / groups;
+    cudaError_t e;
+    if (rows <= 64) {
+        if ((e = plan_tiles<FP8, 64>(P, dev, &plan)) != cudaSuccess) return e;
+    } else {
+        if ((e = plan_tiles<FP8, 128>(P, dev, &plan)) != cudaSuccess) return e;
+        if ((e = plan_tiles<FP8, 256>(P, dev, &plan)) != cudaSuccess) return e;
+    }
+    if (plan.tiles > kMaxTiles) return cudaErrorInvalidConfiguration;
+    if (plan.nt == 64) return launch_tc<FP8, 64>(P, plan, hdr, dev, wait_limit, s);
+    if (plan.nt == 128) return launch_tc<FP8, 128>(P, plan, hdr, dev, wait_limit, s);
+    return launch_tc<FP8, 256>(P, plan, hdr, dev, wait_limit, s);
 }
 
 }  // namespace

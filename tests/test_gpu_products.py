@@ -332,6 +332,19 @@ def test_grouped_groups_that_all_overlap(nv, K, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("N,K", [(260, 2048), (1030, 1040), (5000, 528), (300, 144)])
+@pytest.mark.parametrize("rows", [64, 65, 127, 128, 129, 192, 257, 400])
+def test_tile_heights_and_shared_sums(nv, rows, N, K, fp8):
+    """Few and many tiles just below and above every height of a tile, with K in one, two and four parts."""
+    for E, kind, order in ((1, "even", "list"), (2, "skew", "gather")):
+        a, xd, wd, off, lst, R = _grouped_case(rows * E, 1, E, N, K, kind, order, fp8, rows + N)
+        wk = nv.Workspace(256)
+        y = _call(nv, a, out_dtype=torch.float32, ws=wk)
+        assert wk.status() == nv.NVFP4_OK
+        _check_exact(y, _want(a, xd, wd, off, lst, R)[0], (E, kind, order))
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
 @pytest.mark.parametrize("N", [1, 3, 33, 250, 255, 257, 1022])
 def test_grouped_output_widths(nv, N, fp8):
     """Rows of y that start at every alignment, ends inside a 32-output piece and a 128-row half; the
