@@ -79,9 +79,8 @@ constexpr int kStgRows = 16, kStgPitch = 80;
 
 template <bool FP8, int NT>
 struct Cfg {
-    static constexpr int kBoxes = 4;                             // heights of a box of x: 1 .. 4 times
-    static constexpr int kBoxRows = kNRound / 2;                 // ... this
-    static_assert(kBoxes * kBoxRows * 2 >= NT, "the highest box holds a CTA's share of a tile");
+    static constexpr int kBoxRows = kNRound / 2;                 // heights of a box of x: this times
+    static constexpr int kBoxes = NT / kNRound;                  // ... 1 .. kBoxes
     static constexpr int kStage = kABytes + NT / 2 * kStepBytes;
     static constexpr int kStages = std::min(kMaxStages, (192 * 1024) / kStage);
     static constexpr int kBufs = 512 / NT;                       // tensor-memory buffers of NT columns
@@ -92,13 +91,13 @@ struct Cfg {
     static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 4 + 1;
     static constexpr int kOffTab = kOffBars + kNumBars * 8 + 16; // tile prefix [E + 1], first position [E], rows [E]
     static constexpr int kSmem = 1024 + kOffTab + (3 * NVFP4_MAX_EXPERTS + 1) * 4;
-    static_assert(NT % 64 == 0 && NT <= 256 && kStage % 1024 == 0 && kCols % 16 == 0, "swizzle atoms, fragments");
+    static_assert(NT % kNRound == 0 && NT <= 256 && kStage % 1024 == 0 && kCols % 16 == 0, "swizzle atoms, fragments");
     static_assert(kSmem <= 227 * 1024, "shared memory");
     static_assert(4 * NT / 16 * 2048 <= kOffScales, "exchanged sums fit in the ring");
 };
 
 struct TcRowMaps {
-    CUtensorMap w, x[4];   // x: boxes of one to four times Cfg::kBoxRows rows; x[0] single rows to gather
+    CUtensorMap w, x[4];   // x: boxes of one to kBoxes times Cfg::kBoxRows rows; x[0] single rows to gather
 };
 
 // ---------------------------------------------------------------- pair of CTAs
@@ -826,7 +825,7 @@ cudaError_t plan_tiles(const RowsProduct& P, const DeviceInfo& dev, Plan* best) 
     // tiles at most: every expert has rows, and its last tile one
     p.tiles = ((P.R - groups) / NT + groups) * (long long)m_tiles;
     // as many pairs to a tile as the device runs at a time, where each has kMinSteps steps (us, 1 / 2 or 4 pairs a
-    // tile, 8 bits: 64 rows x 2048 x 8192 24.1 / 9.8, 77 x 5003 x 2000 13.2 / 10.7, 64 x 8192 x 2048 8.9 / 8.4)
+    // tile, 8 bits: 64 rows x 2048 x 8192 24.1 / 9.4, 77 x 5003 x 2000 13.2 / 10.7, 64 x 8192 x 2048 8.9 / 8.4)
     int c2 = 0, c4 = 0;
     if (nk >= 2 * kMinSteps && 2 * p.tiles <= dev.num_sms / 2)
         if (cudaError_t e = resident_clusters<FP8, NT, 2>(dev, &c2); e != cudaSuccess) return e;
