@@ -289,7 +289,7 @@ def moe_route_topk(logits: torch.Tensor, k: int, stream=None):
 
 # names looked up once: a call spends as long on attributes of torch as on its launch otherwise
 _BF16, _F32, _F8, _I32 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32
-_current_device = torch.cuda.current_device
+_current_device = torch._C._cuda_getDevice                # x is on a device, so CUDA is initialised
 _raw_stream = torch._C._cuda_getCurrentRawStream      # torch.cuda.current_stream builds an object: 2 us
 _OUT_TYPE = {_BF16: 0, _F32: 1}
 _GROUPS = struct.Struct("@5iPP")     # moe_groups; packing it costs half of filling a ctypes structure
@@ -305,7 +305,7 @@ def _first(t: torch.Tensor, dtype, where: str, dims=(2,)):
     if t.dtype is not dtype or index < 0 or len(shape) not in dims or not t.is_contiguous():
         _refuse(where, "x must be a contiguous CUDA tensor of %s with %s dimensions" % (
             dtype, " or ".join(map(str, dims))))
-    if max(shape) > 0x7FFFFFFF:          # the C ABI takes int32
+    if shape[0] > 0x7FFFFFFF or shape[1] > 0x7FFFFFFF or shape[-1] > 0x7FFFFFFF:      # the C ABI takes int32
         _refuse(where, "x has shape %s" % (tuple(shape),), NVFP4_ERR_UNSUPPORTED_SHAPE)
     return t.data_ptr(), shape, index
 
@@ -326,10 +326,8 @@ def _output(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _status_word(ws: Optional[Workspace], index: int, where: str):
-    """(address, bytes) of the optional workspace, which has to be on the call's device."""
-    if ws is None:
-        return None, 0
+def _status_word(ws: Workspace, index: int, where: str):
+    """(address, bytes) of a workspace, which has to be on the call's device."""
     if ws.buf.get_device() != index:
         _refuse(where, "the workspace is on %s, x on cuda:%d" % (ws.buf.device, index))
     return ws.buf.data_ptr(), ws.nbytes
@@ -360,9 +358,12 @@ def fp8_quantize_block128(x: torch.Tensor, block_rows: int = 1, q: Optional[torc
     if block_rows != 1 and block_rows != 128:
         _refuse(where, "block_rows must be 1 or 128")
     px, shape, dev = _first(x, _BF16, where, (2, 3))
-    R, K = shape[-2:]
-    B = shape[0] if len(shape) == 3 else 1
-    sshape = (*shape[:-2], R if block_rows == 1 else (R + 127) // 128, (K + 127) // 128)
+    if len(shape) == 2:
+        B, (R, K) = 1, shape
+        sshape = (R if block_rows == 1 else (R + 127) // 128, (K + 127) // 128)
+    else:
+        B, R, K = shape
+        sshape = (B, R if block_rows == 1 else (R + 127) // 128, (K + 127) // 128)
     if q is None:
         q = _output(shape, _F8, x.device, stream)
     if scales is None:
@@ -384,14 +385,16 @@ def fp8_gemm_block128(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, 
     N, KB = w.shape[0], (K + 127) // 128
     if y is None:
         y = _output((T, N), out_dtype, x.device, stream)
-    if y.dtype not in _OUT_TYPE:
-        _refuse(where, "the output is bfloat16 or float32, not %s" % y.dtype)
+    out_dtype = y.dtype
+    out_type = _OUT_TYPE.get(out_dtype)
+    if out_type is None:
+        _refuse(where, "the output is bfloat16 or float32, not %s" % out_dtype)
+    pws, nws = (None, 0) if ws is None else _status_word(ws, dev, where)
     _enqueue(lib.fp8_gemm_block128, where, dev, stream, px,
              _operand(x_scales, _F32, (T, KB), dev, where, "x_scales"), T,
              _operand(w, _F8, (N, K), dev, where, "w"),
              _operand(w_scales, _F32, ((N + 127) // 128, KB), dev, where, "w_scales"), N, K,
-             _operand(y, y.dtype, (T, N), dev, where, "y"), _OUT_TYPE[y.dtype],
-             *_status_word(ws, dev, where))
+             _operand(y, out_dtype, (T, N), dev, where, "y"), out_type, pws, nws)
     return y
 
 
@@ -416,8 +419,11 @@ def _grouped(where, fn, x, x_scales, w, w_scales, dtype, offsets, token_list, k,
                           _operand(offsets, _I32, (E + 1,), dev, where, "offsets"), pl)
     if y is None:
         y = _output((R, N), out_dtype, x.device, stream)
-    if y.dtype not in _OUT_TYPE:
-        _refuse(where, "the output is bfloat16 or float32, not %s" % y.dtype)
+    out_dtype = y.dtype
+    out_type = _OUT_TYPE.get(out_dtype)
+    if out_type is None:
+        _refuse(where, "the output is bfloat16 or float32, not %s" % out_dtype)
+    pws, nws = (None, 0) if ws is None else _status_word(ws, dev, where)
     pw = _operand(w, dtype, (E, N, K), dev, where, "w")
     if w_scales is None:
         operands = (px, pw)
@@ -425,8 +431,8 @@ def _grouped(where, fn, x, x_scales, w, w_scales, dtype, offsets, token_list, k,
         KB = (K + 127) // 128
         operands = (px, _operand(x_scales, _F32, (rows, KB), dev, where, "x_scales"), pw,
                     _operand(w_scales, _F32, (E, (N + 127) // 128, KB), dev, where, "w_scales"))
-    _enqueue(fn, where, dev, stream, groups, *operands, N, K, _operand(y, y.dtype, (R, N), dev, where, "y"),
-             _OUT_TYPE[y.dtype], *_status_word(ws, dev, where))
+    _enqueue(fn, where, dev, stream, groups, *operands, N, K, _operand(y, out_dtype, (R, N), dev, where, "y"),
+             out_type, pws, nws)
     return y
 
 
