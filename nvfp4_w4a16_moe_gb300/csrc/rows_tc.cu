@@ -12,7 +12,7 @@
 // An expert's rows are cut into tiles of nearly equal size. The tiles of the whole call are numbered
 // over the experts (prefix sums over the offsets, made by every CTA for itself: the host never sees the
 // counts), and a persistent grid of pairs walks them. Grouped calls of the layer's shape are bound by the
-// bytes of the experts' matrices: gate/up of 256 bf16 experts of 1024 x 2048, 203 us at 4096 tokens (84 %
+// bytes of the experts' matrices: gate/up of 256 bf16 experts of 1024 x 2048, 207 us at 4096 tokens (83 %
 // of the copy rate), 101 us for the experts that 64 tokens reach.
 //
 // Warp roles of a CTA (both CTAs of a pair but where said):
@@ -868,11 +868,13 @@ cudaError_t launch_tc(const RowsProduct& P, const Plan& plan, WsHeader* hdr, con
 }
 
 // Small tiles have more and smaller stages and more tensor-memory buffers, and there are more of them to go round;
-// large ones read the weights fewer times. Measured (us, tiles of 64 / 256 columns): 256 bf16 experts with 32 rows
-// each 171 / 175, in 8 bits 95 / 101. Tiles of 128 / 256: 128 rows x 8192 x 2048 in 8 bits 9.2 / 10.8, 256 rows 9.8
-// / 13.9, 1024 rows 26.6 / 25.6; 256 8-bit experts of 1024 x 2048 with 128 uneven rows on average 134 / 154, with
-// 160 even ones 139 / 125. So: 64 where the experts' rows, were they even, fit; otherwise what the estimate says,
-// and 128 where it is the same for both.
+// large ones read the weights fewer times. Measured (us):
+//   tiles of 64 / 256 columns: 256 experts of 1024 x 2048 with 32 rows each, bf16 171 / 175, 8 bits 95 / 101
+//   tiles of 128 / 256: 8192 x 2048 in 8 bits, 128 rows 9.2 / 10.8, 256 rows 9.8 / 13.9, 1024 rows 26.6 / 25.6;
+//     256 experts with uneven rows, on average 94: bf16 187 / 191; 128: bf16 206 / 204, 8 bits 134 / 154; with 160
+//     even ones: 8 bits 139 / 125
+// So: 64 where the experts' rows, were they even, fit; otherwise what the estimate says, and 128 where it is the
+// same for both.
 template <bool FP8>
 cudaError_t launch_any(const RowsProduct& P, WsHeader* hdr, const DeviceInfo& dev, uint64_t wait_limit,
                        cudaStream_t s) {
