@@ -60,6 +60,7 @@ constexpr int kMaxStages = 9;
 constexpr int kMaxTiles = 1 << 30;
 constexpr int kMinSteps = 4;             // steps of each pair that shares a tile's K, at least
 constexpr unsigned long long kCopyDrainNs = 10000000ull;
+constexpr unsigned long long kShortLimitNs = 1000000ull;
 constexpr int kGroup = 4;                // steps whose scales are handed over together
 constexpr int kNRound = 64;              // a tile's columns are a multiple of this
 
@@ -122,6 +123,15 @@ __device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
 }
 
+// One look at a barrier's phase, without suspending the thread.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok) : "r"(su32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+
 // Bounded wait on a barrier that either CTA of the pair, or its MMAs, arrive on. One that runs out
 // records the timeout and raises the abort flag of both CTAs; once raised, every wait gives up.
 struct Waiter {
@@ -130,13 +140,19 @@ struct Waiter {
     WsHeader* hdr;
     unsigned long long limit_ns;
 
-    // By all lanes of a warp; the answer is the same in each.
+    // By all lanes of a warp; the answer is the same in each. Reading the clock takes longer than most waits, and a
+    // suspended poll sleeps up to some 10 us, so the clock starts after 64 polls. A short limit (kShortLimitNs) would
+    // be over by then: it counts from the first poll that fails, and no poll suspends.
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+        if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+        const bool brief = limit_ns < kShortLimitNs;
+        if (!brief) {
 #pragma unroll 1
-        for (int i = 0; i < 64; ++i)
-            if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+            for (int i = 0; i < 64; ++i)
+                if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        }
         const unsigned long long t0 = global_timer_ns();
-        while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+        while (!__all_sync(0xffffffffu, brief ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) {
             const bool late = global_timer_ns() - t0 > limit_ns;
             if (__any_sync(0xffffffffu, late || *abort_flag)) {
                 if (late) {

@@ -159,3 +159,40 @@ def test_products_wait_timeout_is_reported(nv, fp8, T, N, K):
     call()
     assert ws.status() == nv.NVFP4_OK
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("T,N,K", [(2000, 2600, 512), (64, 6000, 2048), (300, 513, 4096)],
+                         ids=["one_pair", "two_pairs", "four_pairs"])       # CTA pairs that share a tile's K
+@pytest.mark.parametrize("gather", [False, True], ids=["list", "gather"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_products_wait_that_runs_out_is_reported(nv, fp8, gather, T, N, K):
+    """A limit of 1 ns is over at the first poll that fails, and the first operands take a round trip to memory: the
+    status and the NaN are always there, and the next call is exact (small integers) again."""
+    g = torch.Generator().manual_seed(5)
+    x = torch.randint(-2, 3, (T, K), generator=g).float().cuda()
+    w = torch.randint(-2, 3, (N, K), generator=g).float().cuda()
+    lst = torch.randperm(T, generator=g).to(torch.int32).cuda()
+    want = (x[lst.long()] if gather else x) @ w.t()
+    off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    ws = nv.Workspace(256)
+    y = torch.zeros(T, N, device="cuda")
+    kw = dict(token_list=lst, gather=gather, y=y, ws=ws)
+    if fp8:
+        one = lambda *s: torch.ones(*s, device="cuda")
+        xq, wq = x.to(torch.float8_e4m3fn), w.to(torch.float8_e4m3fn)[None]
+        xs, wsc = one(T, K // 128), one(1, (N + 127) // 128, K // 128)
+        call = lambda: nv.moe_grouped_gemm_fp8(xq, xs, wq, wsc, off, **kw)
+    else:
+        xb, wb = x.to(torch.bfloat16), w.to(torch.bfloat16)[None]
+        call = lambda: nv.moe_grouped_gemm_bf16(xb, wb, off, **kw)
+    try:
+        nv.set_device_wait_limit(1)
+        call()
+        torch.cuda.synchronize()
+        assert ws.status(clear=True) == nv.NVFP4_ERR_DEVICE_TIMEOUT
+        assert torch.isnan(y).any()
+    finally:
+        nv.set_device_wait_limit(0)
+    call()
+    assert ws.status() == nv.NVFP4_OK
+    assert torch.equal(y, want)
