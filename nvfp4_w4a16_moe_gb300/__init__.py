@@ -382,7 +382,11 @@ def fp8_gemm_block128(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, 
     ``ws`` (optional) receives a device wait that ran out in its status word."""
     where = "fp8_gemm_block128"
     px, (T, K), dev = _first(x, _F8, where)
+    if w.dim() != 2:
+        _refuse(where, "w must be [N, K]")
     N, KB = w.shape[0], (K + 127) // 128
+    if N > 0x7FFFFFFF:
+        _refuse(where, "w has %d rows" % N, NVFP4_ERR_UNSUPPORTED_SHAPE)
     if y is None:
         y = _output((T, N), out_dtype, x.device, stream)
     out_dtype = y.dtype
@@ -404,6 +408,8 @@ def _grouped(where, fn, x, x_scales, w, w_scales, dtype, offsets, token_list, k,
     if w.dim() != 3:
         _refuse(where, "w must be [E, N, K]")
     E, N, _ = w.shape
+    if E > 0x7FFFFFFF or N > 0x7FFFFFFF:
+        _refuse(where, "w has shape %s" % (tuple(w.shape),), NVFP4_ERR_UNSUPPORTED_SHAPE)
     if k < 1:
         _refuse(where, "k must be at least 1")
     R = rows * k if gather else rows

@@ -131,3 +131,57 @@ def test_python_refuses_host_tensors(nv):
         nv.fp8_quantize_block128(x, block_rows=64)
     with pytest.raises(nv.NVFP4Error):
         nv.moe_grouped_gemm_bf16(x, torch.zeros(2, 8, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32))
+
+
+class Operand:
+    """What the Python calls read of a tensor, at any size: no memory behind it."""
+
+    def __init__(self, shape, dtype):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, "cuda:0"
+
+    def dim(self):
+        return len(self.shape)
+
+    def get_device(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return FAKE
+
+
+F8, F32, BF16, I32 = torch.float8_e4m3fn, torch.float32, torch.bfloat16, torch.int32
+
+
+@pytest.mark.parametrize("N", [(1 << 31), (1 << 32) + 5])
+def test_outputs_past_32_bits_are_refused(nv, N):
+    """The C ABI takes int32: 2^32 + 5 weight rows must not arrive there as 5."""
+    dense = lambda: nv.fp8_gemm_block128(Operand((4, 16), F8), Operand((4, 1), F32), Operand((N, 16), F8),
+                                         Operand(((N + 127) // 128, 1), F32), y=Operand((4, N), F32))
+    grouped = lambda: nv.moe_grouped_gemm_bf16(Operand((4, 16), BF16), Operand((2, N, 16), BF16), Operand((3,), I32),
+                                               y=Operand((4, N), F32))
+    grouped8 = lambda: nv.moe_grouped_gemm_fp8(Operand((4, 16), F8), Operand((4, 1), F32), Operand((2, N, 16), F8),
+                                               Operand((2, (N + 127) // 128, 1), F32), Operand((3,), I32),
+                                               y=Operand((4, N), F32))
+    for call in (dense, grouped, grouped8):
+        with pytest.raises(nv.NVFP4Error) as e:
+            call()
+        assert e.value.status == nv.NVFP4_ERR_UNSUPPORTED_SHAPE
+
+
+@pytest.mark.parametrize("E", [1 << 31, (1 << 32) + 2])
+def test_experts_past_32_bits_are_refused(nv, E):
+    with pytest.raises(nv.NVFP4Error) as e:
+        nv.moe_grouped_gemm_bf16(Operand((4, 16), BF16), Operand((E, 8, 16), BF16), Operand((E + 1,), I32),
+                                 y=Operand((4, 8), F32))
+    assert e.value.status == nv.NVFP4_ERR_UNSUPPORTED_SHAPE
+
+
+@pytest.mark.parametrize("shape", [(), (16,), (1, 8, 16)])
+def test_a_dense_weight_has_two_dimensions(nv, shape):
+    with pytest.raises(nv.NVFP4Error) as e:
+        nv.fp8_gemm_block128(Operand((4, 16), F8), Operand((4, 1), F32), Operand(shape, F8), Operand((1, 1), F32),
+                             y=Operand((4, 8), F32))
+    assert e.value.status == nv.NVFP4_ERR_INVALID_ARG
