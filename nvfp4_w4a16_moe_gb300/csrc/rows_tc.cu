@@ -570,12 +570,10 @@ rows_tc_kernel(const RowsProduct P, const __grid_constant__ TcRowMaps maps, int 
                     if (++st == C::kStages) st = 0, st_par ^= 1;
                 }
             }
-            if (rank == 0) {
-                // no MMA still reads or writes either CTA's memory when it is freed
-                if (elect_one()) {
-                    commit_pair(done, pair_mask);
-                    drain_wait(done, 0);
-                }
+            // no MMA still reads or writes either CTA's memory, nor has an arrival on the way to it, when it is freed
+            if (elect_one()) {
+                if (rank == 0) commit_pair(done, pair_mask);
+                drain_wait(done, 0);
             }
         } else if (warp >= kGatherWarp0) {
             if (P.gather) {
