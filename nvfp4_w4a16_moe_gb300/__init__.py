@@ -382,9 +382,10 @@ def fp8_gemm_block128(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, 
     ``ws`` (optional) receives a device wait that ran out in its status word."""
     where = "fp8_gemm_block128"
     px, (T, K), dev = _first(x, _F8, where)
-    if w.dim() != 2:
+    wshape = w.shape
+    if len(wshape) != 2:
         _refuse(where, "w must be [N, K]")
-    N, KB = w.shape[0], (K + 127) // 128
+    N, KB = wshape[0], (K + 127) // 128
     if N > 0x7FFFFFFF:
         _refuse(where, "w has %d rows" % N, NVFP4_ERR_UNSUPPORTED_SHAPE)
     if y is None:
@@ -405,11 +406,12 @@ def fp8_gemm_block128(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, 
 def _grouped(where, fn, x, x_scales, w, w_scales, dtype, offsets, token_list, k, gather, scatter, y, out_dtype, ws,
              stream):
     px, (rows, K), dev = _first(x, dtype, where)
-    if w.dim() != 3:
+    wshape = w.shape
+    if len(wshape) != 3:
         _refuse(where, "w must be [E, N, K]")
-    E, N, _ = w.shape
+    E, N, _ = wshape
     if E > 0x7FFFFFFF or N > 0x7FFFFFFF:
-        _refuse(where, "w has shape %s" % (tuple(w.shape),), NVFP4_ERR_UNSUPPORTED_SHAPE)
+        _refuse(where, "w has shape %s" % (tuple(wshape),), NVFP4_ERR_UNSUPPORTED_SHAPE)
     if k < 1:
         _refuse(where, "k must be at least 1")
     R = rows * k if gather else rows
