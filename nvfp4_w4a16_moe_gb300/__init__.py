@@ -289,8 +289,10 @@ def moe_route_topk(logits: torch.Tensor, k: int, stream=None):
 
 # names looked up once: a call spends as long on attributes of torch as on its launch otherwise
 _BF16, _F32, _F8, _I32 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32
-_current_device = torch._C._cuda_getDevice                # x is on a device, so CUDA is initialised
-_raw_stream = torch._C._cuda_getCurrentRawStream      # torch.cuda.current_stream builds an object: 2 us
+# x is on a device when these are called, so CUDA is initialised. The public calls, on which a torch without CUDA
+# falls back, cost more (torch.cuda.current_stream builds an object: 2 us).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
 _OUT_TYPE = {_BF16: 0, _F32: 1}
 _GROUPS = struct.Struct("@5iPP")     # moe_groups; packing it costs half of filling a ctypes structure
 

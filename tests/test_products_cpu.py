@@ -1,6 +1,9 @@
 """Checks of the 8-bit and grouped products that need no GPU: the 64-bit forms that the GPU tests
 compare with, and the refusals of the C entry points (all before CUDA is touched)."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -185,3 +188,15 @@ def test_a_dense_weight_has_two_dimensions(nv, shape):
         nv.fp8_gemm_block128(Operand((4, 16), F8), Operand((4, 1), F32), Operand(shape, F8), Operand((1, 1), F32),
                              y=Operand((4, 8), F32))
     assert e.value.status == nv.NVFP4_ERR_INVALID_ARG
+
+
+def test_imports_on_a_torch_without_cuda(nv):
+    """Such a torch lacks the two private names that the product calls use where they are there."""
+    code = ("import torch\n"
+            "del torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream\n"
+            "import nvfp4_w4a16_moe_gb300 as nv\n"
+            "assert callable(nv._current_device) and callable(nv._raw_stream)\n"
+            "assert nv.lib.nvfp4_version() >= 1\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
