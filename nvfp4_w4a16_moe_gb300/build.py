@@ -9,6 +9,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -47,12 +48,29 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
-def _compile(src: str, extra) -> str:
+def check_launch_registers(source: str, log: str):
+    """The 8-bit tile kernels hand registers from some warps to others, and would wait forever for registers that the
+    launch did not bring, so the library launches them only as compiled to kLaunchRegs registers. A compiler (see its
+    log, ``-Xptxas -v``) or flags that give another count fail here, not at the first call."""
+    want = re.search(r"\bkLaunchRegs = (\d+)", source)
+    if want is None:
+        return
+    used = re.findall(r"Compiling entry function '\S*rows_tc_kernelILb1E\S*' for .*?\bUsed (\d+) registers", log, re.S)
+    if not used or any(u != want.group(1) for u in used):
+        raise RuntimeError("the 8-bit tile kernels have to take %s registers a thread (kLaunchRegs, kEpiRegs and "
+                           "kOtherRegs), but were compiled to %s" % (want.group(1), ", ".join(used) or "none"))
+
+
+def _compile(src: str, extra, verbose: bool = False) -> str:
     obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-    cmd = [nvcc(), *ARCH, *NVCC_FLAGS, *extra, "-c", src, "-o", obj]
+    cmd = [nvcc(), *ARCH, *NVCC_FLAGS, "-Xptxas", "-v", *extra, "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("nvcc failed for %s:\n%s\n%s" % (src, " ".join(cmd), r.stderr))
+    if verbose:
+        sys.stderr.write(r.stderr)
+    with open(src) as f:
+        check_launch_registers(f.read(), r.stderr)
     return obj
 
 
@@ -62,7 +80,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        objs = list(ex.map(lambda s: _compile(s, list(extra) + (["-Xptxas", "-v"] if verbose else [])), srcs))
+        objs = list(ex.map(lambda s: _compile(s, list(extra), verbose), srcs))
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

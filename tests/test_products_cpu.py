@@ -200,3 +200,23 @@ def test_imports_on_a_torch_without_cuda(nv):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+PTXAS = """ptxas info    : Compiling entry function '_ZN14rows_tc_kernelILb%dELi64ELi1EEEvx' for 'sm_103a'
+ptxas info    : Function properties for _ZN14rows_tc_kernelILb%dELi64ELi1EEEvx
+    0 bytes stack frame, 0 bytes spill stores, 0 bytes spill loads
+ptxas info    : Used %d registers, used 1 barriers
+"""
+
+
+def test_build_refuses_another_register_count_than_the_launch_needs(nv):
+    """The 8-bit tile kernels move registers between their warps; compiled to another count they would be refused
+    at every launch. bf16 kernels (Lb0) do not."""
+    from nvfp4_w4a16_moe_gb300 import build
+    source = "constexpr int kLaunchRegs = 80, kEpiRegs = 96;"
+    good = PTXAS % (0, 0, 72) + PTXAS % (1, 1, 80)
+    build.check_launch_registers("constexpr int kOther = 1;", "")
+    build.check_launch_registers(source, good)
+    for bad in (PTXAS % (0, 0, 72), good + PTXAS % (1, 1, 72), PTXAS % (1, 1, 88) + good):
+        with pytest.raises(RuntimeError, match="register"):
+            build.check_launch_registers(source, bad)
