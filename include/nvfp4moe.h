@@ -327,6 +327,10 @@ NVFP4_API nvfp4_status fp8_quantize_block128(const uint16_t* x, int32_t B, int32
  *   y[t,n] = sum_b x_scales[t,b] * w_scales[n/128,b] * sum_{k in block b} x[t,k] * w[n,k]
  *   over the blocks b of 128 columns; every block's sum and the running sum in fp32, one
  *   rounding to the output type.
+ *   The two scales of a block are multiplied first, in fp32, so their product has to be in fp32's normal
+ *   range: from 2^-126 up to below 2^128, or 0 (scales of fp8_quantize_block128: the blocks' largest
+ *   magnitudes multiply to between 2^-108 and 2^145). A smaller one keeps fewer digits; one that
+ *   overflows makes the block's sum infinite, or NaN where it is 0.
  *   x         uint8 E4M3 [T, K] device;  x_scales  fp32 [T, ceil(K/128)]
  *   w         uint8 E4M3 [N, K] device;  w_scales  fp32 [ceil(N/128), ceil(K/128)]
  *   y         bf16 or fp32 [T, N] device (y_type), written
@@ -372,7 +376,8 @@ NVFP4_API nvfp4_status moe_grouped_gemm_bf16(const moe_groups* g, const uint16_t
 /*
  * moe_grouped_gemm_fp8 - moe_grouped_gemm_bf16 with the block-scaled E4M3 operands of
  * fp8_gemm_block128: x uint8 (rows as above) with x_scales fp32 [rows of x, ceil(K/128)],
- * w uint8 [E, N, K] with w_scales fp32 [E, ceil(N/128), ceil(K/128)]. K >= 16, K % 16 == 0.
+ * w uint8 [E, N, K] with w_scales fp32 [E, ceil(N/128), ceil(K/128)]. K >= 16, K % 16 == 0. The
+ * scales' range as there.
  */
 NVFP4_API nvfp4_status moe_grouped_gemm_fp8(const moe_groups* g, const uint8_t* x, const float* x_scales,
                                             const uint8_t* w, const float* w_scales, int32_t N, int32_t K,

@@ -669,3 +669,23 @@ def test_experts_of_a_layer_from_the_routers_lists(nv, T, fp8):
             total += wn[t, j] * r
             slack += wn[t, j] * (ref.bound(r, Sr, I, False, fp8) + 2.0 ** -20 * Sr)
         assert np.all(np.abs(ref.f64(y)[t] - total) <= slack + 1e-30)
+
+
+@pytest.mark.parametrize("T", [1, 8, 40, 300])
+def test_scales_at_the_ends_of_their_range(nv, T):
+    """The contract beyond the normal range of the scales' product: y = fl(fl(xs ws) * sum) for one block."""
+    g = _gen(T)
+    N, K = 200, 128
+    x, w = _small(g, T, K), _small(g, N, K)
+    x[:, 64:] = 0
+    w[5, :64] = 0                                                # sums of zero, the operands are not
+    part = (x.double() @ w.double().t()).numpy().astype(np.float32)
+    assert (part == 0).any()
+    for ex, ew in ((-60, -66), (-70, -70), (60, 67), (60, 90), (100, -100)):
+        xs = torch.full((T, 1), (1 + 2.0 ** -9) * 2.0 ** ex)
+        ws = torch.full((2, 1), (1 + 2.0 ** -20) * 2.0 ** ew)
+        y = nv.fp8_gemm_block128(x.to(F8).cuda(), xs.cuda(), w.to(F8).cuda(), ws.cuda(), out_dtype=torch.float32)
+        with np.errstate(all="ignore"):
+            want = part * (np.float32(xs[0, 0].item()) * np.float32(ws[0, 0].item()))
+        assert want.dtype == np.float32
+        assert np.array_equal(y.cpu().numpy(), want, equal_nan=True), (ex, ew)
