@@ -689,3 +689,14 @@ def test_scales_at_the_ends_of_their_range(nv, T):
             want = part * (np.float32(xs[0, 0].item()) * np.float32(ws[0, 0].item()))
         assert want.dtype == np.float32
         assert np.array_equal(y.cpu().numpy(), want, equal_nan=True), (ex, ew)
+
+
+@pytest.mark.parametrize("K", [16, 32, 48, 64, 80, 96, 112])
+@pytest.mark.parametrize("rows", ["gather", "scatter", "list"])
+@pytest.mark.parametrize("T", [2, 200])
+def test_grouped_fp8_widths_below_a_block(nv, T, rows, K):
+    """Rows of 16 to 112 bytes: one partial block, narrower than a step of the tiles."""
+    a, xd, wd, off, lst, R = _grouped_case(T, 2, 5, 150, K, "skew", rows, True, K + T)
+    want, _, written = _want(a, xd, wd, off, lst, R)
+    assert written.all()
+    _check_exact(_call(nv, a, out_dtype=torch.float32), want)
