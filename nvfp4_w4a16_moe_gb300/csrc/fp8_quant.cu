@@ -179,12 +179,11 @@ cudaError_t launch_fp8_quantize(const uint16_t* x, int B, int R, int K, int bloc
             return launch_pdl(quantize_rows_kernel<kUnroll, false>, grid, kQThreads, 0, s, x, blocks, K, KB, q, scales);
         };
         return blocks < kFewBlocks ? run(std::integral_constant<int, 1>{}) : run(std::integral_constant<int, 4>{});
-    } else {
-        const int RB = (R + 127) / 128;
-        if ((size_t)B * RB * KB > 0x7FFFFFFFu) return cudaErrorInvalidConfiguration;
-        return launch_pdl(quantize_tiles_kernel, (unsigned)((size_t)B * RB * KB), kQThreads, 0, s, x, R, K, RB, KB, q, scales);
     }
-    return cudaGetLastError();
+    const int RB = (R + 127) / 128;
+    const size_t blocks = (size_t)B * RB * KB;
+    if (blocks > 0x7FFFFFFFu) return cudaErrorInvalidConfiguration;
+    return launch_pdl(quantize_tiles_kernel, (unsigned)blocks, kQThreads, 0, s, x, R, K, RB, KB, q, scales);
 }
 
 }  // namespace nvfp4
