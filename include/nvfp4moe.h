@@ -46,6 +46,11 @@
  *     nvfp4_get_device_status, which says so).
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).
  *     Work is enqueued asynchronously on it.
+ *   - nvfp4_gemv_w4a16 and the single-token layer request their weights (of a layer also the router's
+ *     and the shared gate's rows) before they wait for the kernel before them on the stream; they, the
+ *     8-bit quantiser and the products let the next kernel start before their outputs are written. So a
+ *     matrix that one of these calls writes (a router's rows from a product, say) must not be a weight of a
+ *     GEMV or single-token layer enqueued right behind it: let any other kernel or a copy come between.
  *   - Argument and shape checks run on the host, before anything is enqueued; a
  *     failing check returns its status and enqueues nothing.
  *   - A failed kernel launch returns NVFP4_ERR_CUDA. Errors that only the device
@@ -342,7 +347,8 @@ NVFP4_API nvfp4_status fp8_quantize_block128(const uint16_t* x, int32_t B, int32
  *   Shapes: 0 <= T <= NVFP4_MAX_PRODUCT_ROWS, 1 <= N <= 2^22, K >= 16, K % 16 == 0,
  *   K <= NVFP4_MAX_PRODUCT_K. T == 0 enqueues nothing.
  *   Launched with programmatic stream serialisation; it waits for the kernel before it on the
- *   stream before it reads or writes anything (so do the quantiser and the grouped products).
+ *   stream before it reads or writes anything (so do the quantiser and the grouped products), and
+ *   lets the next kernel start before y is written (see the conventions above for what that excludes).
  *   One kernel: up to 8 rows (here T; R of a grouped product) stream the weights through
  *   warp-level MMAs, more rows, and 8-bit weights above 48 MB, run on tcgen05 tiles.
  */

@@ -172,11 +172,14 @@ __device__ __forceinline__ uint4 ld_once_v4(const void* p) {
 }
 
 // The 8-bit and grouped products and the quantiser are launched with programmatic stream serialisation, which
-// takes 2 to 2.7 us off a call in a row of calls (one token through 8192 x 2048 8.2 -> 6.6, quantising 4096 x 2048
+// takes 1.6 to 2.7 us off a call in a row of calls (one token through 8192 x 2048 8.2 -> 6.6, quantising 4096 x 2048
 // 8.2 -> 5.5). Every thread first waits until the kernel before this one is complete and its writes are
 // visible (nothing in global memory is touched before, and data is read with plain loads, not through the
 // non-coherent path). Only then may the next kernel start: one that reads its weights before its own wait (the
-// NVFP4 kernels do) sees all that was enqueued before this kernel. Letting it start earlier measured the same.
+// NVFP4 kernels do) sees all that was enqueued before this kernel, though not this kernel's own outputs: the
+// header forbids those as its weights. Releasing it only after a fence behind the last store would allow them, and
+// costs 0.3 to 0.8 us a call (one token's gate/up over bf16 experts 7.5 -> 8.3, quantising 4096 x 2048 5.0 -> 5.8).
+// Letting it start before the wait measured the same.
 __device__ __forceinline__ void pdl_wait_then_trigger() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
