@@ -359,7 +359,8 @@ NVFP4_API nvfp4_status fp8_gemm_block128(const uint8_t* x, const float* x_scales
 /*
  * moe_grouped_gemm_bf16 - each expert's matrix times the rows routed to it:
  *   y[o(r),:] = W[e] x[i(r),:]  for expert_offsets[e] <= r < expert_offsets[e+1]
- *   with i(r), o(r) as moe_groups says; fp32 sums, one rounding to the output type.
+ *   with i(r), o(r) as moe_groups says; fp32 sums, one rounding to the output type. (The tensor cores' fp32
+ *   sums: the error of an fp32 output grows with K and is about 2e-6 of the outputs' norm at K = 2048.)
  *   Defined by: lynn-engine README, P2/P3-A notes (the routed path as batched projections
  *   over each expert's tokens) and "next steps" (grouped GEMM instead of per-expert
  *   launches), for experts kept in bf16.

@@ -232,11 +232,12 @@ __device__ __forceinline__ int y_row(const RowsProduct& P, int r) {
 }
 
 // Up to kStreamRows rows in all: weights streamed through warp-level MMAs; more: tcgen05 tiles. Measured on
-// a GB300 (us on the device, stream / tiles): 8192 x 2048 in 8 bits at 8 rows 6.2 / 7.9, at 16 rows (two blocks
-// of columns in the streaming kernel) 8.2 / 8.0; 2048 x 8192 at 8 rows 7.4 / 9.9; 8 bf16 experts of 1024 x 2048
-// with a row each 7.2 / 10.6, 15 with 16 rows 19.3 / 13.7.
+// a GB300 with weights that are not in the L2 (us on the device, stream / tiles): 8192 x 2048 in 8 bits at 8 rows
+// 5.8 / 8.3, at 16 rows (two blocks of columns in the streaming kernel) 9.4 / 8.4; 2048 x 8192 at 8 rows 7.2 / 9.6,
+// at 16 rows 10.2 / 9.6; 8 bf16 experts of 1024 x 2048 with a row each 8.1 / 10.3, 8192 x 2048 in bf16 at 16 rows
+// 12.5 / 10.4.
 // Large 8-bit matrices go to the tiles even so, because the streaming kernel's conversions bound it (one row
-// of K = 2048: 33 MB of W 9.1 / 9.6, 67 MB 16.1 / 14.2, 508 MB 109 / 84).
+// of K = 2048: 33 MB of W 9.1 / 9.8, 67 MB 15.2 / 14.7, 508 MB 93 / 80).
 constexpr int kStreamRows = 8;
 constexpr long long kStreamBytes8 = 48ll << 20;
 cudaError_t launch_rows_stream(const RowsProduct& P, const DeviceInfo& dev, cudaStream_t s);

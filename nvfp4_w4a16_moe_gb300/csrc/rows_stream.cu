@@ -8,18 +8,20 @@
 //    column group c takes units c and 4 + c of a chunk, and the words of a unit feed two (bf16) or
 //    four MMAs (8-bit). This permutes K inside a chunk, in the same way for both operands, so the sum is
 //    over the same products; no shared memory or transposition is needed.
-//  - One chunk a warp at a time and four CTAs on an SM: 64 KB of W in flight. (Two chunks a warp and two
-//    CTAs: 9.3 us for the gate/up of one token over 8 bf16 experts of 1024 x 2048, this way 6.9.) A grid
-//    that fills the device less than that requests the next chunk before it uses this one (AHEAD: 80
-//    registers, three CTAs: 2048 x 8192 in bf16 7.4 us against 9.3; on the larger grid above 8.4 against 6.7).
+//  - One chunk a warp at a time and four CTAs on an SM: 64 KB of W in flight. A grid that fills the device
+//    less than that requests the next chunk before it uses this one (AHEAD: 80 registers, three CTAs). Device
+//    time with / without, weights that are not in the L2: one row of 2048 x 8192 in bf16 11.5 / 14.5 us, in
+//    8 bits 7.1 / 10.1; on the larger grid of 8 bf16 experts of 1024 x 2048 with a row each 10.4 / 8.1 (in the
+//    L2 5.9 / 5.4). With AHEAD the 8-bit kernel spills (48 bytes of stack); it is the faster one all the same.
 //  - The warps' fp32 partial sums are added in warp order in shared memory: the same bits on
 //    every run.
 //  - Rows so short that eight warps would not have two chunks each share a CTA instead: with K = 512 in
-//    8 bits a 64-token batch over 256 experts fell from 147 to 58 us.
+//    8 bits the 512 rows of a 64-token batch over 256 experts fell from 147 to 58 us (on this kernel; the tiles
+//    take 32).
 //  - 8-bit operands are converted to f16, exactly, in registers (as fast as the 8-bit form of mma.sync, or
-//    faster: 109 against 113 us for one token and 248320 x 2048, where the conversions bound it at
-//    4.7 TB/s; bf16 streams the same matrix at 6.5 TB/s, 96 % of the measured copy rate). A chunk is one
-//    block of 128, summed from zero in fp32 and added to the running sum times the block's two scales.
+//    3 % faster). The conversions bound large matrices: one token and 248320 x 2048 takes 93 us, 5.5 TB/s,
+//    where bf16 streams the same matrix at 6.6 TB/s, 97 % of the measured copy rate. A chunk is one block
+//    of 128, summed from zero in fp32 and added to the running sum times the block's two scales.
 // Widths that are no multiple of a chunk read zero units past the end.
 #include "common.cuh"
 #include "kernels.cuh"

@@ -25,20 +25,24 @@
 //   Scale warps (8-bit): x_scale * w_scale of every column of four steps, in a ring of their own.
 //   MMA warp: in the pair's first CTA, the MMAs of a step for both. In the second CTA it tells the first
 //     that the step's operands have landed here.
-//   Epilogue warps. bf16: a whole tile is summed in one tensor-memory buffer, then read and written out.
+//   Epilogue warps. bf16: a whole tile is summed in one tensor-memory buffer, then read and written out. The
+//     tensor core's running sum loses more than a register sum would: an fp32 output of K = 2048 is off by
+//     2.2e-6 (norm, against 64 bits; in 8 bits, where blocks of 128 are added in registers, by 8e-8).
 //     8-bit: the operands carry a scale per 128 of K, so every step starts a buffer from zero; the warps
 //     read it, multiply each column with its scale and add it to the tile's sum in registers (fp32),
 //     while the MMAs fill the next buffer. That bounds 8-bit tiles, not the MMAs: a step of 256 x 256 takes
 //     0.58 us where the MMAs alone need 0.27 (over a quarter of it are the multiply-adds; sixteen warps
 //     issue half of their scheduler's slots, eight warps with twice the sums each took 0.82 us). 4096 x 8192
-//     x 2048: 80 us, 1.7 PFLOP/s; gate/up of 4096 tokens over 256 experts of 1024 x 2048: 135 us. Separate
+//     x 2048: 80 us, 1.7 PFLOP/s: seven rounds of 16 steps, 65 us, and of about 2 us in which the same warps
+//     write the tile out and the MMAs, 512 / NT steps ahead at most, stand still; gate/up of 4096 tokens over 256 experts of 1024 x 2048: 135 us. Separate
 //     buffers for the two column halves cost more in operand reads than they hid.
-// Tensor memory holds 512 / NT buffers, so the next tile's or step's MMAs run under the epilogue.
+// Tensor memory holds 512 / NT buffers: as many tiles (bf16) or steps (8-bit) the MMAs can run ahead.
 //
 // Few tiles (few rows of W, a small batch): a cluster of two or four pairs shares a tile's K, and the
-// pairs' sums are exchanged through distributed shared memory, each pair finishing a part of the columns:
-// the sums are added in the order of the pairs. (64 rows times 2048 x 8192 in 8 bits: 24 us with one pair a
-// tile, 9.4 with four.)
+// pairs' sums are exchanged through distributed shared memory, each pair finishing a part of the columns: to
+// its own sum it adds the others' in the order of the pairs, the same order on every run. (64 rows times
+// 2048 x 8192 in 8 bits: 24 us with one pair a tile, 9.0 with four. The 8-bit forms of 256 columns with two and
+// four pairs spill 32 bytes a thread.)
 //
 // Every wait is bounded; one that runs out records NVFP4_ERR_DEVICE_TIMEOUT (where the caller passed a
 // workspace) and makes the pair fill its remaining tiles with NaN.
@@ -829,7 +833,9 @@ struct Plan {
 
 // Tiles of NT columns. The estimate takes the rows to be even over the experts; its figures (us) are fitted to
 // calls of one to three rounds of tiles: a step of N columns 0.08 + 0.00195 N in 8 bits, 0.05 + 0.0007 N in bf16;
-// 2 to write a tile out, 0.5 + 0.009 N to exchange its sums.
+// 2 to write a tile out, 0.5 + 0.009 N to exchange its sums. It leaves out what every plan pays, 2 to 4 us, and is
+// too low where four pairs share 256 columns of a long K (256 x 2048 x 8192: 14.1 for 19.1 in 8 bits, 12.1 for 18.7
+// in bf16).
 template <bool FP8, int NT>
 cudaError_t plan_tiles(const RowsProduct& P, const DeviceInfo& dev, Plan* best) {
     const int m_tiles = (P.N + 2 * kM - 1) / (2 * kM), nk = (P.K * (FP8 ? 1 : 2) + kStepBytes - 1) / kStepBytes;
@@ -887,8 +893,11 @@ cudaError_t launch_tc(const RowsProduct& P, const Plan& plan, WsHeader* hdr, con
 //   tiles of 128 / 256: 8192 x 2048 in 8 bits, 128 rows 9.2 / 10.8, 256 rows 9.8 / 13.9, 1024 rows 26.6 / 25.6;
 //     256 experts with uneven rows, on average 94: bf16 187 / 191; 128: bf16 206 / 204, 8 bits 134 / 154; with 160
 //     even ones: 8 bits 139 / 125
-// So: 64 where the experts' rows, were they even, fit; otherwise what the estimate says, and 128 where it is the
-// same for both.
+//   64 / 128 / 256, 256 experts of 1024 x 2048 with 62 rows on average, the longest with 82: bf16 173 / 171 / 177,
+//     8 bits 95 / 93 / 98; with 913: bf16 179 / 173 / 177, 8 bits 102 / 96 / 104; 31 on average, the longest with
+//     470: bf16 164 / 164 / 172, 8 bits 89 / 87 / 98
+// So: 64 where the experts' rows, were they even, fit (for very uneven rows just below that up to 9 % slower than
+// 128); otherwise what the estimate says, and 128 where it is the same for both.
 template <bool FP8>
 cudaError_t launch_any(const RowsProduct& P, WsHeader* hdr, const DeviceInfo& dev, uint64_t wait_limit,
                        cudaStream_t s) {
