@@ -34,8 +34,9 @@
 //     0.58 us where the MMAs alone need 0.27 (over a quarter of it are the multiply-adds; sixteen warps
 //     issue half of their scheduler's slots, eight warps with twice the sums each took 0.82 us). 4096 x 8192
 //     x 2048: 80 us, 1.7 PFLOP/s: seven rounds of 16 steps, 65 us, and of about 2 us in which the same warps
-//     write the tile out and the MMAs, 512 / NT steps ahead at most, stand still; gate/up of 4096 tokens over 256 experts of 1024 x 2048: 135 us. Separate
-//     buffers for the two column halves cost more in operand reads than they hid.
+//     write the tile out and the MMAs, 512 / NT steps ahead at most, stand still. Gate/up of 4096 tokens over
+//     256 experts of 1024 x 2048: 135 us. Separate buffers for the two column halves cost more in operand reads
+//     than they hid.
 // Tensor memory holds 512 / NT buffers: as many tiles (bf16) or steps (8-bit) the MMAs can run ahead.
 //
 // Few tiles (few rows of W, a small batch): a cluster of two or four pairs shares a tile's K, and the
