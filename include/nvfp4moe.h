@@ -151,6 +151,21 @@ typedef enum {
     NVFP4_OUT_F32 = 1
 } nvfp4_out_type;
 
+/* Form of the rows that rmsnorm_residual and moe_swiglu write. */
+typedef enum {
+    NVFP4_ROWS_BF16 = 0,
+    NVFP4_ROWS_FP8 = 1,               /* E4M3 codes, fp32 scale per 1 x 128, as fp8_quantize_block128 writes them */
+    NVFP4_ROWS_NVFP4 = 2              /* E2M1 codes, E4M3 scale per 16, fp32 scale per row, as nvfp4_quantize_rows */
+} nvfp4_rows_kind;
+
+/* Where rows [R, K] go (device pointers; 16-byte aligned, the fp32 arrays 4-byte). */
+typedef struct {
+    int32_t kind;                    /* nvfp4_rows_kind                                              */
+    void* data;                      /* bf16 [R, K] / uint8 E4M3 [R, K] / uint8 E2M1 pairs [R, K/2]   */
+    void* scales;                    /* unused      / fp32 [R, ceil(K/128)] / uint8 E4M3 [R, K/16]    */
+    float* row_scales;               /* unused      / unused                / fp32 [R]                */
+} nvfp4_rows;
+
 /*
  * Rows grouped by expert, as moe_route_topk lists them: list position r in
  * [expert_offsets[e], expert_offsets[e+1]) belongs to expert e.
@@ -174,6 +189,7 @@ typedef struct {
 /* ------------------------------------------------------------------ limits */
 #define NVFP4_MAX_PRODUCT_ROWS 1048576  /* fp8_gemm_block128: T, moe_groups: R    */
 #define NVFP4_MAX_PRODUCT_K 65536       /* K of the 8-bit and grouped products    */
+#define NVFP4_MAX_ROW_K 32768       /* K of nvfp4_quantize_rows, H and I of rmsnorm_residual and moe_swiglu */
 #define NVFP4_MAX_TOPK 8          /* k <= 8                                    */
 #define NVFP4_MAX_EXPERTS 256     /* E <= 256                                  */
 #define NVFP4_MAX_GEMV_TOKENS 64  /* nvfp4_gemv_w4a16: 1 <= T <= 64            */
@@ -390,6 +406,143 @@ NVFP4_API nvfp4_status moe_grouped_gemm_fp8(const moe_groups* g, const uint8_t* 
                                             const uint8_t* w, const float* w_scales, int32_t N, int32_t K,
                                             void* y, int32_t y_type, void* workspace, size_t workspace_bytes,
                                             void* stream);
+
+/*
+ * nvfp4_quantize_rows - bf16 rows -> NVFP4 rows, the activations of nvfp4_gemm_w4a4 and
+ * moe_grouped_gemm_nvfp4. Per row with a = max |x|, and per block of 16 with b = max |x|:
+ *   row scale    s = the smallest power of two >= a / 2688 (2688 = 6 * 448; 1 where a = 0), at least 2^-126
+ *   block scale  e = the E4M3 value nearest to b / (6 s), ties to even
+ *   code         the E2M1 value nearest to x / (e s) (the real quotient), ties to the even code, at most 6
+ *                in magnitude; the sign of x is kept. Where e = 0 all codes are 0.
+ *   so x is approximated by code * e * s. A row depends on no other row. The row scale is a power of two so
+ *   that the decisions above are exact (E4M3's 15 binades leave the lost one to spare).
+ *   A row that holds a NaN or an infinity has row scale NaN, block scales and codes 0.
+ *   Defined by: the storage section above and nvfp4_pack, with a scale per row in place of the tensor scale
+ *   (lynn-engine README, P89 note: one scale per 16 K elements, consumed exactly).
+ *   x  bf16 [R, K] device;  packed  uint8 [R, K/2], scales  uint8 [R, K/16], row_scales  fp32 [R] device, written
+ *   Shapes: R >= 0, K >= 32, K % 32 == 0, K <= NVFP4_MAX_ROW_K. R == 0 enqueues nothing.
+ */
+NVFP4_API nvfp4_status nvfp4_quantize_rows(const uint16_t* x, int32_t R, int32_t K, uint8_t* packed, uint8_t* scales,
+                                           float* row_scales, void* stream);
+
+/*
+ * nvfp4_dequantize_rows - what NVFP4 rows stand for: y[r,k] = code * block scale * scale[r / scale_rows] in fp32,
+ * then rounded to the output type (nothing is rounded in rows of nvfp4_quantize_rows whose values are in the
+ * type's normal range).
+ *   scale, scale_rows  rows of nvfp4_quantize_rows: row_scales, 1. A matrix of nvfp4_pack (E4M3 scales): its
+ *                      tensor_scale, N. Gate and up of a layer's expert ([2I, H]): gu_tscale, I.
+ *   y  bf16 or fp32 [R, K] device (y_type), written
+ *   Shapes: as nvfp4_quantize_rows, but K <= NVFP4_MAX_PRODUCT_K; scale_rows >= 1.
+ */
+NVFP4_API nvfp4_status nvfp4_dequantize_rows(const uint8_t* packed, const uint8_t* scales, const float* scale,
+                                             int32_t scale_rows, int32_t R, int32_t K, void* y, int32_t y_type,
+                                             void* stream);
+
+/*
+ * rmsnorm_residual - the residual add and the (1 + w) RMSNorm in front of a layer made of the products:
+ *   h_out = bf16(h + delta)            (h itself without delta)
+ *   x     = h_out / sqrt(mean_i h_out[t,i]^2 + eps) * (1 + norm_w)
+ *   with x written once, in the form that out says: rounded to bf16, or quantised from its fp32 value as
+ *   fp8_quantize_block128 and nvfp4_quantize_rows say (their nearest values, decided in fp32 here).
+ *   Defined by: as moe_layer_forward_residual's norm (tutorials index, row 01; write-up, "Fused Kernels").
+ *   h      bf16 [T, H] device;  delta  bf16 [T, H] device or NULL;  norm_w  bf16 [H] device
+ *   h_out  bf16 [T, H] device, written; may be h or delta. NULL without delta.
+ *   out    rows [T, H]; overlaps no input
+ *   Shapes: T >= 0, 8 <= H <= NVFP4_MAX_ROW_K, H a multiple of 8 (bf16), 16 (fp8) or 32 (NVFP4). eps >= 0.
+ *   T == 0 enqueues nothing.
+ */
+NVFP4_API nvfp4_status rmsnorm_residual(const uint16_t* h, const uint16_t* delta, const uint16_t* norm_w, float eps,
+                                        int32_t T, int32_t H, uint16_t* h_out, const nvfp4_rows* out, void* stream);
+
+/*
+ * moe_swiglu - between the gate/up and the down product: x[r,i] = silu(gu[r,i]) * gu[r,I+i], written as
+ * rmsnorm_residual writes its rows.
+ *   Defined by: lynn-engine README, P28 note (gate/up + SiLU yields a [top_k, I] intermediate).
+ *   gu  bf16 or fp32 [R, 2I] device (gu_type: NVFP4_OUT_BF16 or NVFP4_OUT_F32), the rows of a product over
+ *       [gate; up]
+ *   out rows [R, I]; overlaps no input
+ *   Shapes: R >= 0, 8 <= I <= NVFP4_MAX_ROW_K, I a multiple of 8 (bf16), 16 (fp8) or 32 (NVFP4).
+ *   R == 0 enqueues nothing.
+ */
+NVFP4_API nvfp4_status moe_swiglu(const void* gu, int32_t gu_type, int32_t R, int32_t I, const nvfp4_rows* out,
+                                  void* stream);
+
+/*
+ * nvfp4_gemm_w4a4 - dense product of NVFP4 rows and an NVFP4 matrix:
+ *   y[t,n] = x_row_scales[t] * tensor_scale * sum_b x_scales[t,b] * w_scales[n,b] * sum_{k in b} x[t,k] * w[n,k]
+ *   over the blocks b of 16 columns; the tensor cores' fp32 sums, one rounding to the output type.
+ *   The two fp32 scales are multiplied first, so their product has to be in fp32's normal range, or 0.
+ *   Defined by: nvfp4_gemv_w4a16 with the activations of nvfp4_quantize_rows (any number of rows).
+ *   x  uint8 [T, K/2], x_scales uint8 [T, K/16], x_row_scales fp32 [T] device
+ *   W  NVFP4 matrix with E4M3 scales (other kinds: NVFP4_ERR_UNSUPPORTED_SHAPE), as nvfp4_pack writes it
+ *   y  bf16 or fp32 [T, N] device (y_type), written; overlaps no input
+ *   workspace  as for fp8_gemm_block128, and launched as it is.
+ *   Block scales are E4M3 codes without a sign.
+ *   Shapes: 0 <= T <= NVFP4_MAX_PRODUCT_ROWS, 1 <= N <= 2^22, K >= 32, K % 32 == 0, K <= NVFP4_MAX_PRODUCT_K.
+ *   Packed codes 16-byte aligned, block scales 16-byte, fp32 scales 4-byte. T == 0 enqueues nothing.
+ */
+NVFP4_API nvfp4_status nvfp4_gemm_w4a4(const uint8_t* x, const uint8_t* x_scales, const float* x_row_scales, int32_t T,
+                                       const nvfp4_weight* W, void* y, int32_t y_type, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/*
+ * moe_grouped_gemm_nvfp4 - moe_grouped_gemm_bf16 over experts in NVFP4, for NVFP4 rows: a layer's own arrays.
+ *   x  uint8 [rows, K/2], x_scales uint8 [rows, K/16], x_row_scales fp32 [rows] (rows: R, or R/k with gather)
+ *   w  uint8 [E, N, K/2], w_scales uint8 E4M3 [E, N, K/16], w_tscale fp32 [E, w_parts]: rows n of an expert in
+ *      w_parts equal runs, one tensor scale each (gu_*: N = 2I, w_parts 2; dn_*: N = H, w_parts 1)
+ *   Everything else as moe_grouped_gemm_bf16 and nvfp4_gemm_w4a4 say. N % w_parts == 0, w_parts >= 1.
+ */
+NVFP4_API nvfp4_status moe_grouped_gemm_nvfp4(const moe_groups* g, const uint8_t* x, const uint8_t* x_scales,
+                                              const float* x_row_scales, const uint8_t* w, const uint8_t* w_scales,
+                                              const float* w_tscale, int32_t w_parts, int32_t N, int32_t K, void* y,
+                                              int32_t y_type, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_permute - tokens sorted by expert: rows[r] = x[token_list[r] / k], and where each entry went:
+ * positions[token_list[r]] = r.
+ *   Defined by: lynn-engine README, P35 note (sorted-router contract) over moe_route_topk's list.
+ *   x           bf16 or fp32 [T, N] device (type: nvfp4_out_type)
+ *   token_list  int32 [T*k] device;  rows  like x [T*k, N] device or NULL (positions alone)
+ *   positions   int32 [T*k] device, written
+ *   A list entry outside [0, T*k) gives a row of zeros. Positions of entries that the list does not name are
+ *   left as they were (set them to -1 where a list leaves entries out); of one that it names twice either.
+ *   Its gradient: d_x = moe_combine of d_rows without weights.
+ *   Shapes: T >= 0, k >= 1, T * k <= NVFP4_MAX_PRODUCT_ROWS, 1 <= N <= 2^22. T == 0 enqueues nothing.
+ */
+NVFP4_API nvfp4_status moe_permute(const void* x, int32_t type, const int32_t* token_list, int32_t T, int32_t k,
+                                   int32_t N, void* rows, int32_t* positions, void* stream);
+
+/*
+ * moe_combine - the experts' rows back to their tokens with the router's weights:
+ *   y[t] = add[t] + sum_j w[t,j] * rows[positions[t*k + j]]
+ *   in fp32, the products added in the order of j, then add; one rounding to y's type.
+ *   Defined by: lynn-engine README, P29 note (routing-weighted sum), P46/P48 notes (no float atomics).
+ *   rows       bf16 or fp32 [T*k, N] device (rows_type)
+ *   w          fp32 [T, k] device or NULL (all 1)
+ *   positions  int32 [T*k] device, or NULL: entry t*k + j is row t*k + j (a product's scatter). A position
+ *              outside [0, T*k) adds nothing.
+ *   add        bf16 [T, N] device or NULL (the residual stream, a shared expert)
+ *   y          bf16 or fp32 [T, N] device (y_type), written; may be add where y is bf16, overlaps nothing else
+ *   Shapes: as moe_permute.
+ */
+NVFP4_API nvfp4_status moe_combine(const void* rows, int32_t rows_type, const float* w, const int32_t* positions,
+                                   const uint16_t* add, int32_t T, int32_t k, int32_t N, void* y, int32_t y_type,
+                                   void* stream);
+
+/*
+ * moe_combine_backward - the gradients of moe_combine (add's is dy itself). With p = positions[t*k + j], or
+ * t*k + j without positions:
+ *   d_rows[p] = w[t,j] * dy[t]   rounded to the rows' type;   d_w[t,j] = sum_n dy[t,n] * rows[p,n]   in fp32, in a
+ *   fixed order. A position outside [0, T*k) writes no row and has d_w 0; rows that no position names are left
+ *   as they were; one that two entries name is either's.
+ *   dy      bf16 or fp32 [T, N] device (dy_type);  rows  as moe_combine's (NULL where d_w is NULL)
+ *   w       fp32 [T, k] device or NULL (all 1)
+ *   d_rows  like rows, written, or NULL;  d_w  fp32 [T, k], written, or NULL. d_rows may be rows.
+ *   Shapes: as moe_permute.
+ */
+NVFP4_API nvfp4_status moe_combine_backward(const void* dy, int32_t dy_type, const void* rows, int32_t rows_type,
+                                            const float* w, const int32_t* positions, int32_t T, int32_t k, int32_t N,
+                                            void* d_rows, float* d_w, void* stream);
 
 /*
  * moe_layer_forward_noalloc - the same layer as moe_layer_forward, for callers

@@ -8,7 +8,9 @@ raises.
 
 The function names are those of the C ABI in ``include/nvfp4moe.h``:
 ``nvfp4_pack``, ``nvfp4_gemv_w4a16``, ``moe_route_topk``, ``moe_layer_forward``,
-``fp8_quantize_block128``, ``fp8_gemm_block128``, ``moe_grouped_gemm_bf16``, ``moe_grouped_gemm_fp8``.
+``fp8_quantize_block128``, ``fp8_gemm_block128``, ``moe_grouped_gemm_bf16``, ``moe_grouped_gemm_fp8``,
+``nvfp4_quantize_rows``, ``nvfp4_dequantize_rows``, ``nvfp4_gemm_w4a4``, ``moe_grouped_gemm_nvfp4``,
+``rmsnorm_residual``, ``moe_swiglu``, ``moe_permute``, ``moe_combine``, ``moe_combine_backward``.
 """
 from __future__ import annotations
 
@@ -27,6 +29,11 @@ SCALE_E4M3 = 0
 SCALE_FP16 = 1
 SCALE_FP32 = 2     # fp32 scale per 16 elements
 SCALE_UE8M0 = 3    # E8M0 power-of-two scale per 32 elements
+
+# forms of the rows that rmsnorm_residual and moe_swiglu write
+ROWS_BF16 = 0
+ROWS_FP8 = 1       # E4M3 codes, an fp32 scale per 1 x 128
+ROWS_NVFP4 = 2     # E2M1 codes, an E4M3 scale per 16, an fp32 scale per row
 
 
 def scale_shape(rows: int, K: int, kind: int):
@@ -146,6 +153,24 @@ lib.moe_grouped_gemm_bf16.restype = _i32
 lib.moe_grouped_gemm_bf16.argtypes = [_P, _P, _P, _i32, _i32, _P, _i32, _P, _sz, _P]
 lib.moe_grouped_gemm_fp8.restype = _i32
 lib.moe_grouped_gemm_fp8.argtypes = [_P, _P, _P, _P, _P, _i32, _i32, _P, _i32, _P, _sz, _P]
+lib.nvfp4_quantize_rows.restype = _i32
+lib.nvfp4_quantize_rows.argtypes = [_P, _i32, _i32, _P, _P, _P, _P]
+lib.nvfp4_dequantize_rows.restype = _i32
+lib.nvfp4_dequantize_rows.argtypes = [_P, _P, _P, _i32, _i32, _i32, _P, _i32, _P]
+lib.rmsnorm_residual.restype = _i32
+lib.rmsnorm_residual.argtypes = [_P, _P, _P, ctypes.c_float, _i32, _i32, _P, _P, _P]
+lib.moe_swiglu.restype = _i32
+lib.moe_swiglu.argtypes = [_P, _i32, _i32, _i32, _P, _P]
+lib.nvfp4_gemm_w4a4.restype = _i32
+lib.nvfp4_gemm_w4a4.argtypes = [_P, _P, _P, _i32, _P, _P, _i32, _P, _sz, _P]
+lib.moe_grouped_gemm_nvfp4.restype = _i32
+lib.moe_grouped_gemm_nvfp4.argtypes = [_P, _P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _P, _i32, _P, _sz, _P]
+lib.moe_permute.restype = _i32
+lib.moe_permute.argtypes = [_P, _i32, _P, _i32, _i32, _i32, _P, _P, _P]
+lib.moe_combine.restype = _i32
+lib.moe_combine.argtypes = [_P, _i32, _P, _P, _P, _i32, _i32, _i32, _P, _i32, _P]
+lib.moe_combine_backward.restype = _i32
+lib.moe_combine_backward.argtypes = [_P, _i32, _P, _i32, _P, _P, _i32, _i32, _i32, _P, _P, _P]
 lib.moe_layer_forward_noalloc.restype = _i32
 lib.moe_layer_forward_noalloc.argtypes = [ctypes.POINTER(MoELayerDescC), _P, _i32, _P, _P, _P, _P]
 lib.nvfp4_noalloc_status.restype = _i32
@@ -288,13 +313,15 @@ def moe_route_topk(logits: torch.Tensor, k: int, stream=None):
 # ---------------------------------------------------------------- 8-bit and grouped products
 
 # names looked up once: a call spends as long on attributes of torch as on its launch otherwise
-_BF16, _F32, _F8, _I32 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32
+_BF16, _F32, _F8, _I32, _U8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32, torch.uint8
 # x is on a device when these are called, so CUDA is initialised. The public calls, on which a torch without CUDA
 # falls back, cost more (torch.cuda.current_stream builds an object: 2 us).
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
 _OUT_TYPE = {_BF16: 0, _F32: 1}
 _GROUPS = struct.Struct("@5iPP")     # moe_groups; packing it costs half of filling a ctypes structure
+_ROWS = struct.Struct("@iPPP")       # nvfp4_rows
+_WEIGHT = struct.Struct("@PPP3i4x")  # nvfp4_weight
 
 
 def _refuse(where: str, why: str, status: int = NVFP4_ERR_INVALID_ARG):
@@ -405,15 +432,13 @@ def fp8_gemm_block128(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, 
     return y
 
 
-def _grouped(where, fn, x, x_scales, w, w_scales, dtype, offsets, token_list, k, gather, scatter, y, out_dtype, ws,
-             stream):
-    px, (rows, K), dev = _first(x, dtype, where)
-    wshape = w.shape
-    if len(wshape) != 3:
+def _groups(where, rows, dev, w_shape, offsets, token_list, k, gather, scatter):
+    """(list positions, moe_groups) of a grouped product whose x has this many rows."""
+    if len(w_shape) != 3:
         _refuse(where, "w must be [E, N, K]")
-    E, N, _ = wshape
+    E, N, _ = w_shape
     if E > 0x7FFFFFFF or N > 0x7FFFFFFF:
-        _refuse(where, "w has shape %s" % (tuple(wshape),), NVFP4_ERR_UNSUPPORTED_SHAPE)
+        _refuse(where, "w has shape %s" % (tuple(w_shape),), NVFP4_ERR_UNSUPPORTED_SHAPE)
     if k < 1:
         _refuse(where, "k must be at least 1")
     R = rows * k if gather else rows
@@ -425,14 +450,27 @@ def _grouped(where, fn, x, x_scales, w, w_scales, dtype, offsets, token_list, k,
         _refuse(where, "gather and scatter need token_list")
     else:
         pl = 0
-    groups = _GROUPS.pack(R, E, k, 1 if gather else 0, 1 if scatter else 0,
-                          _operand(offsets, _I32, (E + 1,), dev, where, "offsets"), pl)
+    return R, _GROUPS.pack(R, E, k, 1 if gather else 0, 1 if scatter else 0,
+                           _operand(offsets, _I32, (E + 1,), dev, where, "offsets"), pl)
+
+
+def _product_out(where, y, shape, out_dtype, like, stream):
+    """(y, its type for the C ABI), y made where the caller brought none."""
     if y is None:
-        y = _output((R, N), out_dtype, x.device, stream)
-    out_dtype = y.dtype
-    out_type = _OUT_TYPE.get(out_dtype)
+        y = _output(shape, out_dtype, like.device, stream)
+    out_type = _OUT_TYPE.get(y.dtype)
     if out_type is None:
-        _refuse(where, "the output is bfloat16 or float32, not %s" % out_dtype)
+        _refuse(where, "the output is bfloat16 or float32, not %s" % y.dtype)
+    return y, out_type
+
+
+def _grouped(where, fn, x, x_scales, w, w_scales, dtype, offsets, token_list, k, gather, scatter, y, out_dtype, ws,
+             stream):
+    px, (rows, K), dev = _first(x, dtype, where)
+    wshape = w.shape
+    R, groups = _groups(where, rows, dev, wshape, offsets, token_list, k, gather, scatter)
+    E, N, _ = wshape
+    y, out_type = _product_out(where, y, (R, N), out_dtype, x, stream)
     pws, nws = (None, 0) if ws is None else _status_word(ws, dev, where)
     pw = _operand(w, dtype, (E, N, K), dev, where, "w")
     if w_scales is None:
@@ -441,7 +479,7 @@ def _grouped(where, fn, x, x_scales, w, w_scales, dtype, offsets, token_list, k,
         KB = (K + 127) // 128
         operands = (px, _operand(x_scales, _F32, (rows, KB), dev, where, "x_scales"), pw,
                     _operand(w_scales, _F32, (E, (N + 127) // 128, KB), dev, where, "w_scales"))
-    _enqueue(fn, where, dev, stream, groups, *operands, N, K, _operand(y, out_dtype, (R, N), dev, where, "y"),
+    _enqueue(fn, where, dev, stream, groups, *operands, N, K, _operand(y, y.dtype, (R, N), dev, where, "y"),
              out_type, pws, nws)
     return y
 
@@ -467,6 +505,257 @@ def moe_grouped_gemm_fp8(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tenso
     [rows of x, ceil(K/128)], w_scales [E, ceil(N/128), ceil(K/128)]."""
     return _grouped("moe_grouped_gemm_fp8", lib.moe_grouped_gemm_fp8, x, x_scales, w, w_scales, _F8,
                     offsets, token_list, k, gather, scatter, y, out_dtype, ws, stream)
+
+
+# ---------------------------------------------------------------- NVFP4 rows and their products
+
+def _empty_rows(kind: int, R: int, K: int, device, stream):
+    if kind == ROWS_BF16:
+        return _output((R, K), _BF16, device, stream)
+    if kind == ROWS_FP8:
+        return _output((R, K), _F8, device, stream), _output((R, (K + 127) // 128), _F32, device, stream)
+    return (_output((R, K // 2), _U8, device, stream), _output((R, K // 16), _U8, device, stream),
+            _output((R,), _F32, device, stream))
+
+
+def _rows_out(where: str, kind: int, out, R: int, K: int, index: int):
+    """nvfp4_rows of the caller's output tensors, which have to fit rows [R, K] of this kind."""
+    if kind == ROWS_BF16:
+        return _ROWS.pack(kind, _operand(out, _BF16, (R, K), index, where, "out"), 0, 0)
+    if kind == ROWS_FP8:
+        data, scales = out
+        return _ROWS.pack(kind, _operand(data, _F8, (R, K), index, where, "the codes"),
+                          _operand(scales, _F32, (R, (K + 127) // 128), index, where, "the scales"), 0)
+    data, scales, row_scales = out
+    return _ROWS.pack(kind, _operand(data, _U8, (R, K // 2), index, where, "the codes"),
+                      _operand(scales, _U8, (R, K // 16), index, where, "the block scales"),
+                      _operand(row_scales, _F32, (R,), index, where, "the row scales"))
+
+
+def _rows_kind(where: str, kind: int, out):
+    if kind not in (ROWS_BF16, ROWS_FP8, ROWS_NVFP4):
+        _refuse(where, "kind must be ROWS_BF16, ROWS_FP8 or ROWS_NVFP4")
+    if out is not None and kind != ROWS_BF16 and (not isinstance(out, (tuple, list)) or len(out) != kind + 1):
+        _refuse(where, "out must be a tuple of %d tensors" % (kind + 1))
+
+
+def nvfp4_quantize_rows(x: torch.Tensor, out=None, stream=None):
+    """(codes uint8 [R, K/2], E4M3 block scales uint8 [R, K/16], row scales fp32 [R]) of bf16 x [R, K]: the
+    activations of ``nvfp4_gemm_w4a4`` and ``moe_grouped_gemm_nvfp4``. ``out``: the three tensors to write."""
+    where = "nvfp4_quantize_rows"
+    px, (R, K), dev = _first(x, _BF16, where)
+    _rows_kind(where, ROWS_NVFP4, out)
+    if out is None:
+        out = _empty_rows(ROWS_NVFP4, R, K, x.device, stream)
+    packed, scales, row_scales = out
+    _enqueue(lib.nvfp4_quantize_rows, where, dev, stream, px, R, K, _operand(packed, _U8, (R, K // 2), dev, where, "the codes"),
+             _operand(scales, _U8, (R, K // 16), dev, where, "the block scales"),
+             _operand(row_scales, _F32, (R,), dev, where, "the row scales"))
+    return packed, scales, row_scales
+
+
+def nvfp4_dequantize_rows(packed: torch.Tensor, scales: torch.Tensor, scale: torch.Tensor,
+                          y: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, stream=None):
+    """y [R, K] (bf16 or fp32) = code * block scale * fp32 scale of packed uint8 [R, K/2], scales uint8 [R, K/16].
+    ``scale`` fp32: one for each run of R / len(scale) rows (rows of ``nvfp4_quantize_rows``: one a row; a packed
+    matrix: its tensor scale; gate and up of an expert: gu_tscale[e])."""
+    where = "nvfp4_dequantize_rows"
+    px, (R, half), dev = _first(packed, _U8, where)
+    K, count = 2 * half, scale.numel()
+    if K > 0x7FFFFFFF:
+        _refuse(where, "x has shape %s" % (tuple(packed.shape),), NVFP4_ERR_UNSUPPORTED_SHAPE)
+    if R > 0 and (count < 1 or R % count != 0):
+        _refuse(where, "%d scales do not divide %d rows" % (count, R))
+    y, out_type = _product_out(where, y, (R, K), out_dtype, packed, stream)
+    _enqueue(lib.nvfp4_dequantize_rows, where, dev, stream, px, _operand(scales, _U8, (R, K // 16), dev, where, "scales"),
+             _operand(scale, _F32, scale.shape, dev, where, "scale"), R // count if R > 0 else 1, R, K,
+             _operand(y, y.dtype, (R, K), dev, where, "y"), out_type)
+    return y
+
+
+def nvfp4_gemm_w4a4(x: torch.Tensor, x_scales: torch.Tensor, x_row_scales: torch.Tensor, W: NVFP4Weight,
+                    y: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, ws: Optional[Workspace] = None,
+                    stream=None):
+    """y [T, N] (bf16 or fp32) = x W^T for the NVFP4 rows x (codes uint8 [T, K/2], block scales [T, K/16], row scales
+    [T], as ``nvfp4_quantize_rows`` returns them) and a matrix of ``nvfp4_pack`` with E4M3 scales.
+    ``ws`` (optional) receives a device wait that ran out in its status word."""
+    where = "nvfp4_gemm_w4a4"
+    px, (T, half), dev = _first(x, _U8, where)
+    N, K = W.N, W.K
+    if half * 2 != K:
+        _refuse(where, "x has %d columns, W %d" % (2 * half, K))
+    if not 0 < N <= 0x7FFFFFFF or K > 0x7FFFFFFF:
+        _refuse(where, "W is [%d, %d]" % (N, K), NVFP4_ERR_UNSUPPORTED_SHAPE)
+    if W.kind != SCALE_E4M3:
+        _refuse(where, "W has scales of kind %d, not SCALE_E4M3" % W.kind, NVFP4_ERR_UNSUPPORTED_SHAPE)
+    y, out_type = _product_out(where, y, (T, N), out_dtype, x, stream)
+    pws, nws = (None, 0) if ws is None else _status_word(ws, dev, where)
+    wt = W.tensor_scale
+    weight = _WEIGHT.pack(_operand(W.packed, _U8, (N, half), dev, where, "W.packed"),
+                          _operand(W.scales, _U8, (N, K // 16), dev, where, "W.scales"),
+                          _operand(wt, _F32, (1,), dev, where, "W.tensor_scale"), N, K, W.kind)
+    _enqueue(lib.nvfp4_gemm_w4a4, where, dev, stream, px, _operand(x_scales, _U8, (T, K // 16), dev, where, "x_scales"),
+             _operand(x_row_scales, _F32, (T,), dev, where, "x_row_scales"), T, weight,
+             _operand(y, y.dtype, (T, N), dev, where, "y"), out_type, pws, nws)
+    return y
+
+
+def moe_grouped_gemm_nvfp4(x: torch.Tensor, x_scales: torch.Tensor, x_row_scales: torch.Tensor, w: torch.Tensor,
+                           w_scales: torch.Tensor, w_tscale: torch.Tensor, offsets: torch.Tensor,
+                           token_list: Optional[torch.Tensor] = None, k: int = 1, gather: bool = False,
+                           scatter: bool = False, y: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                           ws: Optional[Workspace] = None, stream=None):
+    """``moe_grouped_gemm_bf16`` of NVFP4 rows x (as ``nvfp4_gemm_w4a4``'s) and NVFP4 experts in a layer's own arrays:
+    w uint8 [E, N, K/2], w_scales uint8 [E, N, K/16] (E4M3) and w_tscale fp32 [E] or [E, parts], the tensor scales of
+    `parts` equal runs of an expert's rows (gu_packed, gu_scales, gu_tscale; dn_packed, dn_scales, dn_tscale)."""
+    where = "moe_grouped_gemm_nvfp4"
+    px, (rows, half), dev = _first(x, _U8, where)
+    wshape = w.shape
+    R, groups = _groups(where, rows, dev, wshape, offsets, token_list, k, gather, scatter)
+    E, N, _ = wshape
+    K, tshape = 2 * half, w_tscale.shape
+    if K > 0x7FFFFFFF:
+        _refuse(where, "x has shape %s" % (tuple(x.shape),), NVFP4_ERR_UNSUPPORTED_SHAPE)
+    if len(tshape) not in (1, 2):
+        _refuse(where, "w_tscale must be [E] or [E, parts]")
+    parts = tshape[1] if len(tshape) == 2 else 1
+    y, out_type = _product_out(where, y, (R, N), out_dtype, x, stream)
+    pws, nws = (None, 0) if ws is None else _status_word(ws, dev, where)
+    _enqueue(lib.moe_grouped_gemm_nvfp4, where, dev, stream, groups, px,
+             _operand(x_scales, _U8, (rows, K // 16), dev, where, "x_scales"),
+             _operand(x_row_scales, _F32, (rows,), dev, where, "x_row_scales"),
+             _operand(w, _U8, (E, N, half), dev, where, "w"),
+             _operand(w_scales, _U8, (E, N, K // 16), dev, where, "w_scales"),
+             _operand(w_tscale, _F32, (E,) if len(tshape) == 1 else (E, parts), dev, where, "w_tscale"), parts, N, K,
+             _operand(y, y.dtype, (R, N), dev, where, "y"), out_type, pws, nws)
+    return y
+
+
+# ---------------------------------------------------------------- norm and SwiGLU into rows of a product
+
+def rmsnorm_residual(h: torch.Tensor, norm_w: torch.Tensor, eps: float = 1e-6, delta: Optional[torch.Tensor] = None,
+                     kind: int = ROWS_BF16, h_out: Optional[torch.Tensor] = None, out=None, stream=None):
+    """(h_out, rows): h_out = h + delta (bf16 [T, H]; h itself without ``delta`` and ``h_out``) and the RMSNorm of its
+    rows in the (1 + norm_w) form, as ``kind`` says: ROWS_BF16 a bf16 tensor, ROWS_FP8 (codes, scales) as
+    ``fp8_quantize_block128``, ROWS_NVFP4 (codes, block scales, row scales) as ``nvfp4_quantize_rows``.
+    ``h_out`` may be h or delta; ``out``: the tensor or tensors to write the rows to."""
+    where = "rmsnorm_residual"
+    ph, shape, dev = _first(h, _BF16, where)
+    T, H = shape
+    _rows_kind(where, kind, out)
+    if delta is not None and h_out is None:
+        h_out = _output(shape, _BF16, h.device, stream)
+    if out is None:
+        out = _empty_rows(kind, T, H, h.device, stream)
+    _enqueue(lib.rmsnorm_residual, where, dev, stream, ph,
+             None if delta is None else _operand(delta, _BF16, shape, dev, where, "delta"),
+             _operand(norm_w, _BF16, (H,), dev, where, "norm_w"), eps, T, H,
+             None if h_out is None else _operand(h_out, _BF16, shape, dev, where, "h_out"),
+             _rows_out(where, kind, out, T, H, dev))
+    return (h if h_out is None else h_out), out
+
+
+def moe_swiglu(gu: torch.Tensor, kind: int = ROWS_BF16, out=None, stream=None):
+    """Rows [R, I] of silu(gu[:, :I]) * gu[:, I:] for bf16 or fp32 gu [R, 2I], as ``kind`` says (see
+    ``rmsnorm_residual``)."""
+    where = "moe_swiglu"
+    dtype = gu.dtype
+    gu_type = _OUT_TYPE.get(dtype)
+    if gu_type is None:
+        _refuse(where, "gu is bfloat16 or float32, not %s" % dtype)
+    pg, (R, width), dev = _first(gu, dtype, where)
+    if width % 2 != 0:
+        _refuse(where, "gu has %d columns" % width, NVFP4_ERR_UNSUPPORTED_SHAPE)
+    _rows_kind(where, kind, out)
+    if out is None:
+        out = _empty_rows(kind, R, width // 2, gu.device, stream)
+    _enqueue(lib.moe_swiglu, where, dev, stream, pg, gu_type, R, width // 2,
+             _rows_out(where, kind, out, R, width // 2, dev))
+    return out
+
+
+# ---------------------------------------------------------------- rows sorted by expert and back
+
+def _typed(t: torch.Tensor, where: str, name: str):
+    """(address, shape, device index, type) of a bf16 or fp32 matrix."""
+    type_ = _OUT_TYPE.get(t.dtype)
+    if type_ is None:
+        _refuse(where, "%s is bfloat16 or float32, not %s" % (name, t.dtype))
+    return (*_first(t, t.dtype, where), type_)
+
+
+def _entries(where: str, T: int, k: int):
+    if k < 1 or T * k > 0x7FFFFFFF:
+        _refuse(where, "%d tokens with %d entries each" % (T, k), NVFP4_ERR_UNSUPPORTED_SHAPE)
+    return T * k
+
+
+def moe_permute(x: torch.Tensor, token_list: torch.Tensor, k: int, rows: Optional[torch.Tensor] = None,
+                positions: Optional[torch.Tensor] = None, stream=None):
+    """(rows [T*k, N] = x[token_list / k], positions int32 [T*k]: the row of each entry t*k + j) for bf16 or fp32 x
+    [T, N] and the entry list of ``moe_route_topk``. Positions of entries that the list does not name are left as they
+    were (in a new tensor: -1)."""
+    where = "moe_permute"
+    px, (T, N), dev, type_ = _typed(x, where, "x")
+    R = _entries(where, T, k)
+    if rows is None:
+        rows = _output((R, N), x.dtype, x.device, stream)
+    if positions is None:
+        positions = _output((R,), _I32, x.device, stream)
+        with torch.cuda.stream(stream):
+            positions.fill_(-1)
+    _enqueue(lib.moe_permute, where, dev, stream, px, type_, _operand(token_list, _I32, (R,), dev, where, "token_list"),
+             T, k, N, _operand(rows, x.dtype, (R, N), dev, where, "rows"),
+             _operand(positions, _I32, (R,), dev, where, "positions"))
+    return rows, positions
+
+
+def moe_combine(rows: torch.Tensor, k: int, w: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                add: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                stream=None):
+    """y [T, N] (bf16 or fp32) = add[t] + sum_j w[t, j] rows[positions[t*k + j]] for bf16 or fp32 rows [T*k, N].
+    Without ``positions`` rows are in entry order (a product's scatter); without ``w`` all weights are 1, which is the
+    gradient of ``moe_permute``. ``add`` bf16 [T, N]; y may be add."""
+    where = "moe_combine"
+    px, (R, N), dev, type_ = _typed(rows, where, "rows")
+    if k < 1 or R % k != 0:
+        _refuse(where, "%d rows are no multiple of k = %d" % (R, k), NVFP4_ERR_UNSUPPORTED_SHAPE)
+    T = R // k
+    y, out_type = _product_out(where, y, (T, N), out_dtype, rows, stream)
+    _enqueue(lib.moe_combine, where, dev, stream, px, type_, None if w is None else _operand(w, _F32, (T, k), dev, where, "w"),
+             None if positions is None else _operand(positions, _I32, (R,), dev, where, "positions"),
+             None if add is None else _operand(add, _BF16, (T, N), dev, where, "add"), T, k, N,
+             _operand(y, y.dtype, (T, N), dev, where, "y"), out_type)
+    return y
+
+
+def moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor, w: Optional[torch.Tensor] = None,
+                         positions: Optional[torch.Tensor] = None, d_rows: Optional[torch.Tensor] = None,
+                         d_w: Optional[torch.Tensor] = None, stream=None):
+    """(d_rows like rows, d_w fp32 [T, k]) of ``moe_combine`` for dy [T, N] (bf16 or fp32). A new d_rows holds zeros in
+    rows that no position names; one that is passed keeps what it had there (it may be rows)."""
+    where = "moe_combine_backward"
+    px, (T, N), dev, type_ = _typed(dy, where, "dy")
+    rows_type = _OUT_TYPE.get(rows.dtype)
+    if rows_type is None:
+        _refuse(where, "rows is bfloat16 or float32, not %s" % rows.dtype)
+    R = rows.shape[0] if rows.dim() == 2 else 0
+    if T > 0 and (R < T or R % T != 0):
+        _refuse(where, "rows has shape %s for %d tokens" % (tuple(rows.shape), T), NVFP4_ERR_UNSUPPORTED_SHAPE)
+    k = R // T if T > 0 else 1 if w is None else w.shape[-1]
+    _entries(where, T, k)
+    if d_rows is None:
+        d_rows = _output((R, N), rows.dtype, dy.device, stream)
+        if positions is not None:
+            with torch.cuda.stream(stream):
+                d_rows.zero_()
+    if d_w is None:
+        d_w = _output((T, k), _F32, dy.device, stream)
+    _enqueue(lib.moe_combine_backward, where, dev, stream, px, type_, _operand(rows, rows.dtype, (R, N), dev, where, "rows"),
+             rows_type, None if w is None else _operand(w, _F32, (T, k), dev, where, "w"),
+             None if positions is None else _operand(positions, _I32, (R,), dev, where, "positions"), T, k, N,
+             _operand(d_rows, rows.dtype, (R, N), dev, where, "d_rows"), _operand(d_w, _F32, (T, k), dev, where, "d_w"))
+    return d_rows, d_w
 
 
 # ---------------------------------------------------------------- layer

@@ -157,21 +157,75 @@ nvfp4_status run_product(RowsProduct P, bool fp8, int32_t y_type, void* workspac
                                     static_cast<cudaStream_t>(stream)));
 }
 
-nvfp4_status run_grouped(const moe_groups* g, const void* x, const float* xs, const void* w, const float* ws,
-                         bool fp8, int32_t N, int32_t K, void* y, int32_t y_type, void* workspace,
-                         size_t workspace_bytes, void* stream) {
+// The groups of a call, checked, in P.
+nvfp4_status fill_groups(const moe_groups* g, RowsProduct* P) {
     if (!g) return NVFP4_ERR_INVALID_ARG;
     if (g->E < 1 || g->E > NVFP4_MAX_EXPERTS || g->k < 1 || g->R < 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
     if (g->gather && g->R % g->k != 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
     if (g->R > 0 && (!g->expert_offsets || ((g->gather || g->scatter) && !g->token_list)))
         return NVFP4_ERR_INVALID_ARG;
     if (!aligned4(g->expert_offsets) || !aligned4(g->token_list)) return NVFP4_ERR_MISALIGNED;
+    P->offsets = g->expert_offsets, P->list = g->token_list;
+    P->R = g->R, P->E = g->E, P->k = g->k;
+    P->gather = g->gather != 0, P->scatter = g->scatter != 0;
+    return NVFP4_OK;
+}
+
+nvfp4_status run_grouped(const moe_groups* g, const void* x, const float* xs, const void* w, const float* ws,
+                         bool fp8, int32_t N, int32_t K, void* y, int32_t y_type, void* workspace,
+                         size_t workspace_bytes, void* stream) {
     RowsProduct P{};
-    P.x = x, P.xs = xs, P.w = w, P.ws = ws, P.y = y;
-    P.offsets = g->expert_offsets, P.list = g->token_list;
-    P.R = g->R, P.E = g->E, P.N = N, P.K = K, P.k = g->k;
-    P.gather = g->gather != 0, P.scatter = g->scatter != 0;
+    if (nvfp4_status st = fill_groups(g, &P); st != NVFP4_OK) return st;
+    P.x = x, P.xs = xs, P.w = w, P.ws = ws, P.y = y, P.N = N, P.K = K;
     return run_product(P, fp8, y_type, workspace, workspace_bytes, stream);
+}
+
+// Where rows of K elements go; `empty`: there are none.
+nvfp4_status check_rows(const nvfp4_rows* out, int32_t K, bool empty) {
+    if (!out) return NVFP4_ERR_INVALID_ARG;
+    if (out->kind != NVFP4_ROWS_BF16 && out->kind != NVFP4_ROWS_FP8 && out->kind != NVFP4_ROWS_NVFP4)
+        return NVFP4_ERR_INVALID_ARG;
+    const int unit = out->kind == NVFP4_ROWS_BF16 ? 8 : out->kind == NVFP4_ROWS_FP8 ? 16 : 32;
+    if (K < unit || K % unit != 0 || K > NVFP4_MAX_ROW_K) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    const bool scales = out->kind != NVFP4_ROWS_BF16, rows = out->kind == NVFP4_ROWS_NVFP4;
+    if (!empty && (!out->data || (scales && !out->scales) || (rows && !out->row_scales))) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(out->data) || (scales && !(rows ? aligned16(out->scales) : aligned4(out->scales))) ||
+        (rows && !aligned4(out->row_scales)))
+        return NVFP4_ERR_MISALIGNED;
+    return NVFP4_OK;
+}
+
+// Checks and launch shared by the dense and the grouped NVFP4 product (as run_product).
+nvfp4_status run_nvfp4(Fp4Product P, int32_t y_type, void* workspace, size_t workspace_bytes, void* stream) {
+    RowsProduct& r = P.r;
+    if (y_type != NVFP4_OUT_BF16 && y_type != NVFP4_OUT_F32) return NVFP4_ERR_INVALID_ARG;
+    if (r.R < 0 || r.R > NVFP4_MAX_PRODUCT_ROWS) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (r.N < 1 || r.N > (1 << 22) || (long long)r.E * r.N > 0x7FFFFFFFll) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (P.parts < 1 || r.N % P.parts != 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (r.K < 32 || r.K % 32 != 0 || r.K > NVFP4_MAX_PRODUCT_K) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (workspace && !aligned16(workspace)) return NVFP4_ERR_MISALIGNED;
+    if (workspace && workspace_bytes < sizeof(WsHeader)) return NVFP4_ERR_WORKSPACE_TOO_SMALL;
+    if (r.R > 0) {
+        if (!r.x || !r.w || !r.y || !P.xs || !P.xr || !P.ws || !P.wt) return NVFP4_ERR_INVALID_ARG;
+        if (!aligned16(r.x) || !aligned16(r.w) || !aligned16(r.y) || !aligned16(P.xs) || !aligned16(P.ws) ||
+            !aligned4(P.xr) || !aligned4(P.wt))
+            return NVFP4_ERR_MISALIGNED;
+    }
+    r.x_rows = r.gather ? r.R / r.k : r.R;
+    r.y_f32 = y_type == NVFP4_OUT_F32;
+    DeviceInfo dev;
+    if (nvfp4_status st = device_info(&dev); st != NVFP4_OK) return st;
+    if (r.R == 0) return NVFP4_OK;
+    return from_cuda(launch_rows_fp4(P, static_cast<WsHeader*>(workspace), dev, g_wait_limit.load(),
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+bool out_type(int32_t t) { return t == NVFP4_OUT_BF16 || t == NVFP4_OUT_F32; }
+
+// Shape checks of the calls that take rows to tokens and back.
+nvfp4_status check_entries(int32_t T, int32_t k, int32_t N) {
+    if (T < 0 || k < 1 || (long long)T * k > NVFP4_MAX_PRODUCT_ROWS) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    return N < 1 || N > (1 << 22) ? NVFP4_ERR_UNSUPPORTED_SHAPE : NVFP4_OK;
 }
 
 }  // namespace
@@ -320,6 +374,123 @@ nvfp4_status moe_grouped_gemm_fp8(const moe_groups* g, const uint8_t* x, const f
                                   const float* w_scales, int32_t N, int32_t K, void* y, int32_t y_type,
                                   void* workspace, size_t workspace_bytes, void* stream) {
     return run_grouped(g, x, x_scales, w, w_scales, true, N, K, y, y_type, workspace, workspace_bytes, stream);
+}
+
+nvfp4_status nvfp4_quantize_rows(const uint16_t* x, int32_t R, int32_t K, uint8_t* packed, uint8_t* scales,
+                                 float* row_scales, void* stream) {
+    const nvfp4_rows out{NVFP4_ROWS_NVFP4, packed, scales, row_scales};
+    if (R < 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (nvfp4_status st = check_rows(&out, K, R == 0); st != NVFP4_OK) return st;
+    if (R > 0 && !x) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(x)) return NVFP4_ERR_MISALIGNED;
+    DeviceInfo dev;
+    if (nvfp4_status st = device_info(&dev); st != NVFP4_OK) return st;
+    if (R == 0) return NVFP4_OK;
+    return from_cuda(launch_quantize_rows(x, R, K, out, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_dequantize_rows(const uint8_t* packed, const uint8_t* scales, const float* scale,
+                                   int32_t scale_rows, int32_t R, int32_t K, void* y, int32_t y_type, void* stream) {
+    if (!out_type(y_type)) return NVFP4_ERR_INVALID_ARG;
+    if (R < 0 || scale_rows < 1) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (K < 32 || K % 32 != 0 || K > NVFP4_MAX_PRODUCT_K) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (R > 0 && (!packed || !scales || !scale || !y)) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(packed) || !aligned16(scales) || !aligned4(scale) || !aligned16(y)) return NVFP4_ERR_MISALIGNED;
+    DeviceInfo dev;
+    if (nvfp4_status st = device_info(&dev); st != NVFP4_OK) return st;
+    if (R == 0) return NVFP4_OK;
+    return from_cuda(launch_dequantize_rows(packed, scales, scale, scale_rows, R, K, y, y_type == NVFP4_OUT_F32,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status rmsnorm_residual(const uint16_t* h, const uint16_t* delta, const uint16_t* norm_w, float eps, int32_t T,
+                              int32_t H, uint16_t* h_out, const nvfp4_rows* out, void* stream) {
+    if (T < 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (nvfp4_status st = check_rows(out, H, T == 0); st != NVFP4_OK) return st;
+    if (!(eps >= 0.0f) || !(eps < 1.0e30f)) return NVFP4_ERR_INVALID_ARG;
+    if (!norm_w || (T > 0 && (!h || (delta && !h_out)))) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(h) || !aligned16(delta) || !aligned16(norm_w) || !aligned16(h_out)) return NVFP4_ERR_MISALIGNED;
+    DeviceInfo dev;
+    if (nvfp4_status st = device_info(&dev); st != NVFP4_OK) return st;
+    if (T == 0) return NVFP4_OK;
+    return from_cuda(launch_norm_rows(h, delta, norm_w, eps, T, H, h_out, *out, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status moe_swiglu(const void* gu, int32_t gu_type, int32_t R, int32_t I, const nvfp4_rows* out, void* stream) {
+    if (!out_type(gu_type)) return NVFP4_ERR_INVALID_ARG;
+    if (R < 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (nvfp4_status st = check_rows(out, I, R == 0); st != NVFP4_OK) return st;
+    if (R > 0 && !gu) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(gu)) return NVFP4_ERR_MISALIGNED;
+    DeviceInfo dev;
+    if (nvfp4_status st = device_info(&dev); st != NVFP4_OK) return st;
+    if (R == 0) return NVFP4_OK;
+    return from_cuda(launch_swiglu_rows(gu, gu_type == NVFP4_OUT_F32, R, I, *out, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_gemm_w4a4(const uint8_t* x, const uint8_t* x_scales, const float* x_row_scales, int32_t T,
+                             const nvfp4_weight* W, void* y, int32_t y_type, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+    if (!W || !known_kind(W->kind)) return NVFP4_ERR_INVALID_ARG;
+    if (W->kind != NVFP4_SCALE_E4M3) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    Fp4Product P{};
+    P.r.x = x, P.r.w = W->packed, P.r.y = y, P.r.R = T, P.r.E = 1, P.r.N = W->N, P.r.K = W->K, P.r.k = 1;
+    P.xs = x_scales, P.xr = x_row_scales, P.ws = static_cast<const uint8_t*>(W->scales), P.wt = W->tensor_scale;
+    P.parts = 1;
+    return run_nvfp4(P, y_type, workspace, workspace_bytes, stream);
+}
+
+nvfp4_status moe_grouped_gemm_nvfp4(const moe_groups* g, const uint8_t* x, const uint8_t* x_scales,
+                                    const float* x_row_scales, const uint8_t* w, const uint8_t* w_scales,
+                                    const float* w_tscale, int32_t w_parts, int32_t N, int32_t K, void* y,
+                                    int32_t y_type, void* workspace, size_t workspace_bytes, void* stream) {
+    Fp4Product P{};
+    if (nvfp4_status st = fill_groups(g, &P.r); st != NVFP4_OK) return st;
+    P.r.x = x, P.r.w = w, P.r.y = y, P.r.N = N, P.r.K = K;
+    P.xs = x_scales, P.xr = x_row_scales, P.ws = w_scales, P.wt = w_tscale, P.parts = w_parts;
+    return run_nvfp4(P, y_type, workspace, workspace_bytes, stream);
+}
+
+nvfp4_status moe_permute(const void* x, int32_t type, const int32_t* token_list, int32_t T, int32_t k, int32_t N,
+                         void* rows, int32_t* positions, void* stream) {
+    if (!out_type(type)) return NVFP4_ERR_INVALID_ARG;
+    if (nvfp4_status st = check_entries(T, k, N); st != NVFP4_OK) return st;
+    if (T > 0 && (!token_list || !positions || (rows && !x))) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(rows) || !aligned4(token_list) || !aligned4(positions)) return NVFP4_ERR_MISALIGNED;
+    DeviceInfo dev;
+    if (nvfp4_status st = device_info(&dev); st != NVFP4_OK) return st;
+    if (T == 0) return NVFP4_OK;
+    return from_cuda(launch_permute(x, type == NVFP4_OUT_F32, token_list, T, k, N, rows, positions,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status moe_combine(const void* rows, int32_t rows_type, const float* w, const int32_t* positions,
+                         const uint16_t* add, int32_t T, int32_t k, int32_t N, void* y, int32_t y_type, void* stream) {
+    if (!out_type(rows_type) || !out_type(y_type)) return NVFP4_ERR_INVALID_ARG;
+    if (nvfp4_status st = check_entries(T, k, N); st != NVFP4_OK) return st;
+    if (T > 0 && (!rows || !y)) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(rows) || !aligned16(add) || !aligned16(y) || !aligned4(w) || !aligned4(positions))
+        return NVFP4_ERR_MISALIGNED;
+    DeviceInfo dev;
+    if (nvfp4_status st = device_info(&dev); st != NVFP4_OK) return st;
+    if (T == 0) return NVFP4_OK;
+    return from_cuda(launch_combine(rows, rows_type == NVFP4_OUT_F32, w, positions, add, T, k, N, y,
+                                    y_type == NVFP4_OUT_F32, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status moe_combine_backward(const void* dy, int32_t dy_type, const void* rows, int32_t rows_type, const float* w,
+                                  const int32_t* positions, int32_t T, int32_t k, int32_t N, void* d_rows, float* d_w,
+                                  void* stream) {
+    if (!out_type(dy_type) || !out_type(rows_type)) return NVFP4_ERR_INVALID_ARG;
+    if (nvfp4_status st = check_entries(T, k, N); st != NVFP4_OK) return st;
+    if (T > 0 && (!dy || (!d_rows && !d_w) || (d_w && !rows))) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(dy) || !aligned16(rows) || !aligned16(d_rows) || !aligned4(w) || !aligned4(positions) || !aligned4(d_w))
+        return NVFP4_ERR_MISALIGNED;
+    DeviceInfo dev;
+    if (nvfp4_status st = device_info(&dev); st != NVFP4_OK) return st;
+    if (T == 0) return NVFP4_OK;
+    return from_cuda(launch_combine_backward(dy, dy_type == NVFP4_OUT_F32, rows, rows_type == NVFP4_OUT_F32, w,
+                                             positions, T, k, N, d_rows, d_w, static_cast<cudaStream_t>(stream)));
 }
 
 nvfp4_status nvfp4_scale_kind_of(int32_t N, int32_t K, size_t scale_count, int32_t scale_elem_bytes,

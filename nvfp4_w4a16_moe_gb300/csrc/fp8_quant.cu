@@ -18,13 +18,13 @@
 
 #include "common.cuh"
 #include "kernels.cuh"
+#include "quant.cuh"
 
 namespace nvfp4 {
 
 namespace {
 
 constexpr int kQThreads = 256;
-constexpr float kE4m3Max = 448.0f;
 // Fewer blocks than this: one pair of blocks a warp and short latency (us, 1 against 4 pairs: 1 x 2048 1.6 / 1.9,
 // 512 x 2048 2.3 / 2.4); more: four pairs, whose divisions are done together (4096 x 2048 6.3 / 5.3, 262144 x 2048
 // 351 / 251, 6.4 TB/s).
@@ -40,30 +40,6 @@ __device__ __forceinline__ uint32_t absmax8(const uint4 v) {
         m = max(m, w[i] & 0x7FFF0000u);
     }
     return m;
-}
-
-// Below this amax 448 / amax could overflow: the block is first brought up by 2^64, exactly.
-constexpr float kTinyAmax = 0x1p-100f;
-
-__device__ __forceinline__ float block_scale(uint32_t amax_bits) {
-    return amax_bits == 0u ? 1.0f : __uint_as_float(amax_bits) / kE4m3Max;
-}
-// 448 / amax, of a tiny block 448 / (2^64 amax).
-__device__ __forceinline__ float block_inverse(uint32_t amax_bits) {
-    const float a = __uint_as_float(amax_bits);
-    return amax_bits == 0u ? 1.0f : kE4m3Max / (a < kTinyAmax ? a * 0x1p64f : a);
-}
-
-// p rounded to 16 significant bits. In a block with infinities or NaN nothing is added (half 0), so
-// that the quotient's NaN does not wrap into a number.
-__device__ __forceinline__ float snap16(float p, uint32_t half) {
-    return __uint_as_float((__float_as_uint(p) + half) & 0xFFFFFF00u);
-}
-
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 
 // Eight bf16 of a block with this amax -> eight codes.

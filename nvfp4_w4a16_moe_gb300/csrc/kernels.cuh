@@ -204,6 +204,23 @@ cudaError_t launch_pdl(void (*kernel)(Params...), unsigned grid, unsigned thread
 cudaError_t launch_fp8_quantize(const uint16_t* x, int B, int R, int K, int block_rows, uint8_t* q, float* scales,
                                 cudaStream_t s);
 
+// Rows [R, K] as nvfp4_rows: quantised bf16 rows (kind NVFP4), normed rows, SwiGLU rows.
+cudaError_t launch_quantize_rows(const uint16_t* x, int R, int K, const nvfp4_rows& out, cudaStream_t s);
+cudaError_t launch_norm_rows(const uint16_t* h, const uint16_t* delta, const uint16_t* w, float eps, int T, int H,
+                             uint16_t* h_out, const nvfp4_rows& out, cudaStream_t s);
+cudaError_t launch_swiglu_rows(const void* gu, bool f32, int R, int I, const nvfp4_rows& out, cudaStream_t s);
+cudaError_t launch_dequantize_rows(const uint8_t* packed, const uint8_t* scales, const float* scale, int scale_rows,
+                                   int R, int K, void* y, bool f32, cudaStream_t s);
+
+// Rows sorted by expert and back.
+cudaError_t launch_permute(const void* x, bool f32, const int32_t* list, int T, int k, int N, void* rows,
+                           int32_t* positions, cudaStream_t s);
+cudaError_t launch_combine(const void* rows, bool rows_f32, const float* w, const int32_t* positions,
+                           const uint16_t* add, int T, int k, int N, void* y, bool y_f32, cudaStream_t s);
+cudaError_t launch_combine_backward(const void* dy, bool dy_f32, const void* rows, bool rows_f32, const float* w,
+                                    const int32_t* positions, int T, int k, int N, void* d_rows, float* d_w,
+                                    cudaStream_t s);
+
 // Products of rows of x with one matrix (offsets NULL) or with each expert's:
 // y[o(r)] = W[e(r)] x[i(r)] for the list positions r of every expert. xs NULL: bf16 operands;
 // otherwise E4M3 codes with the scales xs [x_rows, ceil(K/128)], ws [E, ceil(N/128), ceil(K/128)].
@@ -218,6 +235,19 @@ struct RowsProduct {
     int R, x_rows, E, N, K, k;
     int gather, scatter, y_f32;
 };
+
+// The same of NVFP4 rows and matrices: x [x_rows, K/2] with xs [x_rows, K/16] and xr [x_rows], w [E, N, K/2] with
+// ws [E, N, K/16] and wt [E, parts].
+struct Fp4Product {
+    RowsProduct r;           // its xs and ws unused
+    const uint8_t* xs;
+    const float* xr;
+    const uint8_t* ws;
+    const float* wt;
+    int parts;
+};
+cudaError_t launch_rows_fp4(const Fp4Product& P, WsHeader* hdr, const DeviceInfo& dev, uint64_t wait_limit,
+                            cudaStream_t s);
 
 // Row of x and of y of list position r; -1 for an entry outside [0, R).
 __device__ __forceinline__ int x_row(const RowsProduct& P, int r) {

@@ -1,0 +1,283 @@
+// Operators on rows that end in rows of a product: NVFP4 quantisation, the RMSNorm with the residual add, the
+// SwiGLU, each written in bf16, in E4M3 blocks of 1 x 128 or as NVFP4 rows; and NVFP4 rows back.
+//
+//   norm     h' = bf16(h + delta), x = h' / sqrt(mean h'^2 + eps) * (1 + w)
+//   SwiGLU   x = g / (1 + exp(-g)) * u
+//   E4M3     scale = amax / 448 of 128, code nearest to 448 x / amax
+//   NVFP4    s = the power of two >= amax / 2688 of the row, e = E4M3(amax / (6 s)) of 16, code = E2M1(x / (e s))
+//
+// A group of threads holds a row in registers (fp32, eight neighbouring elements a thread and unit) from its one
+// read to its one write. How a row is split over threads depends on its length alone, so a row's result does not
+// depend on the others. The sums and maxima over a row go over the lanes by shuffles, then over the warps in order.
+//
+// Bound: HBM, 2 to 8 bytes read and 0.56 to 4 written per element.
+#include "common.cuh"
+#include "kernels.cuh"
+#include "quant.cuh"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kRowThreads = 128;      // of a CTA, or one row's threads where those are more
+
+enum RowSource { kPlain, kNorm, kSwiglu16, kSwiglu32 };
+
+struct RowParams {
+    const void* in;            // x / h / gu
+    const uint16_t* delta;
+    const uint16_t* w;
+    uint16_t* h_out;
+    float eps;
+    int R, K, group;           // threads of a row
+    nvfp4_rows out;
+};
+
+__device__ __forceinline__ void unpack8(const uint4 u, float (&v)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = bf16lo(w[i]), v[2 * i + 1] = bf16hi(w[i]);
+}
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Eight elements from a 16-byte aligned place.
+template <bool F32>
+__device__ __forceinline__ void load8(const void* base, size_t at, float (&v)[8]) {
+    if constexpr (F32) {
+        const float* p = static_cast<const float*>(base) + at;
+        const uint4 a = ld_once_v4(p), b = ld_once_v4(p + 4);
+        v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
+        v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
+    } else {
+        unpack8(ld_once_v4(static_cast<const uint16_t*>(base) + at), v);
+    }
+}
+// |v| as fp32 bits: NaN above infinity above every number.
+__device__ __forceinline__ uint32_t absmax8(const float (&v)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    return m;
+}
+
+// Over the threads of a row; s: one word a warp. All threads of the CTA call it.
+__device__ __forceinline__ float row_sum(float v, int group, float* s) {
+    const int warp = threadIdx.x >> 5, warps = group >> 5, first = warp / warps * warps;
+    v = warp_sum(v);
+    if (warps == 1) return v;
+    if ((threadIdx.x & 31) == 0) s[warp] = v;
+    __syncthreads();
+    v = 0.f;
+    for (int i = 0; i < warps; ++i) v += s[first + i];
+    return v;
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t v, int group, uint32_t* s) {
+    const int warp = threadIdx.x >> 5, warps = group >> 5, first = warp / warps * warps;
+    v = __reduce_max_sync(0xffffffffu, v);
+    if (warps == 1) return v;
+    if ((threadIdx.x & 31) == 0) s[warp] = v;
+    __syncthreads();
+    for (int i = 0; i < warps; ++i) v = max(v, s[first + i]);
+    return v;
+}
+
+template <int SRC, int OUT, int U>
+__global__ void __launch_bounds__(U == 8 ? NVFP4_MAX_ROW_K / 64 : kRowThreads)
+rows_kernel(const RowParams P) {
+    __shared__ float s_sum[32];
+    __shared__ uint32_t s_max[32];
+    pdl_wait_then_trigger();
+    const int group = P.group, lane = threadIdx.x % group, units = P.K >> 3;
+    const size_t row = (size_t)blockIdx.x * (blockDim.x / group) + threadIdx.x / group;
+    const bool here = row < (size_t)P.R;
+    float v[U][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int unit = lane + u * group;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+        if (!here || unit >= units) continue;
+        const size_t at = row * P.K + unit * 8;
+        if constexpr (SRC == kPlain) {
+            load8<false>(P.in, at, v[u]);
+        } else if constexpr (SRC == kNorm) {
+            load8<false>(P.in, at, v[u]);
+            if (P.delta != nullptr) {
+                float d[8];
+                load8<false>(P.delta, at, d);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[u][i] += d[i];
+                const uint4 h = pack8(v[u]);
+                unpack8(h, v[u]);                   // the residual stream is bf16: the norm sees what is stored
+                *reinterpret_cast<uint4*>(P.h_out + at) = h;
+            } else if (P.h_out != nullptr) {
+                *reinterpret_cast<uint4*>(P.h_out + at) = pack8(v[u]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(v[u][i], v[u][i], ss);
+        } else {
+            float up[8];
+            const size_t g = row * 2 * P.K + unit * 8;
+            load8<SRC == kSwiglu32>(P.in, g, v[u]);
+            load8<SRC == kSwiglu32>(P.in, g + P.K, up);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[u][i] = __fdiv_rn(v[u][i], 1.0f + __expf(-v[u][i])) * up[i];
+        }
+    }
+    if constexpr (SRC == kNorm) {
+        const float r = 1.0f / sqrtf(row_sum(ss, group, s_sum) / (float)P.K + P.eps);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int unit = lane + u * group;
+            if (unit >= units) continue;
+            float w[8];
+            unpack8(*reinterpret_cast<const uint4*>(P.w + unit * 8), w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[u][i] = v[u][i] * r * (1.0f + w[i]);
+        }
+    }
+    if constexpr (OUT == NVFP4_ROWS_BF16) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int unit = lane + u * group;
+            if (here && unit < units)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out.data) + row * P.K + unit * 8) = pack8(v[u]);
+        }
+    } else if constexpr (OUT == NVFP4_ROWS_FP8) {
+        // sixteen neighbouring lanes hold a block
+        const int KB = (P.K + 127) >> 7;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int unit = lane + u * group;
+            uint32_t m = absmax8(v[u]);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (!here || unit >= units) continue;
+            const float inv = block_inverse(m);
+            if ((unit & 15) == 0) static_cast<float*>(P.out.scales)[row * KB + (unit >> 4)] = block_scale(m);
+            const bool tiny = __uint_as_float(m) < kTinyAmax;
+            uint32_t h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float lo = tiny ? v[u][2 * i] * 0x1p64f : v[u][2 * i], hi = tiny ? v[u][2 * i + 1] * 0x1p64f : v[u][2 * i + 1];
+                h[i] = e4m3x2(lo * inv, hi * inv);
+            }
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(P.out.data) + row * P.K + unit * 8) =
+                make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        }
+    } else {
+        uint32_t m[U], all = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) all = max(all, m[u] = absmax8(v[u]));
+        all = row_max(all, group, s_max);
+        const float s = row_scale(all);
+        const bool finite = all < 0x7F800000u;
+        const float is = finite ? inverse_pow2(s) : 0.f;
+        if (here && lane == 0) P.out.row_scales[row] = s;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int unit = lane + u * group;
+            m[u] = max(m[u], __shfl_xor_sync(0xffffffffu, m[u], 1));     // two lanes hold a block of 16
+            if (!here || unit >= units) continue;
+            float inv;
+            const uint32_t e = finite ? nvfp4_block_scale(__uint_as_float(m[u]) * is, &inv) : (inv = 0.f, 0u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[u][i] *= is;
+            const size_t at = row * (P.K >> 3) + unit;
+            static_cast<uint32_t*>(P.out.data)[at] = nvfp4_codes8<SRC == kPlain>(v[u], inv);
+            if ((unit & 1) == 0) static_cast<uint8_t*>(P.out.scales)[at >> 1] = (uint8_t)e;
+        }
+    }
+}
+
+template <int SRC, int OUT, int U>
+cudaError_t launch_u(RowParams P, cudaStream_t s) {
+    const int units = P.K >> 3;
+    P.group = ((units + U - 1) / U + 31) / 32 * 32;
+    const int threads = P.group > kRowThreads ? P.group : kRowThreads / P.group * P.group;
+    const int per = threads / P.group;
+    return launch_pdl(rows_kernel<SRC, OUT, U>, (unsigned)((P.R + per - 1) / per), threads, 0, s, P);
+}
+
+template <int SRC, int OUT>
+cudaError_t launch_rows(const RowParams& P, cudaStream_t s) {
+    const int units = P.K >> 3;
+    if (units <= kRowThreads) return launch_u<SRC, OUT, 1>(P, s);
+    if (units <= 2 * kRowThreads) return launch_u<SRC, OUT, 2>(P, s);
+    if (units <= 4 * kRowThreads) return launch_u<SRC, OUT, 4>(P, s);
+    return launch_u<SRC, OUT, 8>(P, s);
+}
+
+template <int SRC>
+cudaError_t launch_kind(const RowParams& P, cudaStream_t s) {
+    if (P.out.kind == NVFP4_ROWS_BF16) return launch_rows<SRC, NVFP4_ROWS_BF16>(P, s);
+    if (P.out.kind == NVFP4_ROWS_FP8) return launch_rows<SRC, NVFP4_ROWS_FP8>(P, s);
+    return launch_rows<SRC, NVFP4_ROWS_NVFP4>(P, s);
+}
+
+// One block of 16 elements a thread.
+template <bool F32>
+__global__ void __launch_bounds__(256)
+dequantize_rows_kernel(const uint8_t* packed, const uint8_t* scales, const float* scale, int scale_rows, size_t blocks,
+                       int KB, void* y) {
+    pdl_wait_then_trigger();
+    const size_t b = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (b >= blocks) return;
+    const size_t row = b / KB;
+    const uint2 c = *reinterpret_cast<const uint2*>(packed + b * 8);
+    const float e = e4m3_to_f32(scales[b]), s = scale[row / scale_rows];
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 f = e2m1x2_to_f32x2((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
+        v[2 * i] = f.x * e * s, v[2 * i + 1] = f.y * e * s;
+    }
+    if constexpr (F32) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(y) + b * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+        uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + b * 16);
+        o[0] = pack8(*reinterpret_cast<const float(*)[8]>(v));
+        o[1] = pack8(*reinterpret_cast<const float(*)[8]>(v + 8));
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows(const uint16_t* x, int R, int K, const nvfp4_rows& out, cudaStream_t s) {
+    RowParams P{};
+    P.in = x, P.R = R, P.K = K, P.out = out;
+    return launch_rows<kPlain, NVFP4_ROWS_NVFP4>(P, s);
+}
+
+cudaError_t launch_norm_rows(const uint16_t* h, const uint16_t* delta, const uint16_t* w, float eps, int T, int H,
+                             uint16_t* h_out, const nvfp4_rows& out, cudaStream_t s) {
+    RowParams P{};
+    P.in = h, P.delta = delta, P.w = w, P.h_out = h_out == h ? (delta ? h_out : nullptr) : h_out, P.eps = eps;
+    P.R = T, P.K = H, P.out = out;
+    return launch_kind<kNorm>(P, s);
+}
+
+cudaError_t launch_swiglu_rows(const void* gu, bool f32, int R, int I, const nvfp4_rows& out, cudaStream_t s) {
+    RowParams P{};
+    P.in = gu, P.R = R, P.K = I, P.out = out;
+    return f32 ? launch_kind<kSwiglu32>(P, s) : launch_kind<kSwiglu16>(P, s);
+}
+
+cudaError_t launch_dequantize_rows(const uint8_t* packed, const uint8_t* scales, const float* scale, int scale_rows,
+                                   int R, int K, void* y, bool f32, cudaStream_t s) {
+    const size_t blocks = (size_t)R * (K / 16);
+    if ((blocks + 255) / 256 > 0x7FFFFFFFu) return cudaErrorInvalidConfiguration;
+    const unsigned grid = (unsigned)((blocks + 255) / 256);
+    if (f32) return launch_pdl(dequantize_rows_kernel<true>, grid, 256, 0, s, packed, scales, scale, scale_rows, blocks, K / 16, y);
+    return launch_pdl(dequantize_rows_kernel<false>, grid, 256, 0, s, packed, scales, scale, scale_rows, blocks, K / 16, y);
+}
+
+}  // namespace nvfp4
