@@ -134,18 +134,22 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
 }
 
 // ---------------------------------------------------------------- tiles
-struct Tile {
+// ROUND: a tile's columns are a multiple of it, and so are the parts of an expert's rows.
+template <int ROUND>
+struct TileOf {
     int e, r0, n, m0;   // expert, first list position, rows, first weight row
-    __device__ __forceinline__ int mma_n() const { return (n + kNRound - 1) & ~(kNRound - 1); }
+    __device__ __forceinline__ int mma_n() const { return (n + ROUND - 1) & ~(ROUND - 1); }
 };
+using Tile = TileOf<kNRound>;
 
 // The tiles of a pair: token tile tt (numbered over the experts) and weight tile mt of i = first, first +
 // step, ... below total. tab: token-tile prefix [E + 1], first position [E], rows [E].
-struct Walk {
+template <int ROUND>
+struct WalkOf {
     const int* tab;
     int E, m_tiles, i, step, total, tt, mt, dt, dm;
 
-    __device__ __forceinline__ Walk(const int* tab_, int E_, int m_tiles_, int first, int step_, int total_)
+    __device__ __forceinline__ WalkOf(const int* tab_, int E_, int m_tiles_, int first, int step_, int total_)
         : tab(tab_), E(E_), m_tiles(m_tiles_), i(first), step(step_), total(total_), tt(first / m_tiles_),
           mt(first - tt * m_tiles_), dt(step_ / m_tiles_), dm(step_ - dt * m_tiles_) {}
     __device__ __forceinline__ bool more() const { return i < total; }
@@ -155,15 +159,15 @@ struct Walk {
     }
     // By all lanes of a warp: the last expert whose first token tile is at most tt (an empty one before it
     // has the same first), found among every eighth and then among eight.
-    __device__ __forceinline__ Tile tile() const {
+    __device__ __forceinline__ TileOf<ROUND> tile() const {
         const int lane = threadIdx.x & 31;
         const int b = __popc(__ballot_sync(0xffffffffu, 8 * lane < E && tab[min(8 * lane, E)] <= tt)) - 1;
         const int e8 = 8 * b + (lane & 7);
         const int e = 8 * b + __popc(__ballot_sync(0xffffffffu, lane < 8 && e8 < E && tab[min(e8, E)] <= tt)) - 1;
         const int cnt = tab[E + 1 + E + e], parts = tab[e + 1] - tab[e], l = tt - tab[e];
-        // nearly equal parts in multiples of kNRound: parts = ceil(cnt / NT), so none is empty
-        const int per = parts == 1 ? cnt : ((cnt + parts - 1) / parts + kNRound - 1) & ~(kNRound - 1);
-        Tile t;
+        // nearly equal parts in multiples of ROUND: parts = ceil(cnt / NT), so none is empty
+        const int per = parts == 1 ? cnt : ((cnt + parts - 1) / parts + ROUND - 1) & ~(ROUND - 1);
+        TileOf<ROUND> t;
         t.e = uniform(e);
         t.r0 = uniform(tab[E + 1 + e] + l * per);
         t.n = uniform(min(per, cnt - l * per));
@@ -171,6 +175,7 @@ struct Walk {
         return t;
     }
 };
+using Walk = WalkOf<kNRound>;
 
 // The table of a call, by one warp: the tiles of NT rows of every expert, eight experts a lane, then a prefix sum over
 // the lanes. tab: token-tile prefix [E + 1], first position [E], rows [E].

@@ -16,10 +16,11 @@
 //     the scales are 0, so neither a neighbour's NaN scale nor its codes count.
 //   The MMA warp copies a step's scales from the ring to tensor memory (tcgen05.cp, to all four lane quarters), right
 //     before the step's MMAs: the tensor pipe runs copies and MMAs of one thread in the order of issue.
-//   Tensor memory: 512 columns hold two sums of 256 columns, but not the scales as well (48). So the two buffers of a
-//     256-column tile share 48 columns, which the epilogue reads first and hands back on their own.
+//   Tensor memory holds two sums and the scales of a step: 512 columns take tiles of up to 224 columns. (Tiles of 256
+//     whose buffers shared 48 columns, which the epilogue read first, left 1.1 us of every tile without MMAs.)
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.cuh"
@@ -32,43 +33,45 @@ namespace {
 constexpr int kABytes = kM * kStepBytes;
 constexpr int kStepK = 2 * kStepBytes;   // elements of a step
 constexpr int kMmas = kStepK / 64;       // MMAs of a step
-constexpr int kBlkBytes = 2048;          // scales of 128 rows and a step
+constexpr int kSectorBytes = 32;         // block scales of a row in two steps
+constexpr int kBlkBytes = kM * kSectorBytes; // block scales of 128 rows in two steps
 constexpr int kMaxStages = 9;
 constexpr int kMinSteps = 2;             // steps of each pair that shares a tile's K, at least
 
-// Warps: 16 of epilogue, TMA, MMA, four of gather, two for every 128 rows of scales (each takes every other step).
+// Warps: 16 of epilogue, TMA, MMA, four of gather, one for every 128 rows of scales.
 constexpr int kEpiWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kGatherWarp0 = 18, kGatherWarps = 4, kScaleWarp0 = 22;
 
 template <int NT>
 struct Cfg {
+    static constexpr int kRound = NT > 128 ? 32 : kNRound;       // a tile's columns are a multiple of this
     static constexpr int kXBlocks = (NT + 127) / 128, kBlocks = 1 + kXBlocks;     // of 128 rows' scales
-    static constexpr int kThreads = 32 * (kScaleWarp0 + 2 * kBlocks);
-    static constexpr int kBoxRows = kNRound / 2;                 // heights of a box of x: this times
-    static constexpr int kBoxes = NT / kNRound;                  // ... 1 .. kBoxes
-    static constexpr int kOffSf = kABytes + NT / 2 * kStepBytes; // scales of W, then of x
-    static constexpr int kStage = kOffSf + kBlocks * kBlkBytes;
-    static constexpr int kStages = std::min(kMaxStages, (196 * 1024) / kStage);
+    static constexpr int kThreads = 32 * (kScaleWarp0 + kBlocks);
+    static constexpr int kBoxRows = NT > 128 ? 56 : 32;          // rows of x of a copy
+    static constexpr int kStage = kABytes + NT / 2 * kStepBytes;
+    static constexpr int kStages = std::min(kMaxStages, (160 * 1024) / kStage);
+    // ring of block scales of two steps: W's 128 rows, then x's NT
+    static constexpr int kSlotBytes = kBlocks * kBlkBytes, kSlots = NT > 128 ? 3 : 4;
+    static constexpr int kOffSlots = kStages * kStage;
     // tensor memory: buffers of NT columns, then the scales of a step (two sets of them where there is room)
     static constexpr int kSfCols = 4 * kMmas * kBlocks;
-    static constexpr bool kOverlap = NT == 256;
-    static constexpr int kBufs = kOverlap ? 2 : 256 / NT;
-    static constexpr int kBufStep = kOverlap ? 512 - kSfCols - NT : NT;
-    static constexpr int kShared = kOverlap ? NT - kBufStep : 0; // columns that both buffers have
-    static constexpr int kSf = kOverlap ? 512 - kSfCols : 256, kSfSets = kOverlap ? 1 : 2;
+    static constexpr int kBufs = NT > 128 ? 2 : 256 / NT;
+    static constexpr int kSf = kBufs * NT, kSfSets = NT > 128 ? 1 : 2;
     static constexpr int kCols = NT / 4;                         // columns of an epilogue warp, at most
-    static constexpr int kOffStg = kStages * kStage;
+    static constexpr int kOffStg = kOffSlots + kSlots * kSlotBytes;
     static constexpr int kOffBars = kOffStg + kEpiWarps * kStgRows * kStgPitch;
-    static constexpr int kNumBars = 2 * kStages + 3 * kBufs + 1;
+    static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 3 * kSlots + 1;
     static constexpr int kOffTab = kOffBars + kNumBars * 8 + 16; // tile prefix [E + 1], first position [E], rows [E]
     static constexpr int kSmem = 1024 + kOffTab + (3 * NVFP4_MAX_EXPERTS + 1) * 4;
-    static_assert(NT % kNRound == 0 && NT <= 256 && kStage % 1024 == 0 && kCols % 16 == 0, "swizzle atoms, fragments");
+    static_assert(NT % kRound == 0 && NT <= 256 && kStage % 1024 == 0 && NT / 2 % kBoxRows == 0, "swizzle atoms, copies");
     static_assert(kSmem <= 227 * 1024, "shared memory");
     static_assert(4 * NT / 16 * 2048 <= kOffStg, "exchanged sums fit in the ring");
-    static_assert(kShared % 16 == 0 && kSf + kSfSets * kSfCols <= 512, "tensor memory");
+    static_assert(kSf + kSfSets * kSfCols <= 512, "tensor memory");
 };
 
-struct TcRowMaps {
-    CUtensorMap w, x[4];   // x: boxes of one to kBoxes times Cfg::kBoxRows rows; x[0] single rows to gather
+struct Fp4Maps {
+    CUtensorMap w, x;      // x: boxes of kBoxRows rows, or of one to gather
+    CUtensorMap ws, xs;    // block scales, 32 bytes of a row: 128 rows, NT (or one to gather); unused where a row's
+                           // scales are no multiple of 16 bytes
 };
 
 // D (256 x N over both CTAs) = A B^T of 64 columns, scaled by 4 E4M3 scales a row, plus D where accumulate.
@@ -92,32 +95,91 @@ __device__ __forceinline__ uint32_t nvfp4_idesc(int N) {
     return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(2 * kM >> 7) << 27);
 }
 
-// Bytes 16 s .. 16 s + 15 of a row of KB block scales, 0 behind its end. KB is even; its rows start at multiples of
-// `unit` (2, 4 or 16) bytes.
-__device__ __forceinline__ uint4 row_scales16(const uint8_t* row, int s, int KB, int unit) {
-    const uint8_t* p = row + 16 * s;
-    const int left = KB - 16 * s;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (unit == 16) return *reinterpret_cast<const uint4*>(p);
-    if (unit == 4) {
-        const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
-        if (left > 0) v.x = q[0];
-        if (left > 4) v.y = q[1];
-        if (left > 8) v.z = q[2];
-        if (left > 12) v.w = q[3];
-        return v;
-    }
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
-    uint32_t h[8];
+// Block scales of steps 2 m and 2 m + 1 of a row of KB, a number that is no multiple of 16: loads of UNIT (2 or 4) bytes.
+// Behind the end of the row: 0.
+template <int UNIT>
+__device__ __forceinline__ void load_row(const uint8_t* row, int m, int KB, uint32_t (&w)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = left > 2 * i ? q[i] : 0u;
-    return make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+    for (int i = 0; i < 8; ++i) {
+        const int at = 32 * m + 4 * i;
+        if constexpr (UNIT == 4) {
+            w[i] = *reinterpret_cast<const uint32_t*>(row + min(at, KB - 4));
+        } else {
+            const uint32_t lo = *reinterpret_cast<const uint16_t*>(row + min(at, KB - 2));
+            w[i] = lo | (at + 2 < KB ? (uint32_t)*reinterpret_cast<const uint16_t*>(row + at + 2) << 16 : 0u);
+        }
+        if (at >= KB) w[i] = 0u;
+    }
+}
+
+// A warp that puts the scales of 128 rows (blk 0: of W, then of x) of two steps after two steps into line order, in place:
+// from the sectors that the TMA brought, row after row, or (UNIT 2, 4) from global memory.
+template <typename C, int UNIT>
+__device__ __forceinline__ void scale_warp(const Fp4Product& Q, WalkOf<C::kRound> at, int pairs, int m_begin, int blk,
+                                           int rank, uint8_t* slots, uint64_t* raw, uint64_t* ready, uint64_t* empty,
+                                           const Waiter& wait) {
+    const RowsProduct& P = Q.r;
+    const int lane = threadIdx.x & 31, KB = P.K / 16;
+    int slot = 0;
+    uint32_t par = 0;
+#pragma unroll 1
+    for (; at.more(); at.next()) {
+        const uint8_t* row[4] = {};          // UNIT 2, 4: this lane's rows; null: no such row
+        if constexpr (UNIT < 16) {
+            const auto t = at.tile();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (blk == 0) {
+                    const int n = t.m0 + rank * kM + 32 * i + lane;
+                    if (n < P.N) row[i] = Q.ws + ((size_t)t.e * P.N + n) * KB;
+                } else {
+                    const int col = (blk - 1) * 128 + 32 * i + lane;
+                    const int src = col < t.n ? x_row(P, t.r0 + col) : -1;
+                    if (src >= 0) row[i] = Q.xs + (size_t)src * KB;
+                }
+            }
+        }
+#pragma unroll 1
+        for (int j = 0; j < pairs; ++j) {
+            uint8_t* blkp = slots + slot * C::kSlotBytes + blk * kBlkBytes;
+            uint32_t w[4][8];
+            if constexpr (UNIT < 16) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) w[i][k] = 0u;
+                    if (row[i] != nullptr) load_row<UNIT>(row[i], m_begin + j, KB, w[i]);
+                }
+                if (!wait(&empty[slot], par ^ 1u)) return;
+            } else {
+                if (!wait(&raw[slot], par)) return;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // the copies swap the halves of rows 4 .. 7 of every eight (32-byte swizzle): no bank is read twice
+                    const uint8_t* p = blkp + (32 * i + lane) * kSectorBytes;
+                    const int odd = (lane >> 2) & 1;
+                    const uint4 a = *reinterpret_cast<const uint4*>(p + 16 * odd);
+                    const uint4 b = *reinterpret_cast<const uint4*>(p + 16 * (odd ^ 1));
+                    w[i][0] = a.x, w[i][1] = a.y, w[i][2] = a.z, w[i][3] = a.w;
+                    w[i][4] = b.x, w[i][5] = b.y, w[i][6] = b.z, w[i][7] = b.w;
+                }
+                __syncwarp();
+            }
+            uint4* to = reinterpret_cast<uint4*>(blkp) + lane;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) to[32 * k] = make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (elect_one()) mbar_arrive(&ready[slot]);
+            if (++slot == C::kSlots) slot = 0, par ^= 1u;
+        }
+    }
 }
 
 // SPLITS: pairs of a cluster, which share a tile's K.
 template <int NT, int SPLITS>
 __global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(Cfg<NT>::kThreads, 1)
-rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ TcRowMaps maps, int m_tiles, int max_tiles, WsHeader* hdr,
+rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_tiles, int max_tiles, WsHeader* hdr,
                 unsigned long long wait_limit) {
     using C = Cfg<NT>;
     const RowsProduct& P = Q.r;
@@ -134,8 +196,10 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ TcRowMaps maps, int 
     uint64_t* empty = full + C::kStages;                               // MMAs done with the step
     uint64_t* acc_full = empty + C::kStages;                           // tensor-memory buffer summed
     uint64_t* acc_empty = acc_full + C::kBufs;                         // first CTA: ... and read in both
-    uint64_t* shr_empty = acc_empty + C::kBufs;                        // first CTA: ... the columns it shares
-    uint64_t* done = shr_empty + C::kBufs;                             // every MMA of the pair
+    uint64_t* sf_raw = acc_empty + C::kBufs;                           // scales of two steps landed
+    uint64_t* sf_ready = sf_raw + C::kSlots;                           // ... and are in line order
+    uint64_t* sf_empty = sf_ready + C::kSlots;                         // ... and copied to tensor memory
+    uint64_t* done = sf_empty + C::kSlots;                             // every MMA of the pair
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* tab = reinterpret_cast<int*>(sm + C::kOffTab);
@@ -143,14 +207,18 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ TcRowMaps maps, int 
     if (warp == kMmaWarp) {
         if (lane == 0) {
             for (int i = 0; i < C::kStages; ++i) {
-                // the TMA warp, a warp for every 128 rows of scales, each gather warp, in the first CTA the second's word
-                mbar_init(&full[i], 1 + C::kBlocks + (P.gather ? kGatherWarps : 0) + (rank == 0 ? 1 : 0));
+                // the TMA warp, each gather warp, and in the first CTA the second's word
+                mbar_init(&full[i], 1 + (P.gather ? kGatherWarps : 0) + (rank == 0 ? 1 : 0));
                 mbar_init(&empty[i], 1);
             }
             for (int i = 0; i < C::kBufs; ++i) {
                 mbar_init(&acc_full[i], 1);
                 mbar_init(&acc_empty[i], 2 * kEpiWarps);
-                mbar_init(&shr_empty[i], 2 * kEpiWarps);
+            }
+            for (int i = 0; i < C::kSlots; ++i) {
+                mbar_init(&sf_raw[i], 1 + (P.gather ? kGatherWarps : 0));
+                mbar_init(&sf_ready[i], C::kBlocks);
+                mbar_init(&sf_empty[i], 1);
             }
             mbar_init(done, 1);
             *abort_flag = 0;
@@ -173,6 +241,11 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ TcRowMaps maps, int 
     const int total = uniform((int)min((long long)tab[P.E] * m_tiles, (long long)max_tiles));
     const int nk = (P.K + kStepK - 1) / kStepK;
     const int s_begin = nk * pair / SPLITS, s_end = nk * (pair + 1) / SPLITS;      // this pair's steps
+    // scales come for steps 2 m and 2 m + 1 together, by TMA where their rows can be strides of a tensor map
+    const int m_begin = s_begin >> 1, m_pairs = ((s_end - 1) >> 1) - m_begin + 1, KB = P.K / 16;
+    const bool sf_tma = KB % 16 == 0;
+    using Walk = WalkOf<C::kRound>;
+    using Tile = TileOf<C::kRound>;
     const Walk tiles(tab, P.E, m_tiles, blockIdx.x / kCluster, gridDim.x / kCluster, total);
     const Waiter wait{abort_flag, map_rank(su32(const_cast<int*>(abort_flag)), (uint32_t)crank ^ 1u), hdr, wait_limit};
 
@@ -186,20 +259,36 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ TcRowMaps maps, int 
         for (int s = max(0, step - C::kStages); s < step; ++s)
             mbar_wait_bounded(&full[s % C::kStages], (s / C::kStages) & 1, kCopyDrainNs);
     };
+    auto drain_scales = [&](int m) {
+        for (int i = max(0, m - C::kSlots); i < m; ++i)
+            mbar_wait_bounded(&sf_raw[i % C::kSlots], (i / C::kSlots) & 1, kCopyDrainNs);
+    };
 
     if (warp >= kEpiWarps) {
         if (warp == kTmaWarp) {
-            int step = 0;
+            int step = 0, two = 0;                                              // steps and pairs of steps so far
             bool ok = true;
 #pragma unroll 1
             for (Walk at = tiles; at.more() && ok; at.next()) {
                 const Tile t = at.tile();
                 const int share = t.mma_n() / 2;                                // rows of x here
                 const int wy = t.e * P.N + t.m0 + rank * kM;
-                const CUtensorMap* mx = &maps.x[share / C::kBoxRows - 1];
-                const uint32_t bytes = kABytes + (P.gather ? 0 : share * kStepBytes);
+                const int boxes = P.gather ? 0 : (share + C::kBoxRows - 1) / C::kBoxRows;
+                const uint32_t bytes = kABytes + boxes * (C::kBoxRows * kStepBytes);
 #pragma unroll 1
                 for (int s = s_begin; s < s_end; ++s, ++step) {
+                    if (sf_tma && (s == s_begin || (s & 1) == 0)) {
+                        const int sl = two % C::kSlots, u = two / C::kSlots;
+                        if (u > 0) ok = wait(&sf_empty[sl], (u - 1) & 1);
+                        if (!ok) break;
+                        const uint32_t to = sm_base + C::kOffSlots + sl * C::kSlotBytes;
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(&sf_raw[sl], kBlkBytes + (P.gather ? 0 : NT * kSectorBytes));
+                            tma_load_2d(to, &maps.ws, (s >> 1) * kSectorBytes, wy, &sf_raw[sl]);
+                            if (!P.gather) tma_load_2d(to + kBlkBytes, &maps.xs, (s >> 1) * kSectorBytes, t.r0, &sf_raw[sl]);
+                        }
+                        ++two;
+                    }
                     const int st = step % C::kStages, u = step / C::kStages;
                     if (u > 0) ok = wait(&empty[st], (u - 1) & 1);
                     if (!ok) break;
@@ -207,36 +296,39 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ TcRowMaps maps, int 
                     if (elect_one()) {
                         mbar_arrive_expect_tx(&full[st], bytes);
                         tma_load_2d(a, &maps.w, s * kStepBytes, wy, &full[st]);
-                        if (!P.gather) tma_load_2d(b, mx, s * kStepBytes, t.r0 + rank * share, &full[st]);
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_2d(b + i * (C::kBoxRows * kStepBytes), &maps.x, s * kStepBytes,
+                                        t.r0 + rank * share + i * C::kBoxRows, &full[st]);
                     }
                 }
             }
-            if (lane == 0) drain(step);
+            if (lane == 0) {
+                drain(step);
+                drain_scales(two);
+            }
         } else if (warp == kMmaWarp) {
-            int st = 0, buf = 0, use = 0;
-            uint32_t st_par = 0, buf_par = 1;          // an unused buffer's "empty" phase counts as over
+            int st = 0, buf = 0, sl = 0;
+            uint32_t st_par = 0, sl_par = 0, buf_par = 1;          // an unused buffer's "empty" phase counts as over
             bool ok = true;
-            const uint64_t stage0 = sw128_desc(sm_base), scales0 = lines_desc(sm_base + C::kOffSf);
+            const uint64_t stage0 = sw128_desc(sm_base), scales0 = lines_desc(sm_base + C::kOffSlots);
 #pragma unroll 1
-            for (Walk at = tiles; at.more() && ok; at.next(), ++use) {
+            for (Walk at = tiles; at.more() && ok; at.next()) {
                 const int N = at.tile().mma_n();
                 const uint32_t idesc = nvfp4_idesc(N);
 #pragma unroll 1
                 for (int s = s_begin; s < s_end; ++s) {
-                    ok = wait(&full[st], st_par);
+                    if (s == s_begin || (s & 1) == 0) ok = wait(&sf_ready[sl], sl_par);
+                    if (ok) ok = wait(&full[st], st_par);
                     if (!ok) break;
+                    const bool sl_done = (s & 1) != 0 || s == s_end - 1;
                     if (rank != 0) {
                         if (elect_one()) arrive_cluster(map_rank(su32(&full[st]), first_rank));
                     } else {
-                        if (s == s_begin) {
-                            ok = wait(&acc_empty[buf], buf_par);
-                            // the tile before this one still has its buffer, but for the columns that this one shares
-                            if (C::kOverlap && ok && use > 0) ok = wait(&shr_empty[buf ^ 1], ((use - 1) >> 1) & 1);
-                        }
+                        if (s == s_begin) ok = wait(&acc_empty[buf], buf_par);
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t a = stage0 + st * (C::kStage / 16), b = a + kABytes / 16;
-                        const uint64_t sf = scales0 + st * (C::kStage / 16);
+                        const uint64_t sf = scales0 + (sl * C::kSlotBytes + (s & 1) * (kBlkBytes / 2)) / 16;
                         const uint32_t tsf = tmem + C::kSf + (C::kSfSets > 1 ? (s & 1) * C::kSfCols : 0);
                         if (elect_one()) {
                             // columns: 4 for each MMA's scales of W, then 4 kXBlocks for each MMA's of x
@@ -250,14 +342,16 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ TcRowMaps maps, int 
                             }
 #pragma unroll
                             for (int j = 0; j < kMmas; ++j)      // 32 bytes of K an MMA: 2 address units
-                                mma_nvfp4(tmem + buf * C::kBufStep, a + 2 * j, b + 2 * j, idesc, tsf + 4 * j,
+                                mma_nvfp4(tmem + buf * NT, a + 2 * j, b + 2 * j, idesc, tsf + 4 * j,
                                           tsf + 4 * kMmas + 4 * C::kXBlocks * j, s != s_begin || j != 0);
                             commit_pair(&empty[st], pair_mask);
+                            if (sl_done) commit_pair(&sf_empty[sl], pair_mask);
                             if (s == s_end - 1) commit_pair(&acc_full[buf], pair_mask);
                         }
                         if (s == s_end - 1 && ++buf == C::kBufs) buf = 0, buf_par ^= 1;
                     }
                     if (++st == C::kStages) st = 0, st_par ^= 1;
+                    if (sl_done && ++sl == C::kSlots) sl = 0, sl_par ^= 1;
                 }
             }
             // no MMA still reads or writes either CTA's memory, nor has an arrival on the way to it, when it is freed
@@ -269,21 +363,46 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ TcRowMaps maps, int 
             if (P.gather) {
                 // copies of four rows, in turn over the warps: at most kPer a warp and step; lane 4 j + r has
                 // row r of this warp's copy j
-                constexpr int kPer = NT / 2 / 4 / kGatherWarps;
+                constexpr int kPer = (NT / 2 / 4 + kGatherWarps - 1) / kGatherWarps;
                 const int w = warp - kGatherWarp0;
-                int step = 0;
+                // and of all columns' scales: copies of four rows in turn over the warps, kSfPer a warp
+                constexpr int kSfPer = NT / 4 / kGatherWarps, kSfRegs = (4 * kSfPer + 31) / 32;
+                int step = 0, two = 0;
                 bool ok = true;
 #pragma unroll 1
                 for (Walk at = tiles; at.more() && ok; at.next()) {
                     const Tile t = at.tile();
                     const int share = t.mma_n() / 2, copies = share / 4;
+                    const auto row_of = [&](int col) {
+                        const int src = col < t.n ? x_row(P, t.r0 + col) : -1;
+                        return src < 0 ? P.x_rows : src;             // past the last row: zeros
+                    };
                     const int l = 4 * (w + kGatherWarps * (lane >> 2)) + (lane & 3);
-                    const int col = rank * share + l;
-                    int src = l < share && col < t.n ? x_row(P, t.r0 + col) : -1;
-                    if (src < 0) src = P.x_rows;                     // past the last row: zeros
+                    const int src = row_of(l < share ? rank * share + l : t.n);
+                    int sf_src[kSfRegs];
+#pragma unroll
+                    for (int i = 0; i < kSfRegs; ++i)
+                        sf_src[i] = row_of(4 * (w + kGatherWarps * ((32 * i + lane) >> 2)) + (lane & 3));
                     const int mine = (copies - w + kGatherWarps - 1) / kGatherWarps;
 #pragma unroll 1
                     for (int s = s_begin; s < s_end; ++s, ++step) {
+                        if (sf_tma && (s == s_begin || (s & 1) == 0)) {
+                            const int sl = two % C::kSlots, u = two / C::kSlots;
+                            if (u > 0) ok = wait(&sf_empty[sl], (u - 1) & 1);
+                            if (!ok) break;
+                            const uint32_t to = sm_base + C::kOffSlots + sl * C::kSlotBytes + kBlkBytes + w * 4 * kSectorBytes;
+                            if (elect_one()) mbar_arrive_expect_tx(&sf_raw[sl], kSfPer * 4 * kSectorBytes);
+#pragma unroll
+                            for (int j = 0; j < kSfPer; ++j) {
+                                const int v = sf_src[4 * j / 32];
+                                const int r0 = __shfl_sync(0xffffffffu, v, 4 * j & 31), r1 = __shfl_sync(0xffffffffu, v, (4 * j & 31) + 1);
+                                const int r2 = __shfl_sync(0xffffffffu, v, (4 * j & 31) + 2), r3 = __shfl_sync(0xffffffffu, v, (4 * j & 31) + 3);
+                                if (elect_one())
+                                    tma_gather4(to + j * (kGatherWarps * 4 * kSectorBytes), &maps.xs, (s >> 1) * kSectorBytes,
+                                                r0, r1, r2, r3, &sf_raw[sl]);
+                            }
+                            ++two;
+                        }
                         const int st = step % C::kStages, u = step / C::kStages;
                         if (u > 0) ok = wait(&empty[st], (u - 1) & 1);
                         if (!ok) break;
@@ -297,59 +416,22 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ TcRowMaps maps, int 
                             const int r2 = __shfl_sync(0xffffffffu, src, 4 * j + 2);
                             const int r3 = __shfl_sync(0xffffffffu, src, 4 * j + 3);
                             if (elect_one())
-                                tma_gather4(b + j * (kGatherWarps * 4 * kStepBytes), &maps.x[0], s * kStepBytes, r0, r1,
+                                tma_gather4(b + j * (kGatherWarps * 4 * kStepBytes), &maps.x, s * kStepBytes, r0, r1,
                                             r2, r3, &full[st]);
                         }
                     }
                 }
-                if (lane == 0) drain(step);
+                if (lane == 0) {
+                    drain(step);
+                    drain_scales(two);
+                }
             }
         } else {
-            const int blk = (warp - kScaleWarp0) % C::kBlocks, odd = (warp - kScaleWarp0) / C::kBlocks;
-            const int KB = P.K / 16, unit = KB % 16 == 0 ? 16 : KB % 4 == 0 ? 4 : 2;
-            int base = 0;                            // steps of the tiles so far
-            bool ok = true;
-#pragma unroll 1
-            for (Walk at = tiles; at.more() && ok; at.next(), base += s_end - s_begin) {
-                const Tile t = at.tile();
-                const uint8_t* row[4];               // null: no such row
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    row[i] = nullptr;
-                    if (blk == 0) {
-                        const int n = t.m0 + rank * kM + 32 * i + lane;
-                        if (n < P.N) row[i] = Q.ws + ((size_t)t.e * P.N + n) * KB;
-                    } else {
-                        const int col = (blk - 1) * 128 + 32 * i + lane;
-                        const int src = col < t.n ? x_row(P, t.r0 + col) : -1;
-                        if (src >= 0) row[i] = Q.xs + (size_t)src * KB;
-                    }
-                }
-                uint4 v[4];
-                auto load = [&](int s) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[i] = row[i] != nullptr ? row_scales16(row[i], s, KB, unit) : make_uint4(0, 0, 0, 0);
-                };
-                // every other step of the call is this warp's
-                const int s_first = s_begin + ((base ^ odd) & 1);
-                if (s_first < s_end) load(s_first);
-#pragma unroll 1
-                for (int s = s_first; s < s_end; s += 2) {
-                    const int step = base + s - s_begin, st = step % C::kStages, u = step / C::kStages;
-                    if (u > 0) ok = wait(&empty[st], (u - 1) & 1);
-                    if (!ok) break;
-                    uint4* to = reinterpret_cast<uint4*>(sm + st * C::kStage + C::kOffSf + blk * kBlkBytes) + lane;
-                    to[0] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
-                    to[32] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
-                    to[64] = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
-                    to[96] = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (elect_one()) mbar_arrive(&full[st]);
-                    if (s + 2 < s_end) load(s + 2);
-                }
-            }
+            const int blk = warp - kScaleWarp0;
+            uint8_t* slots = sm + C::kOffSlots;
+            if (sf_tma) scale_warp<C, 16>(Q, tiles, m_pairs, m_begin, blk, rank, slots, sf_raw, sf_ready, sf_empty, wait);
+            else if (KB % 4 == 0) scale_warp<C, 4>(Q, tiles, m_pairs, m_begin, blk, rank, slots, sf_raw, sf_ready, sf_empty, wait);
+            else scale_warp<C, 2>(Q, tiles, m_pairs, m_begin, blk, rank, slots, sf_raw, sf_ready, sf_empty, wait);
         }
         if (SPLITS > 1 && tiles.more()) exchange.join();
     } else {
@@ -357,94 +439,106 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ TcRowMaps maps, int 
         uint8_t* stg = sm + C::kOffStg + warp * (kStgRows * kStgPitch);
         const int p = lane & 3, g = lane >> 2;
         const uint32_t first_acc_empty = map_rank(su32(acc_empty), first_rank);
-        const uint32_t first_shr_empty = map_rank(su32(shr_empty), first_rank);
         const int part_rows = P.N / Q.parts;
-        int use = 0;               // buffers read so far
-        bool ok = true;
-#pragma unroll 1
-        for (Walk at = tiles; at.more(); at.next()) {
-            const Tile t = at.tile();
-            const int width = t.mma_n() / 4, c0 = part * width;            // this warp's columns of the tile
-            const int n0 = t.m0 + rank * kM + 32 * q;                      // first output
-            // lane l: row of y (or -1) and row scale of columns c0 + l and c0 + 32 + l, asked for under the MMAs
+        // First column of this warp's chunk i of 16: chunks go round the warps; pairs that share a tile exchange
+        // neighbouring ones.
+        const auto chunk = [&](const Tile& t, int i) { return SPLITS > 1 ? part * (t.mma_n() / 4) + 16 * i : 16 * (4 * i + part); };
+        // What the outputs of a tile need besides the sums. dst, scale of lane l: row of y (or -1) and row scale of
+        // column l % 16 of chunks l / 16 and 2 + l / 16; wt: tensor scales of outputs 8 i + g.
+        struct Ends {
             int dst[2];
-            float scale[2];
+            float scale[2], wt[4];
+        };
+        const auto ends_of = [&](const Tile& t) {
+            Ends e;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int c = 32 * i + lane, col = c0 + c;
-                dst[i] = -1, scale[i] = 0.f;
-                if (c < width && col < t.n) {
+                const int k = 2 * i + (lane >> 4), col = chunk(t, k) + (lane & 15);
+                e.dst[i] = -1, e.scale[i] = 0.f;
+                if ((SPLITS == 1 || 16 * k < t.mma_n() / 4) && col < t.n) {
                     const int src = x_row(P, t.r0 + col);
-                    dst[i] = y_row(P, t.r0 + col);
-                    if (src >= 0) scale[i] = Q.xr[src];
+                    e.dst[i] = y_row(P, t.r0 + col);
+                    if (src >= 0) e.scale[i] = Q.xr[src];
                 }
             }
-            float wt[4];                                                   // tensor scales of outputs n0 + 8 i + g
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int n = n0 + 8 * i + g;
-                wt[i] = n < P.N ? Q.wt[(size_t)t.e * Q.parts + n / part_rows] : 0.f;
+                const int n = t.m0 + rank * kM + 32 * q + 8 * i + g;
+                e.wt[i] = n < P.N ? Q.wt[(size_t)t.e * Q.parts + n / part_rows] : 0.f;
             }
+            return e;
+        };
+        int use = 0;               // buffers read so far
+        bool ok = true;
+        Walk at = tiles;
+        Tile t{};
+        Ends ends{};
+        if (at.more()) t = at.tile(), ends = ends_of(t);
+#pragma unroll 1
+        while (at.more()) {
+            const int n0 = t.m0 + rank * kM + 32 * q;                      // first output
+            // the next tile's are asked for under this one's MMAs
+            at.next();
+            Tile t2 = t;
+            Ends ends2 = ends;
+            if (at.more()) t2 = at.tile(), ends2 = ends_of(t2);
             const int buf = use % C::kBufs;
-            const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + buf * C::kBufStep + c0;
+            const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + buf * NT;
             if (ok) ok = wait(&acc_full[buf], (use / C::kBufs) & 1);
             tc_fence_after();
-            const auto sums = [&](int c, float (&v)[16]) {
-                if (ok) {
-                    tmem_ld_frag(lanes + c, v);
-                    tmem_wait16(v);
-                }
-            };
-            const auto finish = [&](int c, float (&v)[16]) {
-                const int d = c & 32 ? dst[1] : dst[0];
-                const float sc = c & 32 ? scale[1] : scale[0];
+            const auto finish = [&](int i, float (&v)[16]) {
+                const float sc = i & 2 ? ends.scale[1] : ends.scale[0];
                 float s4[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    s4[i] = __shfl_sync(0xffffffffu, sc, (c & 16) + 8 * (i >> 1) + 2 * p + (i & 1));
+                for (int k = 0; k < 4; ++k)
+                    s4[k] = __shfl_sync(0xffffffffu, sc, (i & 1) * 16 + 8 * (k >> 1) + 2 * p + (k & 1));
 #pragma unroll
-                for (int i = 0; i < 16; ++i)     // lane group 2 L + u, column 2 j + b of the fragment
-                    v[i] *= s4[2 * ((i >> 2) & 1) + (i & 1)] * wt[2 * (i >> 3) + ((i >> 1) & 1)];
+                for (int k = 0; k < 16; ++k)     // lane group 2 L + u, column 2 j + b of the fragment
+                    v[k] *= s4[2 * ((k >> 2) & 1) + (k & 1)] * ends.wt[2 * (k >> 3) + ((k >> 1) & 1)];
                 if (*abort_flag)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(0x7FC00000u);
-                store_frag(P, v, __shfl_sync(0xffffffffu, d, (c & 16) + (lane & 15)), n0, stg);
+                    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(0x7FC00000u);
+                store_frag(P, v, __shfl_sync(0xffffffffu, i & 2 ? ends.dst[1] : ends.dst[0], (i & 1) * 16 + (lane & 15)), n0, stg);
+            };
+            const auto hand_back = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (ok && elect_one()) arrive_cluster(first_acc_empty + 8 * buf);
             };
             if constexpr (SPLITS > 1) {
+                const int width = t.mma_n() / 4, c0 = part * width;            // this warp's columns of the tile
+                const auto sums = [&](int c, float (&v)[16]) {
+                    if (ok) {
+                        tmem_ld_frag(lanes + c0 + c, v);
+                        tmem_wait16(v);
+                    }
+                };
                 exchange.send(sums, t, width, c0, part, q);
 #pragma unroll
                 for (int c = 0; c < C::kCols; c += 16) {
                     if (c >= width || c0 + c >= t.n) break;
                     float v[16];
                     sums(c, v);
-                    if (exchange.finish(v, c, width, part, q)) finish(c, v);
+                    if (exchange.finish(v, c, width, part, q)) finish(c / 16, v);
                 }
             } else {
-                // The columns that the next tile's buffer shares come first: the last ones of buffer 0, the first of
-                // buffer 1.
-                const bool down = C::kOverlap && buf == 0;
-                const auto shared_left = [&](int c) {              // chunk c is in, or before, the shared columns
-                    return down ? c0 + c + 16 > NT - C::kShared : c0 + c < C::kShared;
-                };
-                bool told = !C::kOverlap;
-                const auto tell = [&](uint32_t bar) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (ok && elect_one()) arrive_cluster(bar + 8 * buf);
-                };
+                // A buffer is handed back when its last chunk is in registers.
+                const int chunks = (t.n - 16 * part + 63) / 64;            // none where it is not positive
 #pragma unroll 1
-                for (int i = 0; i < width; i += 16) {
-                    const int c = down ? width - 16 - i : i;
-                    if (!told && !shared_left(c)) tell(first_shr_empty), told = true;
-                    if (c0 + c >= t.n) continue;                    // padding is neither read nor written
+                for (int i = 0; i < chunks; ++i) {
                     float v[16];
-                    sums(c, v);
-                    finish(c, v);
+                    if (ok) {
+                        tmem_ld_frag(lanes + chunk(t, i), v);
+                        tmem_wait16(v);
+                    }
+                    if (i == chunks - 1) hand_back();
+                    finish(i, v);
                 }
-                if (!told) tell(first_shr_empty);
-                tell(first_acc_empty);
+                if (chunks <= 0) hand_back();
             }
             ++use;
+            t = t2;
+            ends = ends2;
         }
     }
     tc_fence_before();
@@ -503,12 +597,14 @@ cudaError_t plan_tiles(const RowsProduct& P, const DeviceInfo& dev, Plan* best) 
     p.tiles = ((P.R - groups) / NT + groups) * (long long)m_tiles;
     // as many pairs to a tile as the device runs at a time, where each has kMinSteps steps
     int c2 = 0, c4 = 0;
-    if (nk >= 2 * kMinSteps && 2 * p.tiles <= dev.num_sms / 2)
-        if (cudaError_t e = resident_clusters<NT, 2>(dev, &c2); e != cudaSuccess) return e;
-    if (nk >= 4 * kMinSteps && 4 * p.tiles <= dev.num_sms / 2)
-        if (cudaError_t e = resident_clusters<NT, 4>(dev, &c4); e != cudaSuccess) return e;
+    if constexpr (NT <= 128) {
+        if (nk >= 2 * kMinSteps && 2 * p.tiles <= dev.num_sms / 2)
+            if (cudaError_t e = resident_clusters<NT, 2>(dev, &c2); e != cudaSuccess) return e;
+        if (nk >= 4 * kMinSteps && 4 * p.tiles <= dev.num_sms / 2)
+            if (cudaError_t e = resident_clusters<NT, 4>(dev, &c4); e != cudaSuccess) return e;
+    }
     p.splits = p.tiles <= c4 ? 4 : p.tiles <= c2 ? 2 : 1;
-    const int parts = (rows + NT - 1) / NT, n = ((rows + parts - 1) / parts + kNRound - 1) / kNRound * kNRound;
+    const int parts = (rows + NT - 1) / NT, n = ((rows + parts - 1) / parts + Cfg<NT>::kRound - 1) / Cfg<NT>::kRound * Cfg<NT>::kRound;
     const long long even = (long long)groups * parts * m_tiles, rounds = (even + dev.num_sms / 2 - 1) / (dev.num_sms / 2);
     const float step = 0.08f + 0.0012f * n;
     p.us = rounds * ((nk + p.splits - 1) / p.splits * step + 1.0f + (p.splits > 1 ? 0.5f + 0.009f * n : 0.0f));
@@ -517,7 +613,7 @@ cudaError_t plan_tiles(const RowsProduct& P, const DeviceInfo& dev, Plan* best) 
 }
 
 template <int NT, int SPLITS>
-cudaError_t launch_clusters(const Fp4Product& P, const TcRowMaps& maps, int tiles, WsHeader* hdr,
+cudaError_t launch_clusters(const Fp4Product& P, const Fp4Maps& maps, int tiles, WsHeader* hdr,
                             const DeviceInfo& dev, uint64_t wait_limit, cudaStream_t s) {
     int resident = 0;
     if (cudaError_t e = resident_clusters<NT, SPLITS>(dev, &resident); e != cudaSuccess) return e;
@@ -527,20 +623,36 @@ cudaError_t launch_clusters(const Fp4Product& P, const TcRowMaps& maps, int tile
                       m_tiles, tiles, hdr, (unsigned long long)wait_limit);
 }
 
+// [rows, KB] block scales, read as box_rows x 32 bytes, 32-byte swizzled in shared memory.
+bool encode_scales(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* m, const void* base, uint64_t KB, uint64_t rows,
+                   uint32_t box_rows) {
+    const cuuint64_t dims[2] = {KB, rows};
+    const cuuint64_t strides[1] = {KB};
+    const cuuint32_t box[2] = {kSectorBytes, box_rows};
+    const cuuint32_t one[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int NT>
 cudaError_t launch_tiles(const Fp4Product& P, const Plan& plan, WsHeader* hdr, const DeviceInfo& dev,
                          uint64_t wait_limit, cudaStream_t s) {
-    using C = Cfg<NT>;
     PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
-    TcRowMaps maps;
+    Fp4Maps maps;
     const uint64_t bytes = P.r.K / 2;
     if (fn == nullptr || !encode_rows(fn, &maps.w, P.r.w, true, bytes, (uint64_t)P.r.E * P.r.N, kM)) return cudaErrorInvalidValue;
-    for (int i = 0; i < (P.r.gather ? 1 : C::kBoxes); ++i)
-        if (!encode_rows(fn, &maps.x[i], P.r.x, true, bytes, P.r.x_rows, P.r.gather ? 1 : (i + 1) * C::kBoxRows))
-            return cudaErrorInvalidValue;
+    if (!encode_rows(fn, &maps.x, P.r.x, true, bytes, P.r.x_rows, P.r.gather ? 1 : Cfg<NT>::kBoxRows)) return cudaErrorInvalidValue;
+    maps.ws = maps.xs = maps.w;
+    if (const uint64_t KB = P.r.K / 16; KB % 16 == 0 &&
+        (!encode_scales(fn, &maps.ws, P.ws, KB, (uint64_t)P.r.E * P.r.N, kM) ||
+         !encode_scales(fn, &maps.xs, P.xs, KB, P.r.x_rows, P.r.gather ? 1 : NT)))
+        return cudaErrorInvalidValue;
     const int tiles = (int)plan.tiles;
-    if (plan.splits == 4) return launch_clusters<NT, 4>(P, maps, tiles, hdr, dev, wait_limit, s);
-    if (plan.splits == 2) return launch_clusters<NT, 2>(P, maps, tiles, hdr, dev, wait_limit, s);
+    if constexpr (NT <= 128) {
+        if (plan.splits == 4) return launch_clusters<NT, 4>(P, maps, tiles, hdr, dev, wait_limit, s);
+        if (plan.splits == 2) return launch_clusters<NT, 2>(P, maps, tiles, hdr, dev, wait_limit, s);
+    }
     return launch_clusters<NT, 1>(P, maps, tiles, hdr, dev, wait_limit, s);
 }
 
@@ -556,12 +668,12 @@ cudaError_t launch_rows_fp4(const Fp4Product& P, WsHeader* hdr, const DeviceInfo
         if ((e = plan_tiles<64>(P.r, dev, &plan)) != cudaSuccess) return e;
     } else {
         if ((e = plan_tiles<128>(P.r, dev, &plan)) != cudaSuccess) return e;
-        if ((e = plan_tiles<256>(P.r, dev, &plan)) != cudaSuccess) return e;
+        if ((e = plan_tiles<224>(P.r, dev, &plan)) != cudaSuccess) return e;
     }
     if (plan.tiles > kMaxTiles) return cudaErrorInvalidConfiguration;
     if (plan.nt == 64) return launch_tiles<64>(P, plan, hdr, dev, wait_limit, s);
     if (plan.nt == 128) return launch_tiles<128>(P, plan, hdr, dev, wait_limit, s);
-    return launch_tiles<256>(P, plan, hdr, dev, wait_limit, s);
+    return launch_tiles<224>(P, plan, hdr, dev, wait_limit, s);
 }
 
 }  // namespace nvfp4
