@@ -43,6 +43,7 @@ constexpr int kEpiWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kGatherWarp0 = 18, k
 
 template <int NT>
 struct Cfg {
+    static constexpr int kNT = NT;
     static constexpr int kRound = NT > 128 ? 32 : kNRound;       // a tile's columns are a multiple of this
     static constexpr int kXBlocks = (NT + 127) / 128, kBlocks = 1 + kXBlocks;     // of 128 rows' scales
     static constexpr int kThreads = 32 * (kScaleWarp0 + kBlocks);
@@ -58,8 +59,12 @@ struct Cfg {
     static constexpr int kSf = kBufs * NT, kSfSets = NT > 128 ? 1 : 2;
     static constexpr int kCols = NT / 4;                         // columns of an epilogue warp, at most
     static constexpr int kOffStg = kOffSlots + kSlots * kSlotBytes;
-    static constexpr int kOffBars = kOffStg + kEpiWarps * kStgRows * kStgPitch;
-    static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 3 * kSlots + 1;
+    // what the epilogue needs of a tile: address of the row of y (0: none) and row scale of its columns, tensor scale of
+    // the CTA's outputs, its rows and first output
+    static constexpr int kEndsBytes = NT * 12 + kM * 4 + 16, kEnds = 3;
+    static constexpr int kOffEnds = kOffStg + kEpiWarps * kStgRows * kStgPitch;
+    static constexpr int kOffBars = kOffEnds + kEnds * kEndsBytes;
+    static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 3 * kSlots + 2 * kEnds + 1;
     static constexpr int kOffTab = kOffBars + kNumBars * 8 + 16; // tile prefix [E + 1], first position [E], rows [E]
     static constexpr int kSmem = 1024 + kOffTab + (3 * NVFP4_MAX_EXPERTS + 1) * 4;
     static_assert(NT % kRound == 0 && NT <= 256 && kStage % 1024 == 0 && NT / 2 % kBoxRows == 0, "swizzle atoms, copies");
@@ -113,20 +118,22 @@ __device__ __forceinline__ void load_row(const uint8_t* row, int m, int KB, uint
 }
 
 // A warp that puts the scales of 128 rows (blk 0: of W, then of x) of two steps after two steps into line order, in place:
-// from the sectors that the TMA brought, row after row, or (UNIT 2, 4) from global memory.
+// from the sectors that the TMA brought, row after row, or (UNIT 2, 4) from global memory. Behind a tile's scales it looks
+// up what the epilogue needs of these 128 rows: the loads' latency is hidden under the tile's MMAs.
 template <typename C, int UNIT>
 __device__ __forceinline__ void scale_warp(const Fp4Product& Q, WalkOf<C::kRound> at, int pairs, int m_begin, int blk,
                                            int rank, uint8_t* slots, uint64_t* raw, uint64_t* ready, uint64_t* empty,
-                                           const Waiter& wait) {
+                                           uint8_t* ends, uint64_t* ends_full, uint64_t* ends_empty, const Waiter& wait) {
     const RowsProduct& P = Q.r;
     const int lane = threadIdx.x & 31, KB = P.K / 16;
-    int slot = 0;
-    uint32_t par = 0;
+    const int part_rows = P.N / Q.parts;
+    int slot = 0, end = 0;
+    uint32_t par = 0, end_par = 0;
 #pragma unroll 1
     for (; at.more(); at.next()) {
+        const auto t = at.tile();
         const uint8_t* row[4] = {};          // UNIT 2, 4: this lane's rows; null: no such row
         if constexpr (UNIT < 16) {
-            const auto t = at.tile();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (blk == 0) {
@@ -173,7 +180,54 @@ __device__ __forceinline__ void scale_warp(const Fp4Product& Q, WalkOf<C::kRound
             if (elect_one()) mbar_arrive(&ready[slot]);
             if (++slot == C::kSlots) slot = 0, par ^= 1u;
         }
+        // every load of a kind is asked for before the first is used
+        unsigned long long* to = reinterpret_cast<unsigned long long*>(ends + end * C::kEndsBytes);
+        float* scale = reinterpret_cast<float*>(to + C::kNT);
+        float* tensor = scale + C::kNT;
+        int* tile = reinterpret_cast<int*>(tensor + kM);
+        float f[4];
+        int d[4] = {-1, -1, -1, -1};
+        if (blk == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                f[i] = Q.wt[(size_t)t.e * Q.parts + min(t.m0 + rank * kM + 32 * i + lane, P.N - 1) / part_rows];
+        } else {
+            int src[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = t.r0 + min((blk - 1) * 128 + 32 * i + lane, t.n - 1);
+                src[i] = x_row(P, r), d[i] = y_row(P, r);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = Q.xr[max(src[i], 0)];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (src[i] < 0) f[i] = 0.f;
+                if ((blk - 1) * 128 + 32 * i + lane >= t.n) d[i] = -1;
+            }
+        }
+        if (!wait(&ends_empty[end], end_par ^ 1u)) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (blk == 0) {
+                tensor[32 * i + lane] = f[i];
+            } else if (const int col = (blk - 1) * 128 + 32 * i + lane; col < C::kNT) {
+                scale[col] = f[i];
+                to[col] = d[i] < 0 ? 0ull : (unsigned long long)P.y + ((unsigned long long)d[i] * P.N << (P.y_f32 ? 2 : 1));
+            }
+        }
+        if (blk == 0 && lane == 0) tile[0] = t.n, tile[1] = t.m0;
+        __syncwarp();
+        if (elect_one()) mbar_arrive(&ends_full[end]);
+        if (++end == C::kEnds) end = 0, end_par ^= 1u;
     }
+}
+
+// (a, b) *= s * t, each product rounded: the packed fp32 pipe.
+__device__ __forceinline__ void scale2(float& a, float& b, const float2 s, float t) {
+    asm("{\n .reg .b64 v, s, t;\n mov.b64 v, {%0, %1};\n mov.b64 s, {%2, %3};\n mov.b64 t, {%4, %4};\n"
+        " mul.rn.f32x2 s, s, t;\n mul.rn.f32x2 v, v, s;\n mov.b64 {%0, %1}, v;\n}"
+        : "+f"(a), "+f"(b) : "f"(s.x), "f"(s.y), "f"(t));
 }
 
 // SPLITS: pairs of a cluster, which share a tile's K.
@@ -199,7 +253,9 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
     uint64_t* sf_raw = acc_empty + C::kBufs;                           // scales of two steps landed
     uint64_t* sf_ready = sf_raw + C::kSlots;                           // ... and are in line order
     uint64_t* sf_empty = sf_ready + C::kSlots;                         // ... and copied to tensor memory
-    uint64_t* done = sf_empty + C::kSlots;                             // every MMA of the pair
+    uint64_t* ends_full = sf_empty + C::kSlots;                        // scales and rows of a tile's outputs
+    uint64_t* ends_empty = ends_full + C::kEnds;                       // ... and read
+    uint64_t* done = ends_empty + C::kEnds;                            // every MMA of the pair
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* tab = reinterpret_cast<int*>(sm + C::kOffTab);
@@ -219,6 +275,10 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                 mbar_init(&sf_raw[i], 1 + (P.gather ? kGatherWarps : 0));
                 mbar_init(&sf_ready[i], C::kBlocks);
                 mbar_init(&sf_empty[i], 1);
+            }
+            for (int i = 0; i < C::kEnds; ++i) {
+                mbar_init(&ends_full[i], C::kBlocks);
+                mbar_init(&ends_empty[i], kEpiWarps);
             }
             mbar_init(done, 1);
             *abort_flag = 0;
@@ -429,9 +489,13 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
         } else {
             const int blk = warp - kScaleWarp0;
             uint8_t* slots = sm + C::kOffSlots;
-            if (sf_tma) scale_warp<C, 16>(Q, tiles, m_pairs, m_begin, blk, rank, slots, sf_raw, sf_ready, sf_empty, wait);
-            else if (KB % 4 == 0) scale_warp<C, 4>(Q, tiles, m_pairs, m_begin, blk, rank, slots, sf_raw, sf_ready, sf_empty, wait);
-            else scale_warp<C, 2>(Q, tiles, m_pairs, m_begin, blk, rank, slots, sf_raw, sf_ready, sf_empty, wait);
+            const auto run = [&](auto unit) {
+                scale_warp<C, decltype(unit)::value>(Q, tiles, m_pairs, m_begin, blk, rank, slots, sf_raw, sf_ready, sf_empty,
+                                                     sm + C::kOffEnds, ends_full, ends_empty, wait);
+            };
+            if (sf_tma) run(std::integral_constant<int, 16>{});
+            else if (KB % 4 == 0) run(std::integral_constant<int, 4>{});
+            else run(std::integral_constant<int, 2>{});
         }
         if (SPLITS > 1 && tiles.more()) exchange.join();
     } else {
@@ -439,106 +503,161 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
         uint8_t* stg = sm + C::kOffStg + warp * (kStgRows * kStgPitch);
         const int p = lane & 3, g = lane >> 2;
         const uint32_t first_acc_empty = map_rank(su32(acc_empty), first_rank);
-        const int part_rows = P.N / Q.parts;
-        // First column of this warp's chunk i of 16: chunks go round the warps; pairs that share a tile exchange
-        // neighbouring ones.
-        const auto chunk = [&](const Tile& t, int i) { return SPLITS > 1 ? part * (t.mma_n() / 4) + 16 * i : 16 * (4 * i + part); };
-        // What the outputs of a tile need besides the sums. dst, scale of lane l: row of y (or -1) and row scale of
-        // column l % 16 of chunks l / 16 and 2 + l / 16; wt: tensor scales of outputs 8 i + g.
-        struct Ends {
-            int dst[2];
-            float scale[2], wt[4];
-        };
-        const auto ends_of = [&](const Tile& t) {
-            Ends e;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int k = 2 * i + (lane >> 4), col = chunk(t, k) + (lane & 15);
-                e.dst[i] = -1, e.scale[i] = 0.f;
-                if ((SPLITS == 1 || 16 * k < t.mma_n() / 4) && col < t.n) {
-                    const int src = x_row(P, t.r0 + col);
-                    e.dst[i] = y_row(P, t.r0 + col);
-                    if (src >= 0) e.scale[i] = Q.xr[src];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = t.m0 + rank * kM + 32 * q + 8 * i + g;
-                e.wt[i] = n < P.N ? Q.wt[(size_t)t.e * Q.parts + n / part_rows] : 0.f;
-            }
-            return e;
-        };
-        int use = 0;               // buffers read so far
+        const int tiles_here = tiles.more() ? (total - 1 - tiles.i) / tiles.step + 1 : 0;
+        int end = 0;
+        uint32_t end_par = 0;
         bool ok = true;
-        Walk at = tiles;
-        Tile t{};
-        Ends ends{};
-        if (at.more()) t = at.tile(), ends = ends_of(t);
 #pragma unroll 1
-        while (at.more()) {
-            const int n0 = t.m0 + rank * kM + 32 * q;                      // first output
-            // the next tile's are asked for under this one's MMAs
-            at.next();
-            Tile t2 = t;
-            Ends ends2 = ends;
-            if (at.more()) t2 = at.tile(), ends2 = ends_of(t2);
+        for (int use = 0; use < tiles_here; ++use) {
             const int buf = use % C::kBufs;
             const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + buf * NT;
+            if (ok) ok = wait(&ends_full[end], end_par);
+            const unsigned long long* to = reinterpret_cast<const unsigned long long*>(sm + C::kOffEnds + end * C::kEndsBytes);
+            const float* scale = reinterpret_cast<const float*>(to + NT);
+            const float* tensor = scale + NT;
+            int rows = reinterpret_cast<const int*>(tensor + kM)[0], m0 = reinterpret_cast<const int*>(tensor + kM)[1], r0 = 0;
+            float wt[4];                                                   // tensor scales of outputs n0 + 8 i + g
+#pragma unroll
+            for (int i = 0; i < 4; ++i) wt[i] = tensor[32 * q + 8 * i + g];
             if (ok) ok = wait(&acc_full[buf], (use / C::kBufs) & 1);
+            if (!ok) {                                                     // an abandoned call: nobody looked this tile up
+                Walk at = tiles;
+                for (int i = 0; i < use; ++i) at.next();
+                const Tile t = at.tile();
+                rows = t.n, m0 = t.m0, r0 = t.r0;
+            }
             tc_fence_after();
-            const auto finish = [&](int i, float (&v)[16]) {
-                const float sc = i & 2 ? ends.scale[1] : ends.scale[0];
-                float s4[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    s4[k] = __shfl_sync(0xffffffffu, sc, (i & 1) * 16 + 8 * (k >> 1) + 2 * p + (k & 1));
-#pragma unroll
-                for (int k = 0; k < 16; ++k)     // lane group 2 L + u, column 2 j + b of the fragment
-                    v[k] *= s4[2 * ((k >> 2) & 1) + (k & 1)] * ends.wt[2 * (k >> 3) + ((k >> 1) & 1)];
-                if (*abort_flag)
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(0x7FC00000u);
-                store_frag(P, v, __shfl_sync(0xffffffffu, i & 2 ? ends.dst[1] : ends.dst[0], (i & 1) * 16 + (lane & 15)), n0, stg);
-            };
+            const int n0 = m0 + rank * kM + 32 * q;                        // first output
+            const int width = ((rows + C::kRound - 1) & ~(C::kRound - 1)) / 4;
             const auto hand_back = [&] {
                 tc_fence_before();
                 __syncwarp();
                 if (ok && elect_one()) arrive_cluster(first_acc_empty + 8 * buf);
             };
+            // sums of columns c .. c + 15 times their two scales; v[8 L + 4 j + 2 u + b]: output 16 L + 8 u + g, column
+            // 8 j + 2 p + b
+            const auto scaled = [&](int c, float (&v)[16]) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float2 s = *reinterpret_cast<const float2*>(scale + c + 8 * j + 2 * p);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = 8 * (i >> 1) + 4 * j + 2 * (i & 1);
+                        scale2(v[k], v[k + 1], s, wt[i]);
+                    }
+                }
+                if (!ok)
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(0x7FC00000u);
+            };
+            // rows of y that are no multiple of 16 bytes, fp32, and abandoned calls
+            const auto store_any = [&](int c, const float (&v)[16]) {
+                const int col = c + (lane & 15);
+                int d = -1;
+                if (col < rows) {
+                    if (ok) {
+                        const unsigned long long a = to[col];
+                        if (a != 0) d = (int)((a - (unsigned long long)P.y >> (P.y_f32 ? 2 : 1)) / (unsigned long long)P.N);
+                    } else {
+                        d = y_row(P, r0 + col);
+                    }
+                }
+                store_frag(P, v, d, n0, stg);
+            };
+            // bf16 with rows of whole 16-byte pieces: 16 rows of 32 outputs through shared memory. Piece m of row r lies at
+            // 64 r + 16 (m ^ (r >> 1) % 4): neither eight rows of a piece nor two whole rows meet on a bank.
+            const uint32_t st_to = su32(stg) + (lane & 7) * 64 + 16 * ((lane >> 3) ^ ((lane >> 1) & 3));
+            const uint8_t* st_from = stg + g * 64 + 16 * (p ^ ((g >> 1) & 3));
+            const bool piece = n0 + 8 * p < P.N;
+            const auto store16 = [&](int c, const uint32_t (&w)[8]) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                                 :: "r"(st_to + 512 * j), "r"(w[4 * j]), "r"(w[4 * j + 1]), "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
+                                 : "memory");
+                const unsigned long long a0 = to[c + g], a1 = to[c + 8 + g];
+                __syncwarp();
+                const uint4 u0 = *reinterpret_cast<const uint4*>(st_from), u1 = *reinterpret_cast<const uint4*>(st_from + 512);
+                const unsigned long long o = 2ull * (unsigned)(n0 + 8 * p);
+                if (a0 != 0 && piece) *reinterpret_cast<uint4*>(a0 + o) = u0;
+                if (a1 != 0 && piece) *reinterpret_cast<uint4*>(a1 + o) = u1;
+                __syncwarp();
+            };
+            const auto packed = [&](const float (&v)[16], uint32_t (&w)[8]) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = 8 * (i >> 1) + 4 * j + 2 * (i & 1);
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[4 * j + i]) : "f"(v[k + 1]), "f"(v[k]));
+                    }
+            };
+            const bool plain = ok && !P.y_f32 && (P.N & 7) == 0;
             if constexpr (SPLITS > 1) {
-                const int width = t.mma_n() / 4, c0 = part * width;            // this warp's columns of the tile
+                const int c0 = part * width;                               // this warp's columns of the tile
                 const auto sums = [&](int c, float (&v)[16]) {
                     if (ok) {
                         tmem_ld_frag(lanes + c0 + c, v);
                         tmem_wait16(v);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(0x7FC00000u);
                     }
                 };
+                Tile t{};
+                t.n = rows;
                 exchange.send(sums, t, width, c0, part, q);
 #pragma unroll
                 for (int c = 0; c < C::kCols; c += 16) {
-                    if (c >= width || c0 + c >= t.n) break;
+                    if (c >= width || c0 + c >= rows) break;
                     float v[16];
                     sums(c, v);
-                    if (exchange.finish(v, c, width, part, q)) finish(c / 16, v);
+                    if (!exchange.finish(v, c, width, part, q)) continue;
+                    scaled(c0 + c, v);
+                    if (plain) {
+                        uint32_t w[8];
+                        packed(v, w);
+                        store16(c0 + c, w);
+                    } else {
+                        store_any(c0 + c, v);
+                    }
                 }
             } else {
-                // A buffer is handed back when its last chunk is in registers.
-                const int chunks = (t.n - 16 * part + 63) / 64;            // none where it is not positive
-#pragma unroll 1
-                for (int i = 0; i < chunks; ++i) {
-                    float v[16];
-                    if (ok) {
-                        tmem_ld_frag(lanes + chunk(t, i), v);
-                        tmem_wait16(v);
-                    }
-                    if (i == chunks - 1) hand_back();
-                    finish(i, v);
-                }
+                // Chunks of 16 columns go round the warps; the next is asked for before this one is written. A buffer is
+                // handed back when its last chunk is in registers.
+                const int chunks = (rows - 16 * part + 63) / 64;           // none where it is not positive
+                float v[16];
                 if (chunks <= 0) hand_back();
+                if (plain) {
+                    if (chunks > 0) tmem_ld_frag(lanes + 16 * part, v);
+#pragma unroll 1
+                    for (int i = 0; i < chunks; ++i) {
+                        const int c = 64 * i + 16 * part;
+                        tmem_wait16(v);
+                        if (i == chunks - 1) hand_back();
+                        scaled(c, v);
+                        uint32_t w[8];
+                        packed(v, w);
+                        if (i + 1 < chunks) tmem_ld_frag(lanes + c + 64, v);
+                        store16(c, w);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < chunks; ++i) {
+                        const int c = 64 * i + 16 * part;
+                        if (ok) {
+                            tmem_ld_frag(lanes + c, v);
+                            tmem_wait16(v);
+                        }
+                        if (i == chunks - 1) hand_back();
+                        scaled(c, v);
+                        store_any(c, v);
+                    }
+                }
             }
-            ++use;
-            t = t2;
-            ends = ends2;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ends_empty[end]);
+            if (++end == C::kEnds) end = 0, end_par ^= 1u;
         }
     }
     tc_fence_before();
