@@ -38,8 +38,9 @@ constexpr int kBlkBytes = kM * kSectorBytes; // block scales of 128 rows in two 
 constexpr int kMaxStages = 9;
 constexpr int kMinSteps = 2;             // steps of each pair that shares a tile's K, at least
 
-// Warps: 16 of epilogue, TMA, MMA, four of gather, one for every 128 rows of scales.
-constexpr int kEpiWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kGatherWarp0 = 18, kGatherWarps = 4, kScaleWarp0 = 22;
+// Warps: 16 of epilogue, TMA, MMA, four of gather, one that looks up the tiles' ends, one for every 128 rows of scales.
+constexpr int kEpiWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kGatherWarp0 = 18, kGatherWarps = 4, kEndsWarp = 22;
+constexpr int kScaleWarp0 = 23;
 
 template <int NT>
 struct Cfg {
@@ -118,22 +119,20 @@ __device__ __forceinline__ void load_row(const uint8_t* row, int m, int KB, uint
 }
 
 // A warp that puts the scales of 128 rows (blk 0: of W, then of x) of two steps after two steps into line order, in place:
-// from the sectors that the TMA brought, row after row, or (UNIT 2, 4) from global memory. Behind a tile's scales it looks
-// up what the epilogue needs of these 128 rows: the loads' latency is hidden under the tile's MMAs.
+// from the sectors that copies brought, row after row, or (UNIT 2, 4) from global memory.
 template <typename C, int UNIT>
 __device__ __forceinline__ void scale_warp(const Fp4Product& Q, WalkOf<C::kRound> at, int pairs, int m_begin, int blk,
                                            int rank, uint8_t* slots, uint64_t* raw, uint64_t* ready, uint64_t* empty,
-                                           uint8_t* ends, uint64_t* ends_full, uint64_t* ends_empty, const Waiter& wait) {
+                                           const Waiter& wait) {
     const RowsProduct& P = Q.r;
     const int lane = threadIdx.x & 31, KB = P.K / 16;
-    const int part_rows = P.N / Q.parts;
-    int slot = 0, end = 0;
-    uint32_t par = 0, end_par = 0;
+    int slot = 0;
+    uint32_t par = 0;
 #pragma unroll 1
     for (; at.more(); at.next()) {
-        const auto t = at.tile();
         const uint8_t* row[4] = {};          // UNIT 2, 4: this lane's rows; null: no such row
         if constexpr (UNIT < 16) {
+            const auto t = at.tile();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (blk == 0) {
@@ -180,46 +179,66 @@ __device__ __forceinline__ void scale_warp(const Fp4Product& Q, WalkOf<C::kRound
             if (elect_one()) mbar_arrive(&ready[slot]);
             if (++slot == C::kSlots) slot = 0, par ^= 1u;
         }
-        // every load of a kind is asked for before the first is used
+    }
+}
+
+// The warp that looks up what the epilogue needs of a tile: for its columns row scale and address of the row of y, for the
+// CTA's outputs the tensor scale. The list entries of the next tile are asked for with this one's scales.
+template <typename C>
+__device__ __forceinline__ void ends_warp(const Fp4Product& Q, WalkOf<C::kRound> at, int rank, uint8_t* ends,
+                                          uint64_t* ends_full, uint64_t* ends_empty, const Waiter& wait) {
+    constexpr int kPer = C::kNT / 32;
+    const RowsProduct& P = Q.r;
+    const int lane = threadIdx.x & 31, part_rows = P.N / Q.parts;
+    const bool listed = P.gather || P.scatter;
+    if (!at.more()) return;
+    auto t = at.tile();
+    int entry[kPer];
+    const auto ask = [&] {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int r = t.r0 + min(32 * i + lane, t.n - 1);
+            entry[i] = listed ? P.list[r] : r;
+        }
+    };
+    ask();
+    int end = 0;
+    uint32_t par = 0;
+#pragma unroll 1
+    for (bool more = true; more;) {
+        const auto now = t;
+        int src[kPer], d[kPer];
+        float f[kPer], w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = Q.wt[(size_t)now.e * Q.parts + min(now.m0 + rank * kM + 32 * i + lane, P.N - 1) / part_rows];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int col = 32 * i + lane, r = now.r0 + min(col, now.n - 1);
+            const bool good = (unsigned)entry[i] < (unsigned)P.R;
+            src[i] = P.gather ? (good ? entry[i] / P.k : -1) : r;
+            d[i] = col < now.n ? (P.scatter ? (good ? entry[i] : -1) : r) : -1;
+            f[i] = Q.xr[max(src[i], 0)];
+        }
+        at.next();
+        more = at.more();
+        if (more) t = at.tile(), ask();
+        if (!wait(&ends_empty[end], par ^ 1u)) return;
         unsigned long long* to = reinterpret_cast<unsigned long long*>(ends + end * C::kEndsBytes);
         float* scale = reinterpret_cast<float*>(to + C::kNT);
         float* tensor = scale + C::kNT;
         int* tile = reinterpret_cast<int*>(tensor + kM);
-        float f[4];
-        int d[4] = {-1, -1, -1, -1};
-        if (blk == 0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                f[i] = Q.wt[(size_t)t.e * Q.parts + min(t.m0 + rank * kM + 32 * i + lane, P.N - 1) / part_rows];
-        } else {
-            int src[4];
+        for (int i = 0; i < 4; ++i) tensor[32 * i + lane] = w[i];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = t.r0 + min((blk - 1) * 128 + 32 * i + lane, t.n - 1);
-                src[i] = x_row(P, r), d[i] = y_row(P, r);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = Q.xr[max(src[i], 0)];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (src[i] < 0) f[i] = 0.f;
-                if ((blk - 1) * 128 + 32 * i + lane >= t.n) d[i] = -1;
-            }
+        for (int i = 0; i < kPer; ++i) {
+            scale[32 * i + lane] = src[i] < 0 ? 0.f : f[i];
+            to[32 * i + lane] = d[i] < 0 ? 0ull : (unsigned long long)P.y + ((unsigned long long)d[i] * P.N << (P.y_f32 ? 2 : 1));
         }
-        if (!wait(&ends_empty[end], end_par ^ 1u)) return;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (blk == 0) {
-                tensor[32 * i + lane] = f[i];
-            } else if (const int col = (blk - 1) * 128 + 32 * i + lane; col < C::kNT) {
-                scale[col] = f[i];
-                to[col] = d[i] < 0 ? 0ull : (unsigned long long)P.y + ((unsigned long long)d[i] * P.N << (P.y_f32 ? 2 : 1));
-            }
-        }
-        if (blk == 0 && lane == 0) tile[0] = t.n, tile[1] = t.m0;
+        if (lane == 0) tile[0] = now.n, tile[1] = now.m0;
         __syncwarp();
         if (elect_one()) mbar_arrive(&ends_full[end]);
-        if (++end == C::kEnds) end = 0, end_par ^= 1u;
+        if (++end == C::kEnds) end = 0, par ^= 1u;
     }
 }
 
@@ -272,12 +291,12 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                 mbar_init(&acc_empty[i], 2 * kEpiWarps);
             }
             for (int i = 0; i < C::kSlots; ++i) {
-                mbar_init(&sf_raw[i], 1 + (P.gather ? kGatherWarps : 0));
+                mbar_init(&sf_raw[i], 1 + (P.gather ? 32 * kGatherWarps : 0));
                 mbar_init(&sf_ready[i], C::kBlocks);
                 mbar_init(&sf_empty[i], 1);
             }
             for (int i = 0; i < C::kEnds; ++i) {
-                mbar_init(&ends_full[i], C::kBlocks);
+                mbar_init(&ends_full[i], 1);
                 mbar_init(&ends_empty[i], kEpiWarps);
             }
             mbar_init(done, 1);
@@ -419,48 +438,49 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                 if (rank == 0) commit_pair(done, pair_mask);
                 drain_wait(done, 0);
             }
-        } else if (warp < kScaleWarp0) {
+        } else if (warp == kEndsWarp) {
+            ends_warp<C>(Q, tiles, rank, sm + C::kOffEnds, ends_full, ends_empty, wait);
+        } else if (warp < kEndsWarp) {
             if (P.gather) {
                 // copies of four rows, in turn over the warps: at most kPer a warp and step; lane 4 j + r has
                 // row r of this warp's copy j
                 constexpr int kPer = (NT / 2 / 4 + kGatherWarps - 1) / kGatherWarps;
                 const int w = warp - kGatherWarp0;
-                // and of all columns' scales: copies of four rows in turn over the warps, kSfPer a warp
-                constexpr int kSfPer = NT / 4 / kGatherWarps, kSfRegs = (4 * kSfPer + 31) / 32;
+                // and the scales of all columns, 16 bytes a lane, two lanes a row: lane pair l of the four warps has rows l,
+                // 64 + l, ... (gathered by TMA, rows of 32 bytes cost as much as rows of 128)
+                constexpr int kSfPer = (NT + 63) / 64;
+                const int half = lane & 1, sf_l = 16 * w + (lane >> 1);
                 int step = 0, two = 0;
                 bool ok = true;
 #pragma unroll 1
                 for (Walk at = tiles; at.more() && ok; at.next()) {
                     const Tile t = at.tile();
                     const int share = t.mma_n() / 2, copies = share / 4;
-                    const auto row_of = [&](int col) {
-                        const int src = col < t.n ? x_row(P, t.r0 + col) : -1;
-                        return src < 0 ? P.x_rows : src;             // past the last row: zeros
-                    };
+                    const auto row_of = [&](int col) { return col < t.n ? x_row(P, t.r0 + col) : -1; };
                     const int l = 4 * (w + kGatherWarps * (lane >> 2)) + (lane & 3);
-                    const int src = row_of(l < share ? rank * share + l : t.n);
-                    int sf_src[kSfRegs];
+                    int src = row_of(l < share ? rank * share + l : t.n);
+                    if (src < 0) src = P.x_rows;                     // past the last row: zeros
+                    int sf_src[kSfPer];
 #pragma unroll
-                    for (int i = 0; i < kSfRegs; ++i)
-                        sf_src[i] = row_of(4 * (w + kGatherWarps * ((32 * i + lane) >> 2)) + (lane & 3));
+                    for (int i = 0; i < kSfPer; ++i) sf_src[i] = row_of(64 * i + sf_l);
                     const int mine = (copies - w + kGatherWarps - 1) / kGatherWarps;
 #pragma unroll 1
                     for (int s = s_begin; s < s_end; ++s, ++step) {
                         if (sf_tma && (s == s_begin || (s & 1) == 0)) {
-                            const int sl = two % C::kSlots, u = two / C::kSlots;
+                            const int sl = two % C::kSlots, u = two / C::kSlots, byte = (s >> 1) * kSectorBytes + 16 * half;
                             if (u > 0) ok = wait(&sf_empty[sl], (u - 1) & 1);
                             if (!ok) break;
-                            const uint32_t to = sm_base + C::kOffSlots + sl * C::kSlotBytes + kBlkBytes + w * 4 * kSectorBytes;
-                            if (elect_one()) mbar_arrive_expect_tx(&sf_raw[sl], kSfPer * 4 * kSectorBytes);
+                            // in the order of the 32-byte swizzle: the halves of rows 4 .. 7 of every eight change places
+                            const uint32_t to = sm_base + C::kOffSlots + sl * C::kSlotBytes + kBlkBytes + sf_l * kSectorBytes +
+                                                16 * (half ^ ((sf_l >> 2) & 1));
 #pragma unroll
-                            for (int j = 0; j < kSfPer; ++j) {
-                                const int v = sf_src[4 * j / 32];
-                                const int r0 = __shfl_sync(0xffffffffu, v, 4 * j & 31), r1 = __shfl_sync(0xffffffffu, v, (4 * j & 31) + 1);
-                                const int r2 = __shfl_sync(0xffffffffu, v, (4 * j & 31) + 2), r3 = __shfl_sync(0xffffffffu, v, (4 * j & 31) + 3);
-                                if (elect_one())
-                                    tma_gather4(to + j * (kGatherWarps * 4 * kSectorBytes), &maps.xs, (s >> 1) * kSectorBytes,
-                                                r0, r1, r2, r3, &sf_raw[sl]);
+                            for (int i = 0; i < kSfPer; ++i) {
+                                if (64 * i + sf_l >= NT) break;
+                                const bool there = sf_src[i] >= 0 && byte < KB;
+                                cp_async16_zfill(to + i * 64 * kSectorBytes, there ? Q.xs + (size_t)sf_src[i] * KB + byte : Q.xs,
+                                                 there ? 16 : 0);
                             }
+                            cp_async_arrive_noinc(&sf_raw[sl]);
                             ++two;
                         }
                         const int st = step % C::kStages, u = step / C::kStages;
@@ -481,6 +501,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                         }
                     }
                 }
+                asm volatile("cp.async.wait_all;" ::: "memory");
                 if (lane == 0) {
                     drain(step);
                     drain_scales(two);
@@ -490,8 +511,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
             const int blk = warp - kScaleWarp0;
             uint8_t* slots = sm + C::kOffSlots;
             const auto run = [&](auto unit) {
-                scale_warp<C, decltype(unit)::value>(Q, tiles, m_pairs, m_begin, blk, rank, slots, sf_raw, sf_ready, sf_empty,
-                                                     sm + C::kOffEnds, ends_full, ends_empty, wait);
+                scale_warp<C, decltype(unit)::value>(Q, tiles, m_pairs, m_begin, blk, rank, slots, sf_raw, sf_ready, sf_empty, wait);
             };
             if (sf_tma) run(std::integral_constant<int, 16>{});
             else if (KB % 4 == 0) run(std::integral_constant<int, 4>{});
