@@ -101,13 +101,13 @@ __device__ __forceinline__ uint32_t nvfp4_idesc(int N) {
     return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(2 * kM >> 7) << 27);
 }
 
-// Block scales of steps 2 m and 2 m + 1 of a row of KB, a number that is no multiple of 16: loads of UNIT (2 or 4) bytes.
-// Behind the end of the row: 0.
+// Block scales of step s of a row of KB, a number that is no multiple of 16: loads of UNIT (2 or 4) bytes. Behind the end
+// of the row: 0.
 template <int UNIT>
-__device__ __forceinline__ void load_row(const uint8_t* row, int m, int KB, uint32_t (&w)[8]) {
+__device__ __forceinline__ void load_row(const uint8_t* row, int s, int KB, uint32_t (&w)[4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int at = 32 * m + 4 * i;
+    for (int i = 0; i < 4; ++i) {
+        const int at = 16 * s + 4 * i;
         if constexpr (UNIT == 4) {
             w[i] = *reinterpret_cast<const uint32_t*>(row + min(at, KB - 4));
         } else {
@@ -118,7 +118,7 @@ __device__ __forceinline__ void load_row(const uint8_t* row, int m, int KB, uint
     }
 }
 
-// A warp that puts the scales of 128 rows (blk 0: of W, then of x) of two steps after two steps into line order, in place:
+// A warp that puts the scales of 128 rows (blk 0: of W, then of x) of two steps after two steps into line order: in place,
 // from the sectors that copies brought, row after row, or (UNIT 2, 4) from global memory.
 template <typename C, int UNIT>
 __device__ __forceinline__ void scale_warp(const Fp4Product& Q, WalkOf<C::kRound> at, int pairs, int m_begin, int blk,
@@ -130,38 +130,46 @@ __device__ __forceinline__ void scale_warp(const Fp4Product& Q, WalkOf<C::kRound
     uint32_t par = 0;
 #pragma unroll 1
     for (; at.more(); at.next()) {
-        const uint8_t* row[4] = {};          // UNIT 2, 4: this lane's rows; null: no such row
+        int row[4];                          // UNIT 2, 4: this lane's rows, or -1
         if constexpr (UNIT < 16) {
             const auto t = at.tile();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (blk == 0) {
                     const int n = t.m0 + rank * kM + 32 * i + lane;
-                    if (n < P.N) row[i] = Q.ws + ((size_t)t.e * P.N + n) * KB;
+                    row[i] = n < P.N ? t.e * P.N + n : -1;
                 } else {
                     const int col = (blk - 1) * 128 + 32 * i + lane;
-                    const int src = col < t.n ? x_row(P, t.r0 + col) : -1;
-                    if (src >= 0) row[i] = Q.xs + (size_t)src * KB;
+                    row[i] = col < t.n ? x_row(P, t.r0 + col) : -1;
                 }
             }
         }
 #pragma unroll 1
         for (int j = 0; j < pairs; ++j) {
             uint8_t* blkp = slots + slot * C::kSlotBytes + blk * kBlkBytes;
-            uint32_t w[4][8];
+            uint4* to = reinterpret_cast<uint4*>(blkp) + lane;
             if constexpr (UNIT < 16) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) w[i][k] = 0u;
-                    if (row[i] != nullptr) load_row<UNIT>(row[i], m_begin + j, KB, w[i]);
-                }
+                const uint8_t* base = blk == 0 ? Q.ws : Q.xs;
                 if (!wait(&empty[slot], par ^ 1u)) return;
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[4][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        load_row<UNIT>(base + (size_t)max(row[i], 0) * KB, 2 * (m_begin + j) + h, KB, w[i]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (row[i] < 0) w[i][k] = 0u;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) to[128 * h + 32 * k] = make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
+                }
             } else {
                 if (!wait(&raw[slot], par)) return;
+                uint32_t w[4][8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    // the copies swap the halves of rows 4 .. 7 of every eight (32-byte swizzle): no bank is read twice
+                    // the halves of rows 4 .. 7 of every eight have changed places (32-byte swizzle): no bank is read twice
                     const uint8_t* p = blkp + (32 * i + lane) * kSectorBytes;
                     const int odd = (lane >> 2) & 1;
                     const uint4 a = *reinterpret_cast<const uint4*>(p + 16 * odd);
@@ -170,10 +178,9 @@ __device__ __forceinline__ void scale_warp(const Fp4Product& Q, WalkOf<C::kRound
                     w[i][4] = b.x, w[i][5] = b.y, w[i][6] = b.z, w[i][7] = b.w;
                 }
                 __syncwarp();
-            }
-            uint4* to = reinterpret_cast<uint4*>(blkp) + lane;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) to[32 * k] = make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
+                for (int k = 0; k < 8; ++k) to[32 * k] = make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
+            }
             fence_proxy_async_smem();
             __syncwarp();
             if (elect_one()) mbar_arrive(&ready[slot]);
