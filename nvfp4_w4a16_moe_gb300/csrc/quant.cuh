@@ -46,22 +46,40 @@ __device__ __forceinline__ float row_scale(uint32_t amax_bits) {
 // 1 / s of a power of two 2^-126 .. 2^126.
 __device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
-// E4M3 code of a block whose largest magnitude is b row scales, and the reciprocal of its value (0 for code 0).
-// b / 6 of a bf16 b is on a rounding point of E4M3 exactly or off it by over 2^-13; the division rounds correctly.
+// 1 / x within 2^-23.
+__device__ __forceinline__ float fast_rcp(float x) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// E4M3 code of a block whose largest magnitude is b row scales, and the reciprocal of its value within 2^-23 (0 for code
+// 0). EXACT: b is bf16, so that b / 6 is on a rounding point of E4M3 or off it by over 2^-13: the product with 1 / 6,
+// within 2^-22 of it, goes back on the point when it is rounded to 16 bits.
+template <bool EXACT>
 __device__ __forceinline__ uint32_t nvfp4_block_scale(float b, float* inv) {
-    const uint32_t e = e4m3x2(__fdiv_rn(b, 6.0f), 0.f) & 0xFFu;
-    *inv = e == 0u ? 0.f : __fdiv_rn(1.0f, e4m3_to_f32(e));
+    const float q = b * (1.0f / 6.0f);
+    const uint32_t e = e4m3x2(EXACT ? snap16(q, 0x80u) : q, 0.f) & 0xFFu;
+    *inv = e == 0u ? 0.f : fast_rcp(e4m3_to_f32(e));
     return e;
 }
 
-// Eight values (in row scales) of a block -> eight codes, the first in the low four bits. EXACT: the values are
-// bf16, so that v / e (8 bits by at most 4) is on a rounding point of E2M1 or off it by over 2^-8: p, within 2^-22
-// of the quotient, goes back on the point when it is rounded to 16 bits.
+// (a, b) *= s, each product rounded: the packed fp32 pipe.
+__device__ __forceinline__ void mul2(float& a, float& b, float s) {
+    asm("{\n .reg .b64 v, s;\n mov.b64 v, {%0, %1};\n mov.b64 s, {%2, %2};\n mul.rn.f32x2 v, v, s;\n"
+        " mov.b64 {%0, %1}, v;\n}" : "+f"(a), "+f"(b) : "f"(s));
+}
+
+// Eight values (in row scales) of a block times 1 / its scale -> eight codes, the first in the low four bits. EXACT: the
+// values are bf16, so that v / e (8 bits by at most 4) is on a rounding point of E2M1 or off it by over 2^-8: p, within
+// 2^-22 of the quotient, goes back on the point when it is rounded to 16 bits.
 template <bool EXACT>
-__device__ __forceinline__ uint32_t nvfp4_codes8(const float (&v)[8], float inv) {
-    float p[8];
+__device__ __forceinline__ uint32_t nvfp4_codes8(float (&p)[8], float inv) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = EXACT ? snap16(v[i] * inv, 0x80u) : v[i] * inv;
+    for (int i = 0; i < 8; i += 2) mul2(p[i], p[i + 1], inv);
+    if (EXACT)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = snap16(p[i], 0x80u);
     uint32_t r;
     asm("{\n .reg .b8 a, b, c, d;\n"
         " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"

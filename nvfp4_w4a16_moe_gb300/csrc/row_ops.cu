@@ -57,12 +57,12 @@ __device__ __forceinline__ void load8(const void* base, size_t at, float (&v)[8]
         unpack8(ld_once_v4(static_cast<const uint16_t*>(base) + at), v);
     }
 }
-// |v| as fp32 bits: NaN above infinity above every number.
+// Largest |v| as fp32 bits: NaN above infinity above every number.
 __device__ __forceinline__ uint32_t absmax8(const float (&v)[8]) {
-    uint32_t m = 0;
+    float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    return m;
+    for (int i = 0; i < 8; i += 2) asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(v[i]), "f"(v[i + 1]));
+    return __float_as_uint(m) & 0x7FFFFFFFu;
 }
 
 // Over the threads of a row; s: one word a warp. All threads of the CTA call it.
@@ -87,7 +87,7 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, int group, uint32_t* s) 
 }
 
 template <int SRC, int OUT, int U>
-__global__ void __launch_bounds__(U == 8 ? NVFP4_MAX_ROW_K / 64 : kRowThreads)
+__global__ void __launch_bounds__(U >= 4 ? NVFP4_MAX_ROW_K / 64 : kRowThreads)
 rows_kernel(const RowParams P) {
     __shared__ float s_sum[32];
     __shared__ uint32_t s_max[32];
@@ -127,7 +127,7 @@ rows_kernel(const RowParams P) {
             load8<SRC == kSwiglu32>(P.in, g, v[u]);
             load8<SRC == kSwiglu32>(P.in, g + P.K, up);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] = __fdiv_rn(v[u][i], 1.0f + __expf(-v[u][i])) * up[i];
+            for (int i = 0; i < 8; ++i) v[u][i] = v[u][i] * fast_rcp(1.0f + __expf(-v[u][i])) * up[i];
         }
     }
     if constexpr (SRC == kNorm) {
@@ -159,15 +159,19 @@ rows_kernel(const RowParams P) {
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
             if (!here || unit >= units) continue;
-            const float inv = block_inverse(m);
-            if ((unit & 15) == 0) static_cast<float*>(P.out.scales)[row * KB + (unit >> 4)] = block_scale(m);
-            const bool tiny = __uint_as_float(m) < kTinyAmax;
+            // the values are fp32 with errors of their own: 448 / a and a / 448 within 2^-22 do
+            const float a = __uint_as_float(m);
+            const bool tiny = a < kTinyAmax;
+            const float inv = m == 0u ? 1.0f : kE4m3Max * fast_rcp(tiny ? a * 0x1p64f : a);
+            if ((unit & 15) == 0) static_cast<float*>(P.out.scales)[row * KB + (unit >> 4)] = m == 0u ? 1.0f : a * (1.0f / kE4m3Max);
+            if (tiny)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[u][i] *= 0x1p64f;
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) mul2(v[u][i], v[u][i + 1], inv);
             uint32_t h[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float lo = tiny ? v[u][2 * i] * 0x1p64f : v[u][2 * i], hi = tiny ? v[u][2 * i + 1] * 0x1p64f : v[u][2 * i + 1];
-                h[i] = e4m3x2(lo * inv, hi * inv);
-            }
+            for (int i = 0; i < 4; ++i) h[i] = e4m3x2(v[u][2 * i], v[u][2 * i + 1]);
             *reinterpret_cast<uint2*>(static_cast<uint8_t*>(P.out.data) + row * P.K + unit * 8) =
                 make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
         }
@@ -186,9 +190,9 @@ rows_kernel(const RowParams P) {
             m[u] = max(m[u], __shfl_xor_sync(0xffffffffu, m[u], 1));     // two lanes hold a block of 16
             if (!here || unit >= units) continue;
             float inv;
-            const uint32_t e = finite ? nvfp4_block_scale(__uint_as_float(m[u]) * is, &inv) : (inv = 0.f, 0u);
+            const uint32_t e = nvfp4_block_scale<SRC == kPlain>(finite ? __uint_as_float(m[u]) * is : 0.f, &inv);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] *= is;
+            for (int i = 0; i < 8; i += 2) mul2(v[u][i], v[u][i + 1], is);
             const size_t at = row * (P.K >> 3) + unit;
             static_cast<uint32_t*>(P.out.data)[at] = nvfp4_codes8<SRC == kPlain>(v[u], inv);
             if ((unit & 1) == 0) static_cast<uint8_t*>(P.out.scales)[at >> 1] = (uint8_t)e;
@@ -208,9 +212,9 @@ cudaError_t launch_u(RowParams P, cudaStream_t s) {
 template <int SRC, int OUT>
 cudaError_t launch_rows(const RowParams& P, cudaStream_t s) {
     const int units = P.K >> 3;
-    if (units <= kRowThreads) return launch_u<SRC, OUT, 1>(P, s);
-    if (units <= 2 * kRowThreads) return launch_u<SRC, OUT, 2>(P, s);
-    if (units <= 4 * kRowThreads) return launch_u<SRC, OUT, 4>(P, s);
+    if (units <= 32) return launch_u<SRC, OUT, 1>(P, s);
+    if (units <= 64) return launch_u<SRC, OUT, 2>(P, s);
+    if (units <= NVFP4_MAX_ROW_K / 16) return launch_u<SRC, OUT, 4>(P, s);
     return launch_u<SRC, OUT, 8>(P, s);
 }
 
