@@ -70,7 +70,7 @@ __device__ __forceinline__ void mul2(float& a, float& b, float s) {
         " mov.b64 {%0, %1}, v;\n}" : "+f"(a), "+f"(b) : "f"(s));
 }
 
-// Eight values (in row scales) of a block times 1 / its scale -> eight codes, the first in the low four bits. EXACT: the
+// Eight values of a block times 1 / (block scale * row scale) -> eight codes, the first in the low four bits. EXACT: the
 // values are bf16, so that v / e (8 bits by at most 4) is on a rounding point of E2M1 or off it by over 2^-8: p, within
 // 2^-22 of the quotient, goes back on the point when it is rounded to 16 bits.
 template <bool EXACT>

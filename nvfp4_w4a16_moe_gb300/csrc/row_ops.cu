@@ -21,7 +21,7 @@ namespace {
 
 constexpr int kRowThreads = 128;      // of a CTA, or one row's threads where those are more
 
-enum RowSource { kPlain, kNorm, kSwiglu16, kSwiglu32 };
+enum RowSource { kPlain, kNorm, kNormDelta, kSwiglu16, kSwiglu32 };
 
 struct RowParams {
     const void* in;            // x / h / gu
@@ -45,18 +45,32 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// Eight elements from a 16-byte aligned place.
+// Eight elements as they lie in memory (16-byte aligned), or zeros: asked for without a branch, so that many are under way.
 template <bool F32>
-__device__ __forceinline__ void load8(const void* base, size_t at, float (&v)[8]) {
-    if constexpr (F32) {
-        const float* p = static_cast<const float*>(base) + at;
-        const uint4 a = ld_once_v4(p), b = ld_once_v4(p + 4);
-        v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
-        v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
-    } else {
-        unpack8(ld_once_v4(static_cast<const uint16_t*>(base) + at), v);
+struct Raw8 {
+    uint4 a, b;
+
+    __device__ __forceinline__ void ask(const void* base, size_t at, bool there) {
+        const uint8_t* p = static_cast<const uint8_t*>(base) + at * (F32 ? 4 : 2);
+        a = ld_if(p, there);
+        if (F32) b = ld_if(p + 16, there);
     }
-}
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        if constexpr (F32) {
+            v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
+            v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
+        } else {
+            unpack8(a, v);
+        }
+    }
+    static __device__ __forceinline__ uint4 ld_if(const void* p, bool there) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n"
+                     " @p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+                     : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w) : "l"(p), "r"((uint32_t)there));
+        return v;
+    }
+};
 // Largest |v| as fp32 bits: NaN above infinity above every number.
 __device__ __forceinline__ uint32_t absmax8(const float (&v)[8]) {
     float m = 0.f;
@@ -95,51 +109,55 @@ rows_kernel(const RowParams P) {
     const int group = P.group, lane = threadIdx.x % group, units = P.K >> 3;
     const size_t row = (size_t)blockIdx.x * (blockDim.x / group) + threadIdx.x / group;
     const bool here = row < (size_t)P.R;
+    constexpr bool norm = SRC == kNorm || SRC == kNormDelta, two = SRC != kPlain && SRC != kNorm, f32 = SRC == kSwiglu32;
+    Raw8<f32> in[U], in2[two ? U : 1];       // x / h / g, and delta / u
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int unit = lane + u * group;
+        const bool there = here && unit < units;
+        const size_t at = row * P.K + unit * 8, wide = at + row * P.K;
+        in[u].ask(P.in, SRC == kSwiglu16 || f32 ? wide : at, there);
+        if (SRC == kNormDelta) in2[u].ask(P.delta, at, there);
+        if (SRC == kSwiglu16 || f32) in2[u].ask(P.in, wide + P.K, there);
+    }
     float v[U][8];
     float ss = 0.f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int unit = lane + u * group;
+        in[u].get(v[u]);
+        if constexpr (SRC == kNormDelta) {
+            float d[8];
+            in2[u].get(d);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-        if (!here || unit >= units) continue;
-        const size_t at = row * P.K + unit * 8;
-        if constexpr (SRC == kPlain) {
-            load8<false>(P.in, at, v[u]);
-        } else if constexpr (SRC == kNorm) {
-            load8<false>(P.in, at, v[u]);
-            if (P.delta != nullptr) {
-                float d[8];
-                load8<false>(P.delta, at, d);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[u][i] += d[i];
-                const uint4 h = pack8(v[u]);
-                unpack8(h, v[u]);                   // the residual stream is bf16: the norm sees what is stored
-                *reinterpret_cast<uint4*>(P.h_out + at) = h;
-            } else if (P.h_out != nullptr) {
-                *reinterpret_cast<uint4*>(P.h_out + at) = pack8(v[u]);
-            }
+            for (int i = 0; i < 8; ++i) v[u][i] += d[i];
+            in[u].a = pack8(v[u]);
+            unpack8(in[u].a, v[u]);             // the residual stream is bf16: the norm sees what is stored
+        }
+        if constexpr (norm) {
+            if (P.h_out != nullptr && here && unit < units)
+                *reinterpret_cast<uint4*>(P.h_out + row * P.K + unit * 8) = in[u].a;
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss = fmaf(v[u][i], v[u][i], ss);
-        } else {
+        }
+        if constexpr (SRC == kSwiglu16 || f32) {
             float up[8];
-            const size_t g = row * 2 * P.K + unit * 8;
-            load8<SRC == kSwiglu32>(P.in, g, v[u]);
-            load8<SRC == kSwiglu32>(P.in, g + P.K, up);
+            in2[u].get(up);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[u][i] = v[u][i] * fast_rcp(1.0f + __expf(-v[u][i])) * up[i];
         }
     }
-    if constexpr (SRC == kNorm) {
+    if constexpr (norm) {
+        Raw8<false> w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) w[u].a = Raw8<false>::ld_if(P.w + (lane + u * group) * 8, lane + u * group < units);
         const float r = 1.0f / sqrtf(row_sum(ss, group, s_sum) / (float)P.K + P.eps);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int unit = lane + u * group;
-            if (unit >= units) continue;
-            float w[8];
-            unpack8(*reinterpret_cast<const uint4*>(P.w + unit * 8), w);
+            float g[8];
+            w[u].get(g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] = v[u][i] * r * (1.0f + w[i]);
+            for (int i = 0; i < 8; ++i) v[u][i] = v[u][i] * r * (1.0f + g[i]);
         }
     }
     if constexpr (OUT == NVFP4_ROWS_BF16) {
@@ -182,7 +200,16 @@ rows_kernel(const RowParams P) {
         all = row_max(all, group, s_max);
         const float s = row_scale(all);
         const bool finite = all < 0x7F800000u;
-        const float is = finite ? inverse_pow2(s) : 0.f;
+        float is = finite ? inverse_pow2(s) : 0.f;
+        if (is > 0x1p100f) {              // 1 / (e s) would not be a number: bring the row up first, exactly
+            is *= 0x1p-64f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                m[u] = m[u] == 0u ? 0u : __float_as_uint(__uint_as_float(m[u]) * 0x1p64f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[u][i] *= 0x1p64f;
+            }
+        }
         if (here && lane == 0) P.out.row_scales[row] = s;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -191,10 +218,8 @@ rows_kernel(const RowParams P) {
             if (!here || unit >= units) continue;
             float inv;
             const uint32_t e = nvfp4_block_scale<SRC == kPlain>(finite ? __uint_as_float(m[u]) * is : 0.f, &inv);
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) mul2(v[u][i], v[u][i + 1], is);
             const size_t at = row * (P.K >> 3) + unit;
-            static_cast<uint32_t*>(P.out.data)[at] = nvfp4_codes8<SRC == kPlain>(v[u], inv);
+            static_cast<uint32_t*>(P.out.data)[at] = nvfp4_codes8<SRC == kPlain>(v[u], inv * is);
             if ((unit & 1) == 0) static_cast<uint8_t*>(P.out.scales)[at >> 1] = (uint8_t)e;
         }
     }
@@ -209,11 +234,16 @@ cudaError_t launch_u(RowParams P, cudaStream_t s) {
     return launch_pdl(rows_kernel<SRC, OUT, U>, (unsigned)((P.R + per - 1) / per), threads, 0, s, P);
 }
 
+// Up to 1024 columns: a warp a row, no barriers. More: four units a thread, but two where a norm's sum stands between
+// reading and writing (us, two / four units a thread: norm of 65536 x 2048 into bf16 155 / 158, E4M3 149 / 160, NVFP4
+// 150 / 146; SwiGLU 127 / 116, 125 / 128, 134 / 123; quantiser 85 / 72; norm of 7 x 1056 1.6 / 1.8). The rule goes by the
+// columns alone, so that a row's sum does not depend on how many rows there are.
 template <int SRC, int OUT>
 cudaError_t launch_rows(const RowParams& P, cudaStream_t s) {
     const int units = P.K >> 3;
+    constexpr bool norm = SRC == kNorm || SRC == kNormDelta;
     if (units <= 32) return launch_u<SRC, OUT, 1>(P, s);
-    if (units <= 64) return launch_u<SRC, OUT, 2>(P, s);
+    if (units <= (norm ? 2 * kRowThreads : 64)) return launch_u<SRC, OUT, 2>(P, s);
     if (units <= NVFP4_MAX_ROW_K / 16) return launch_u<SRC, OUT, 4>(P, s);
     return launch_u<SRC, OUT, 8>(P, s);
 }
@@ -266,7 +296,7 @@ cudaError_t launch_norm_rows(const uint16_t* h, const uint16_t* delta, const uin
     RowParams P{};
     P.in = h, P.delta = delta, P.w = w, P.h_out = h_out == h ? (delta ? h_out : nullptr) : h_out, P.eps = eps;
     P.R = T, P.K = H, P.out = out;
-    return launch_kind<kNorm>(P, s);
+    return delta != nullptr ? launch_kind<kNormDelta>(P, s) : launch_kind<kNorm>(P, s);
 }
 
 cudaError_t launch_swiglu_rows(const void* gu, bool f32, int R, int I, const nvfp4_rows& out, cudaStream_t s) {
