@@ -216,6 +216,8 @@ nvfp4_status run_nvfp4(Fp4Product P, int32_t y_type, void* workspace, size_t wor
     DeviceInfo dev;
     if (nvfp4_status st = device_info(&dev); st != NVFP4_OK) return st;
     if (r.R == 0) return NVFP4_OK;
+    if (r.R <= kStreamRows && (long long)std::min(r.R, r.E) * r.N * (r.K / 2) <= kStreamBytes4)
+        return from_cuda(launch_fp4_stream(P, dev, static_cast<cudaStream_t>(stream)));
     return from_cuda(launch_rows_fp4(P, static_cast<WsHeader*>(workspace), dev, g_wait_limit.load(),
                                      static_cast<cudaStream_t>(stream)));
 }

@@ -230,7 +230,141 @@ cudaError_t launch_stream(const RowsProduct& P, const DeviceInfo& dev, cudaStrea
     return launch_pdl(rows_stream_kernel<FP8, false>, (unsigned)grid, kSThreads, 0, s, P, n_tiles, k_split);
 }
 
+// ---------------------------------------------------------------- NVFP4
+// Eight E2M1 codes of a word times a block scale (f16, twice) -> four f16x2. A code has 2 significant bits and an E4M3
+// scale 4, and 2^-10 to 2688 are f16's normal range: exact.
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t scale, uint32_t (&v)[4]) {
+    asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+        " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n cvt.rn.f16x2.e2m1x2 %2, c;\n"
+        " cvt.rn.f16x2.e2m1x2 %3, d;\n}" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[i]) : "r"(scale));
+}
+// Two block scales -> each as f16, twice.
+__device__ __forceinline__ uint2 scales_f16(uint32_t two) {
+    uint32_t h;
+    asm("{\n .reg .b16 a;\n cvt.u16.u32 a, %1;\n cvt.rn.f16x2.e4m3x2 %0, a;\n}" : "=r"(h) : "r"(two));
+    return make_uint2(__byte_perm(h, h, 0x1010), __byte_perm(h, h, 0x3232));
+}
+// 16 bytes and the two block scales of 32 codes; zeros where there are none (asked for without a branch).
+struct Unit4 {
+    uint4 v;
+    uint32_t s;
+
+    __device__ __forceinline__ void ask(const uint8_t* codes, const uint8_t* scales, int u, bool there) {
+        v = make_uint4(0, 0, 0, 0), s = 0u;
+        asm volatile("{\n .reg .pred p;\n .reg .b16 h;\n setp.ne.u32 p, %7, 0;\n mov.b16 h, 0;\n"
+                     " @p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%5];\n @p ld.global.u16 h, [%6];\n"
+                     " cvt.u32.u16 %4, h;\n}"
+                     : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w), "=r"(s)
+                     : "l"(codes + (size_t)u * 16), "l"(scales + 2 * u), "r"((uint32_t)there));
+    }
+};
+
+// As rows_stream_kernel: a chunk is 128 bytes of a row, 256 codes with 16 scales; both operands become f16, the products
+// are exact, the sums fp32.
+template <bool AHEAD>
+__global__ void __launch_bounds__(kSThreads, AHEAD ? 2 : 3)
+fp4_stream_kernel(const Fp4Product Q, int n_tiles, int k_split) {
+    __shared__ float s_acc[kSWarps][16][kRows + 1];
+    const RowsProduct& P = Q.r;
+    pdl_wait_then_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int k_part = warp & (k_split - 1), n_part = warp / k_split;
+    const int pass = blockIdx.x / n_tiles;
+    const int n0 = ((blockIdx.x - pass * n_tiles) * (kSWarps / k_split) + n_part) * 16;
+    int e, r0, rows;
+    if (!locate_pass(P, pass, &e, &r0, &rows)) return;
+    const int g = lane >> 2, c = lane & 3;
+    const int units = P.K / 32, chunks = (units + 7) >> 3;
+    const uint8_t *w[2], *ws[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const size_t at = (size_t)e * P.N + min(n0 + g + 8 * i, P.N - 1);
+        w[i] = static_cast<const uint8_t*>(P.w) + at * (P.K / 2);
+        ws[i] = Q.ws + at * (P.K / 16);
+    }
+    Unit4 a[2][2];
+    const auto load_w = [&](int ch, Unit4 (&v)[2][2]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int u = ch * 8 + 4 * h + c;
+                v[h][i].ask(w[i], ws[i], u, n0 + g + 8 * i < P.N && u < units);
+            }
+    };
+    load_w(k_part, a);                             // on its way while the list is read
+    const int row = g < rows ? x_row(P, r0 + g) : -1;
+    const uint8_t* x = static_cast<const uint8_t*>(P.x) + (size_t)max(row, 0) * (P.K / 2);
+    const uint8_t* xs = Q.xs + (size_t)max(row, 0) * (P.K / 16);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int ch = k_part; ch < chunks; ch += k_split) {
+        Unit4 next[2][2], b[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int u = ch * 8 + 4 * h + c;
+            b[h].ask(x, xs, u, row >= 0 && u < units);
+        }
+        if (AHEAD) load_w(ch + k_split, next);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint2 sp = scales_f16(a[h][0].s), sq = scales_f16(a[h][1].s), sx = scales_f16(b[h].s);
+            const uint32_t p[4] = {a[h][0].v.x, a[h][0].v.y, a[h][0].v.z, a[h][0].v.w};
+            const uint32_t q[4] = {a[h][1].v.x, a[h][1].v.y, a[h][1].v.z, a[h][1].v.w};
+            const uint32_t r[4] = {b[h].v.x, b[h].v.y, b[h].v.z, b[h].v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t fp[4], fq[4], fx[4];
+                e2m1x8_f16(p[i], i < 2 ? sp.x : sp.y, fp);
+                e2m1x8_f16(q[i], i < 2 ? sq.x : sq.y, fq);
+                e2m1x8_f16(r[i], i < 2 ? sx.x : sx.y, fx);
+                mma_f16(acc, fp[0], fq[0], fp[1], fq[1], fx[0], fx[1]);
+                mma_f16(acc, fp[2], fq[2], fp[3], fq[3], fx[2], fx[3]);
+            }
+        }
+        if (AHEAD) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) a[h][0] = next[h][0], a[h][1] = next[h][1];
+        } else if (ch + k_split < chunks) {
+            load_w(ch + k_split, a);
+        }
+    }
+    s_acc[warp][g][2 * c] = acc[0];
+    s_acc[warp][g][2 * c + 1] = acc[1];
+    s_acc[warp][g + 8][2 * c] = acc[2];
+    s_acc[warp][g + 8][2 * c + 1] = acc[3];
+    __syncthreads();
+    const int span = kSWarps / k_split * 16, first = (blockIdx.x - pass * n_tiles) * span, part_rows = P.N / Q.parts;
+    for (int i = threadIdx.x; i < span * rows; i += kSThreads) {
+        const int col = i / span, m = i - col * span;
+        if (first + m >= P.N) continue;
+        float v = 0.f;
+        for (int k = 0; k < k_split; ++k) v += s_acc[(m >> 4) * k_split + k][m & 15][col];
+        const int src = x_row(P, r0 + col), dst = y_row(P, r0 + col);
+        if (dst < 0) continue;
+        v *= (src < 0 ? 0.f : Q.xr[src]) * Q.wt[(size_t)e * Q.parts + (first + m) / part_rows];
+        const size_t at = (size_t)dst * P.N + first + m;
+        if (P.y_f32) static_cast<float*>(P.y)[at] = v;
+        else static_cast<uint16_t*>(P.y)[at] = f32_to_bf16(v);
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_fp4_stream(const Fp4Product& Q, const DeviceInfo& dev, cudaStream_t s) {
+    const RowsProduct& P = Q.r;
+    const int chunks = (P.K / 2 + 127) / 128;
+    int k_split = kSWarps;
+    while (k_split > 1 && chunks < 2 * k_split) k_split /= 2;
+    const int span = kSWarps / k_split * 16, n_tiles = (P.N + span - 1) / span;
+    const int groups = std::min(P.R, P.E);
+    const long long grid = ((P.R - groups) / kRows + groups) * (long long)n_tiles;
+    if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+    if (grid <= 2 * dev.num_sms)
+        return launch_pdl(fp4_stream_kernel<true>, (unsigned)grid, kSThreads, 0, s, Q, n_tiles, k_split);
+    return launch_pdl(fp4_stream_kernel<false>, (unsigned)grid, kSThreads, 0, s, Q, n_tiles, k_split);
+}
 
 cudaError_t launch_rows_stream(const RowsProduct& P, const DeviceInfo& dev, cudaStream_t s) {
     return P.xs != nullptr ? launch_stream<true>(P, dev, s) : launch_stream<false>(P, dev, s);
