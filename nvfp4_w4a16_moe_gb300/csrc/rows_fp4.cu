@@ -459,17 +459,30 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                 const int half = lane & 1, sf_l = 16 * w + (lane >> 1);
                 int step = 0, two = 0;
                 bool ok = true;
+                Walk at = tiles;
+                Tile t{};
+                // list entries of this lane's rows, asked for a tile ahead: of x, then of the scales
+                int entry[1 + kSfPer];
+                const int l = 4 * (w + kGatherWarps * (lane >> 2)) + (lane & 3);
+                const auto ask = [&] {
+                    t = at.tile();
+                    const int col = rank * (t.mma_n() / 2) + l;
+                    entry[0] = P.list[t.r0 + min(col, t.n - 1)];
+#pragma unroll
+                    for (int i = 0; i < kSfPer; ++i) entry[1 + i] = P.list[t.r0 + min(64 * i + sf_l, t.n - 1)];
+                };
+                if (at.more()) ask();
 #pragma unroll 1
-                for (Walk at = tiles; at.more() && ok; at.next()) {
-                    const Tile t = at.tile();
-                    const int share = t.mma_n() / 2, copies = share / 4;
-                    const auto row_of = [&](int col) { return col < t.n ? x_row(P, t.r0 + col) : -1; };
-                    const int l = 4 * (w + kGatherWarps * (lane >> 2)) + (lane & 3);
-                    int src = row_of(l < share ? rank * share + l : t.n);
+                while (at.more() && ok) {
+                    const int share = t.mma_n() / 2, copies = share / 4, n = t.n;
+                    const auto row_of = [&](int e, int col) { return col < n && (unsigned)e < (unsigned)P.R ? e / P.k : -1; };
+                    int src = row_of(entry[0], l < share ? rank * share + l : n);
                     if (src < 0) src = P.x_rows;                     // past the last row: zeros
                     int sf_src[kSfPer];
 #pragma unroll
-                    for (int i = 0; i < kSfPer; ++i) sf_src[i] = row_of(64 * i + sf_l);
+                    for (int i = 0; i < kSfPer; ++i) sf_src[i] = row_of(entry[1 + i], 64 * i + sf_l);
+                    at.next();
+                    if (at.more()) ask();
                     const int mine = (copies - w + kGatherWarps - 1) / kGatherWarps;
 #pragma unroll 1
                     for (int s = s_begin; s < s_end; ++s, ++step) {
