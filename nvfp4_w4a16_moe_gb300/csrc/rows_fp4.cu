@@ -484,6 +484,11 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                     at.next();
                     if (at.more()) ask();
                     const int mine = (copies - w + kGatherWarps - 1) / kGatherWarps;
+                    int rows4[kPer][4];
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) rows4[j][i] = __shfl_sync(0xffffffffu, src, 4 * j + i);
 #pragma unroll 1
                     for (int s = s_begin; s < s_end; ++s, ++step) {
                         if (sf_tma && (s == s_begin || (s & 1) == 0)) {
@@ -511,13 +516,9 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
 #pragma unroll
                         for (int j = 0; j < kPer; ++j) {
                             if (j >= mine) break;
-                            const int r0 = __shfl_sync(0xffffffffu, src, 4 * j);
-                            const int r1 = __shfl_sync(0xffffffffu, src, 4 * j + 1);
-                            const int r2 = __shfl_sync(0xffffffffu, src, 4 * j + 2);
-                            const int r3 = __shfl_sync(0xffffffffu, src, 4 * j + 3);
                             if (elect_one())
-                                tma_gather4(b + j * (kGatherWarps * 4 * kStepBytes), &maps.x, s * kStepBytes, r0, r1,
-                                            r2, r3, &full[st]);
+                                tma_gather4(b + j * (kGatherWarps * 4 * kStepBytes), &maps.x, s * kStepBytes,
+                                            rows4[j][0], rows4[j][1], rows4[j][2], rows4[j][3], &full[st]);
                         }
                     }
                 }
