@@ -231,7 +231,7 @@ cudaError_t launch_u(RowParams P, cudaStream_t s) {
     P.group = ((units + U - 1) / U + 31) / 32 * 32;
     const int threads = P.group > kRowThreads ? P.group : kRowThreads / P.group * P.group;
     const int per = threads / P.group;
-    return launch_pdl(rows_kernel<SRC, OUT, U>, (unsigned)((P.R + per - 1) / per), threads, 0, s, P);
+    return launch_pdl(rows_kernel<SRC, OUT, U>, (unsigned)(((long long)P.R + per - 1) / per), threads, 0, s, P);
 }
 
 // Up to 1024 columns: a warp a row, no barriers. More: four units a thread, but two where a norm's sum stands between

@@ -203,3 +203,21 @@ def test_streams_graphs_and_nothing_to_do(nv):
     assert r0.shape == (0, N) and p0.shape == (0,)
     assert nv.moe_combine(none, k).shape == (0, N)
     assert nv.moe_combine_backward(none, none, torch.empty(0, k, device="cuda"))[1].shape == (0, k)
+
+
+def test_rows_past_32_bits(nv):
+    """4.4e9 elements of rows: the last entries are where they should be."""
+    T, k, N = 65536, 8, 8400
+    x = torch.zeros(T, N, dtype=BF16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x[-4:] = torch.randint(-4, 5, (4, N), generator=g, device="cuda").to(BF16)
+    lst = torch.arange(T * k, dtype=torch.int32, device="cuda").roll(5)
+    rows, pos = nv.moe_permute(x, lst, k)
+    assert torch.equal(pos, torch.arange(T * k, dtype=torch.int32, device="cuda").roll(-5))
+    assert torch.equal(rows[:5], x[-1:].expand(5, N)) and torch.equal(rows[-1], x[-1]) and torch.equal(rows[-4], x[-2])
+    w = torch.full((T, k), 0.5, device="cuda")
+    y = nv.moe_combine(rows, k, w, pos)
+    assert torch.equal(y[-4:], x[-4:] * 4) and not y[:-4].any()
+    d_rows, d_w = nv.moe_combine_backward(x, rows, w, pos)
+    assert torch.equal(d_w[-4:], (x[-4:].float() ** 2).sum(1, keepdim=True).expand(4, k))
+    assert torch.equal(d_rows[:5], rows[:5] * 0.5) and torch.equal(d_rows[-8:], rows[-8:] * 0.5)

@@ -367,6 +367,98 @@ def test_empty_and_refusals(nv):
             nv.moe_grouped_gemm_nvfp4(**dict(a, **bad))
 
 
+# ---------------------------------------------------------------- waits
+
+@pytest.mark.parametrize("rows", ["list", "gather", "scatter"])
+@pytest.mark.parametrize("T,N,K", [(2000, 2600, 512), (2000, 2600, 544), (64, 6000, 2048), (128, 513, 4096), (300, 300, 1056)],
+                         ids=["one_pair", "one_pair_odd", "two_pairs", "four_pairs", "odd"])
+def test_a_wait_that_runs_out_is_reported(nv, T, N, K, rows):
+    """A limit of 1 ns is over at the first poll that fails, and the first operands take a round trip to memory: the
+    status and the NaN are always there, and the next call is exact again."""
+    a, xd, wd, off, lst, R = _case(T, 1, 1, N, K, "one", rows, 1, T)
+    want = _want(a, xd, wd, off, lst, R)[0]
+    ws = nv.Workspace(256)
+    for dtype in (F32, BF16):
+        buf = torch.zeros(R * N + 64, dtype=dtype, device="cuda")
+        y = buf[:R * N].view(R, N)
+        try:
+            nv.set_device_wait_limit(1)
+            nv.moe_grouped_gemm_nvfp4(**a, y=y, ws=ws)
+            torch.cuda.synchronize()
+            assert ws.status(clear=True) == nv.NVFP4_ERR_DEVICE_TIMEOUT
+            assert torch.isnan(y).any() and not buf[R * N:].any()
+        finally:
+            nv.set_device_wait_limit(0)
+        nv.moe_grouped_gemm_nvfp4(**a, y=y, ws=ws)
+        assert ws.status() == nv.NVFP4_OK
+        _check_exact(y, want, dtype)
+
+
+@pytest.mark.parametrize("limit", [200, 2000, 20000])
+def test_waits_that_may_run_out(nv, limit):
+    """Limits around what the waits take: the status and the NaN go together, whatever has finished is right, and
+    the next call is exact."""
+    for T, N, K, rows in ((700, 1030, 2048, "gather"), (64, 6000, 2048, "list"), (100, 513, 4096, "scatter")):
+        a, xd, wd, off, lst, R = _case(T, 1, 3, N, K, "skew", rows, 1, T)
+        want = torch.from_numpy(_want(a, xd, wd, off, lst, R)[0]).float().cuda()
+        ws = nv.Workspace(256)
+        y = torch.zeros(R, N, device="cuda")
+        try:
+            nv.set_device_wait_limit(limit)
+            for _ in range(3):
+                nv.moe_grouped_gemm_nvfp4(**a, y=y, ws=ws)
+                torch.cuda.synchronize()
+                code = ws.status(clear=True)
+                bad = y.isnan()
+                assert code == (nv.NVFP4_ERR_DEVICE_TIMEOUT if bad.any() else nv.NVFP4_OK) or code == nv.NVFP4_ERR_DEVICE_TIMEOUT
+                assert torch.equal(y[~bad], want[~bad])
+        finally:
+            nv.set_device_wait_limit(0)
+        nv.moe_grouped_gemm_nvfp4(**a, y=y, ws=ws)
+        assert ws.status() == nv.NVFP4_OK and torch.equal(y, want)
+
+
+_FIRST_IN_CAPTURE = """
+import sys
+sys.path[:0] = [%r, %r]
+import torch
+import nvfp4_w4a16_moe_gb300 as nv
+T, N, K = %d, 300, 2048
+x = torch.ones(T, K, dtype=torch.bfloat16, device="cuda")
+w = torch.zeros(K, dtype=torch.bfloat16, device="cuda")
+W = nv.nvfp4_pack(torch.ones(N, K, device="cuda"))
+gu = torch.ones(T, 2 * K, dtype=torch.bfloat16, device="cuda")
+lst = torch.arange(T, dtype=torch.int32, device="cuda").flip(0).contiguous()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    h, q = nv.rmsnorm_residual(x, w, 0.0, kind=nv.ROWS_NVFP4)
+    y = nv.nvfp4_gemm_w4a4(*q, W)
+    z = nv.nvfp4_gemm_w4a4(*nv.nvfp4_quantize_rows(x), W, out_dtype=torch.float32)
+    s = nv.moe_swiglu(gu)
+    r, p = nv.moe_permute(z, lst, 1)
+    c = nv.moe_combine(r, 1, None, p, out_dtype=torch.float32)
+g.replay()
+torch.cuda.synchronize()
+# W is 6 * 448 * fl(1 / 2688): 1 within its roundings. A row of ones has row scale 2^-11 (the power of two above 1 / 2688),
+# block scale 352 (of 320 and 352 the nearer to 2^11 / 6 = 341.3) and codes 6 (2^11 / 352 = 5.8): 6 * 352 / 2^11 = 33 / 32.
+want = K * 33 / 32
+assert (y.float() - want).abs().max() <= want * 2.0 ** -8 and (z - want).abs().max() <= want * 2.0 ** -20
+assert torch.equal(c, z) and torch.equal(r, z.flip(0))
+"""
+
+
+@pytest.mark.parametrize("T", [4, 300])
+def test_first_calls_of_a_process_inside_a_capture(nv, T):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = _FIRST_IN_CAPTURE % (root, os.path.join(root, "tests"), T)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 # ---------------------------------------------------------------- together
 
 def test_chains_over_reused_buffers(nv):

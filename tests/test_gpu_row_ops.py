@@ -267,3 +267,23 @@ def test_row_ops_outputs_streams_and_graphs(nv):
     assert nv.moe_swiglu(e(0, 64)).shape == (0, 32)
     assert nv.rmsnorm_residual(e(0, 64), e(64))[1].shape == (0, 64)
     assert nv.nvfp4_dequantize_rows(e(0, 32, dtype=torch.uint8), e(0, 4, dtype=torch.uint8), e(0, dtype=torch.float32)).shape == (0, 64)
+
+
+def test_rows_past_32_bits(nv):
+    """2.3e9 elements: the last rows are where they should be."""
+    R, K = 70001, 32768
+    x = torch.zeros(R, K, dtype=BF16, device="cuda")
+    tail = torch.randn(3, K, generator=_gen(1)).to(BF16).cuda()
+    x[-3:] = tail
+    packed, scales, rs = nv.nvfp4_quantize_rows(x)
+    for a, b in zip((packed, scales, rs), nv.nvfp4_quantize_rows(tail)):
+        assert torch.equal(a[-3:], b) and not a[1000].any() or a.dtype == torch.float32
+    back = nv.nvfp4_dequantize_rows(packed, scales, rs)
+    assert torch.equal(back[-3:], nv.nvfp4_dequantize_rows(*nv.nvfp4_quantize_rows(tail)))
+    del back, packed, scales
+    w = torch.zeros(K, dtype=BF16, device="cuda")
+    _, (q, s) = nv.rmsnorm_residual(x, w, kind=nv.ROWS_FP8)
+    _, (qt, st) = nv.rmsnorm_residual(tail, w, kind=nv.ROWS_FP8)
+    assert torch.equal(q[-3:].view(torch.uint8), qt.view(torch.uint8)) and torch.equal(s[-3:], st)
+    del q, s
+    assert torch.equal(nv.moe_swiglu(x)[-3:], nv.moe_swiglu(tail))
