@@ -87,6 +87,27 @@ struct Waiter {
         }
         return true;
     }
+    // The same by one thread alone.
+    __device__ __forceinline__ bool one(uint64_t* bar, uint32_t parity) const {
+        if (mbar_test_wait(bar, parity)) return true;
+        const bool brief = limit_ns < kShortLimitNs;
+        if (!brief) {
+#pragma unroll 1
+            for (int i = 0; i < 64; ++i)
+                if (mbar_try_wait(bar, parity)) return true;
+        }
+        const unsigned long long t0 = global_timer_ns();
+        while (!(brief ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) {
+            const bool late = global_timer_ns() - t0 > limit_ns;
+            if (late) {
+                *abort_flag = 1;
+                asm volatile("st.volatile.shared::cluster.u32 [%0], %1;" :: "r"(peer_flag), "r"(1) : "memory");
+                if (hdr != nullptr) record_status(hdr, NVFP4_ERR_DEVICE_TIMEOUT);
+            }
+            if (late || *abort_flag) return false;
+        }
+        return true;
+    }
 };
 
 // One lane of the (converged) warp. The tensor-core and TMA instructions take uniform registers: under

@@ -36,6 +36,7 @@ constexpr int kMmas = kStepK / 64;       // MMAs of a step
 constexpr int kSectorBytes = 32;         // block scales of a row in two steps
 constexpr int kBlkBytes = kM * kSectorBytes; // block scales of 128 rows in two steps
 constexpr int kMaxStages = 9;
+constexpr int kWidths = 16;
 constexpr int kMinSteps = 2;             // steps of each pair that shares a tile's K, at least
 
 // Warps: 16 of epilogue, TMA, MMA, four of gather, one that looks up the tiles' ends, one for every 128 rows of scales.
@@ -66,10 +67,11 @@ struct Cfg {
     static constexpr int kOffEnds = kOffStg + kEpiWarps * kStgRows * kStgPitch;
     static constexpr int kOffBars = kOffEnds + kEnds * kEndsBytes;
     static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 3 * kSlots + 2 * kEnds + 1;
-    static constexpr int kOffTab = kOffBars + kNumBars * 8 + 16; // tile prefix [E + 1], first position [E], rows [E]
+    static constexpr int kOffWidths = kOffBars + kNumBars * 8 + 16;  // MMA columns of the latest tiles [kWidths]
+    static constexpr int kOffTab = kOffWidths + kWidths * 4;     // tile prefix [E + 1], first position [E], rows [E]
     static constexpr int kSmem = 1024 + kOffTab + (3 * NVFP4_MAX_EXPERTS + 1) * 4;
     static_assert(NT % kRound == 0 && NT <= 256 && kStage % 1024 == 0 && NT / 2 % kBoxRows == 0, "swizzle atoms, copies");
-    static_assert(kSmem <= 227 * 1024, "shared memory");
+    static_assert(kSmem <= 227 * 1024 && kStages < kWidths, "shared memory");
     static_assert(4 * NT / 16 * 2048 <= kOffStg, "exchanged sums fit in the ring");
     static_assert(kSf + kSfSets * kSfCols <= 512, "tensor memory");
 };
@@ -291,6 +293,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* tab = reinterpret_cast<int*>(sm + C::kOffTab);
+    volatile int* widths = reinterpret_cast<volatile int*>(sm + C::kOffWidths);
 
     if (warp == kMmaWarp) {
         if (lane == 0) {
@@ -339,6 +342,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
     using Walk = WalkOf<C::kRound>;
     using Tile = TileOf<C::kRound>;
     const Walk tiles(tab, P.E, m_tiles, blockIdx.x / kCluster, gridDim.x / kCluster, total);
+    const int tiles_here = tiles.more() ? (total - 1 - tiles.i) / tiles.step + 1 : 0;
     const Waiter wait{abort_flag, map_rank(su32(const_cast<int*>(abort_flag)), (uint32_t)crank ^ 1u), hdr, wait_limit};
 
     // one tile at most to a cluster of several pairs
@@ -358,10 +362,10 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
 
     if (warp >= kEpiWarps) {
         if (warp == kTmaWarp) {
-            int step = 0, two = 0;                                              // steps and pairs of steps so far
+            int step = 0, two = 0, i_tile = 0;                                  // steps, pairs of steps and tiles so far
             bool ok = true;
 #pragma unroll 1
-            for (Walk at = tiles; at.more() && ok; at.next()) {
+            for (Walk at = tiles; at.more() && ok; at.next(), ++i_tile) {
                 const Tile t = at.tile();
                 const int share = t.mma_n() / 2;                                // rows of x here
                 const int wy = t.e * P.N + t.m0 + rank * kM;
@@ -386,6 +390,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                     if (!ok) break;
                     const uint32_t a = sm_base + st * C::kStage, b = a + kABytes;
                     if (elect_one()) {
+                        if (s == s_begin) widths[i_tile % kWidths] = 2 * share;  // for the MMA thread, with the arrival
                         mbar_arrive_expect_tx(&full[st], bytes);
                         tma_load_2d(a, &maps.w, s * kStepBytes, wy, &full[st]);
                         for (int i = 0; i < boxes; ++i)
@@ -399,38 +404,42 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                 drain_scales(two);
             }
         } else if (warp == kMmaWarp) {
-            int st = 0, buf = 0, sl = 0;
-            uint32_t st_par = 0, sl_par = 0, buf_par = 1;          // an unused buffer's "empty" phase counts as over
-            bool ok = true;
-            const uint64_t stage0 = sw128_desc(sm_base), scales0 = lines_desc(sm_base + C::kOffSlots);
+            // One thread: in a loop of the whole warp with votes at every wait the waits that did not have to wait took as
+            // long as a third of the MMAs.
+            if (elect_one()) {
+                int st = 0, buf = 0, sl = 0;
+                uint32_t st_par = 0, sl_par = 0, buf_par = 1;      // an unused buffer's "empty" phase counts as over
+                bool ok = true;
+                const uint64_t stage0 = sw128_desc(sm_base), scales0 = lines_desc(sm_base + C::kOffSlots);
 #pragma unroll 1
-            for (Walk at = tiles; at.more() && ok; at.next()) {
-                const int N = at.tile().mma_n();
-                const uint32_t idesc = nvfp4_idesc(N);
+                for (int i = 0; i < tiles_here && ok; ++i) {
+                    uint32_t idesc = 0;
 #pragma unroll 1
-                for (int s = s_begin; s < s_end; ++s) {
-                    if (s == s_begin || (s & 1) == 0) ok = wait(&sf_ready[sl], sl_par);
-                    if (ok) ok = wait(&full[st], st_par);
-                    if (!ok) break;
-                    const bool sl_done = (s & 1) != 0 || s == s_end - 1;
-                    if (rank != 0) {
-                        if (elect_one()) arrive_cluster(map_rank(su32(&full[st]), first_rank));
-                    } else {
-                        if (s == s_begin) ok = wait(&acc_empty[buf], buf_par);
+                    for (int s = s_begin; s < s_end; ++s) {
+                        if (s == s_begin || (s & 1) == 0) ok = wait.one(&sf_ready[sl], sl_par);
+                        if (ok) ok = wait.one(&full[st], st_par);
                         if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t a = stage0 + st * (C::kStage / 16), b = a + kABytes / 16;
-                        const uint64_t sf = scales0 + (sl * C::kSlotBytes + (s & 1) * (kBlkBytes / 2)) / 16;
-                        const uint32_t tsf = tmem + C::kSf + (C::kSfSets > 1 ? (s & 1) * C::kSfCols : 0);
-                        if (elect_one()) {
+                        const bool sl_done = (s & 1) != 0 || s == s_end - 1;
+                        if (rank != 0) {
+                            arrive_cluster(map_rank(su32(&full[st]), first_rank));
+                        } else {
+                            if (s == s_begin) {
+                                ok = wait.one(&acc_empty[buf], buf_par);
+                                idesc = nvfp4_idesc(widths[i % kWidths]);
+                            }
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t a = stage0 + st * (C::kStage / 16), b = a + kABytes / 16;
+                            const uint64_t sf = scales0 + (sl * C::kSlotBytes + (s & 1) * (kBlkBytes / 2)) / 16;
+                            const uint32_t tsf = tmem + C::kSf + (C::kSfSets > 1 ? (s & 1) * C::kSfCols : 0);
                             // columns: 4 for each MMA's scales of W, then 4 kXBlocks for each MMA's of x
 #pragma unroll
                             for (int j = 0; j < kMmas; ++j) {
                                 copy_scales(tsf + 4 * j, sf + j * (512 / 16));
 #pragma unroll
-                                for (int i = 0; i < C::kXBlocks; ++i)
-                                    copy_scales(tsf + 4 * kMmas + 4 * (C::kXBlocks * j + i),
-                                                sf + ((1 + i) * kBlkBytes + j * 512) / 16);
+                                for (int k = 0; k < C::kXBlocks; ++k)
+                                    copy_scales(tsf + 4 * kMmas + 4 * (C::kXBlocks * j + k),
+                                                sf + ((1 + k) * kBlkBytes + j * 512) / 16);
                             }
 #pragma unroll
                             for (int j = 0; j < kMmas; ++j)      // 32 bytes of K an MMA: 2 address units
@@ -438,19 +447,20 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                                           tsf + 4 * kMmas + 4 * C::kXBlocks * j, s != s_begin || j != 0);
                             commit_pair(&empty[st], pair_mask);
                             if (sl_done) commit_pair(&sf_empty[sl], pair_mask);
-                            if (s == s_end - 1) commit_pair(&acc_full[buf], pair_mask);
+                            if (s == s_end - 1) {
+                                commit_pair(&acc_full[buf], pair_mask);
+                                if (++buf == C::kBufs) buf = 0, buf_par ^= 1;
+                            }
                         }
-                        if (s == s_end - 1 && ++buf == C::kBufs) buf = 0, buf_par ^= 1;
+                        if (++st == C::kStages) st = 0, st_par ^= 1;
+                        if (sl_done && ++sl == C::kSlots) sl = 0, sl_par ^= 1;
                     }
-                    if (++st == C::kStages) st = 0, st_par ^= 1;
-                    if (sl_done && ++sl == C::kSlots) sl = 0, sl_par ^= 1;
                 }
-            }
-            // no MMA still reads or writes either CTA's memory, nor has an arrival on the way to it, when it is freed
-            if (elect_one()) {
+                // no MMA still reads or writes either CTA's memory, nor has an arrival on the way to it, when it is freed
                 if (rank == 0) commit_pair(done, pair_mask);
                 drain_wait(done, 0);
             }
+            __syncwarp();
         } else if (warp == kEndsWarp) {
             ends_warp<C>(Q, tiles, rank, sm + C::kOffEnds, ends_full, ends_empty, wait);
         } else if (warp < kEndsWarp) {
@@ -550,7 +560,6 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
         uint8_t* stg = sm + C::kOffStg + warp * (kStgRows * kStgPitch);
         const int p = lane & 3, g = lane >> 2;
         const uint32_t first_acc_empty = map_rank(su32(acc_empty), first_rank);
-        const int tiles_here = tiles.more() ? (total - 1 - tiles.i) / tiles.step + 1 : 0;
         int end = 0;
         uint32_t end_par = 0;
         bool ok = true;
