@@ -5,22 +5,33 @@
 // memory, and keeps the running sum in fp32: the block scales cost no arithmetic outside the tensor cores, and the
 // epilogue multiplies by the two fp32 scales once.
 //
-// Tiles, pairs of CTAs, warp roles, the walk over the experts and the exchange between pairs that share a tile's K are
-// those of rows_tc.cu (pair_tc.cuh). What differs:
+// Tiles, pairs of CTAs, the walk over the experts and the exchange between pairs that share a tile's K are those of
+// rows_tc.cu (pair_tc.cuh). What differs:
 //   A step is 128 bytes of a row as there, 256 elements: four MMAs of 64 columns, each with 4 scales a row.
-//   Scale warps bring the step's 16 block scales of every row. Both operands store them row by row, [rows, K/16],
-//     while the tensor cores want, for every 64 columns, 32 lines of 16 bytes: line l holds the four scales of rows l,
-//     32 + l, 64 + l and 96 + l. A lane loads the 16 bytes of those four rows, which are then lines l of the step's
-//     four MMAs when read across: a transposition of registers, four 16-byte loads and stores for 2 KB of scales, no
-//     second copy of the weights' scales in another order. Behind the end of K and for rows that the tile does not have
-//     the scales are 0, so neither a neighbour's NaN scale nor its codes count.
-//   The MMA warp copies a step's scales from the ring to tensor memory (tcgen05.cp, to all four lane quarters), right
+//   Block scales. Both operands store them row by row, [rows, K/16], while the tensor cores want, for every 64 columns, 32
+//     lines of 16 bytes: line l holds the four scales of rows l, 32 + l, 64 + l and 96 + l. Copies bring 32 bytes of every
+//     row, the scales of two steps, and a warp for every 128 rows puts them into line order in place: a lane holds the
+//     words of its four rows, which are lines l of the eight MMAs when read across. No second copy of the weights' scales
+//     in another order is needed. Rows whose scales are no multiple of 16 bytes
+//     (K is none of 256) are no strides of a tensor map; two, four or eight of them together are (OddCopies): 48 bytes of
+//     each, out of which the same warp takes its 32. (That warp loading them from global memory: 4096 x 8192 x 2016 in 76
+//     us, rows gathered for 256 experts in 190; now 52 and 101.) Behind the end of K the scales are 0, so neither the codes
+//     nor NaN scales that lie there count.
+//   The MMA thread copies a step's scales from the ring to tensor memory (tcgen05.cp, to all four lane quarters), right
 //     before the step's MMAs: the tensor pipe runs copies and MMAs of one thread in the order of issue.
 //   Tensor memory holds two sums and the scales of a step: 512 columns take tiles of up to 224 columns. (Tiles of 256
 //     whose buffers shared 48 columns, which the epilogue read first, left 1.1 us of every tile without MMAs.)
+//   A warp looks up a tile ahead what the epilogue needs of its rows (scales, places of y), so that no epilogue warp waits
+//     for a list entry. The epilogue writes past L1.
+//
+// What bounds it: with many rows the operands on their way into shared memory, 30 KB a step and SM at some 64 bytes a
+// clock (0.29 us for 224 columns, 6 PFLOP/s: 4096 x 8192 x 8192 in 90 us), and below K = 1024 the outputs, which memory
+// takes at 4.5 TB/s (4096 x 8192 x 512: 22 us, of which a fill of y takes 17). 4096 x 8192 x 2048 takes 33.4 us, 4.1
+// PFLOP/s. With few rows to many experts the weights from memory (64 tokens to eight of 256 experts of 1024 x 2048 each:
+// 38 us for the 200 MB of some 170 experts), with few rows of one matrix the start of a launch: some 4.5 us pass before and after the steps.
 #include <atomic>
+#include <cmath>
 #include <cstring>
-#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.cuh"
@@ -34,16 +45,18 @@ constexpr int kABytes = kM * kStepBytes;
 constexpr int kStepK = 2 * kStepBytes;   // elements of a step
 constexpr int kMmas = kStepK / 64;       // MMAs of a step
 constexpr int kSectorBytes = 32;         // block scales of a row in two steps
-constexpr int kBlkBytes = kM * kSectorBytes; // block scales of 128 rows in two steps
+constexpr int kOddBytes = 48;            // ... with the 16-byte pieces that they lie in, where rows are no multiple of 16 bytes
+constexpr int kRing = 192 * 1024;        // operands and scales
 constexpr int kMaxStages = 9;
 constexpr int kWidths = 16;
 constexpr int kMinSteps = 2;             // steps of each pair that shares a tile's K, at least
 
-// Warps: 16 of epilogue, TMA, MMA, four of gather, one that looks up the tiles' ends, one for every 128 rows of scales.
+// Warps: 16 of epilogue, TMA, MMA, four of gather (which bring OddCopies where no rows are gathered), one that looks up the tiles' ends, one for every 128 rows of scales.
 constexpr int kEpiWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kGatherWarp0 = 18, kGatherWarps = 4, kEndsWarp = 22;
 constexpr int kScaleWarp0 = 23;
 
-template <int NT>
+// ODD: a row's scales are no multiple of 16 bytes (K is none of 256).
+template <int NT, bool ODD>
 struct Cfg {
     static constexpr int kNT = NT;
     static constexpr int kRound = NT > 128 ? 32 : kNRound;       // a tile's columns are a multiple of this
@@ -51,9 +64,11 @@ struct Cfg {
     static constexpr int kThreads = 32 * (kScaleWarp0 + kBlocks);
     static constexpr int kBoxRows = NT > 128 ? 56 : 32;          // rows of x of a copy
     static constexpr int kStage = kABytes + NT / 2 * kStepBytes;
-    static constexpr int kStages = std::min(kMaxStages, (160 * 1024) / kStage);
     // ring of block scales of two steps: W's 128 rows, then x's NT
-    static constexpr int kSlotBytes = kBlocks * kBlkBytes, kSlots = NT > 128 ? 3 : 4;
+    static constexpr int kXRows = std::min(NT, 128);             // rows of x whose scales come together
+    static constexpr int kRowBytes = ODD ? kOddBytes : kSectorBytes, kBlkBytes = kM * kRowBytes;
+    static constexpr int kSlotBytes = kBlocks * kBlkBytes, kSlots = NT > 128 && !ODD ? 3 : 4;
+    static constexpr int kStages = std::min(kMaxStages, (kRing - kSlots * kSlotBytes) / kStage);
     static constexpr int kOffSlots = kStages * kStage;
     // tensor memory: buffers of NT columns, then the scales of a step (two sets of them where there is room)
     static constexpr int kSfCols = 4 * kMmas * kBlocks;
@@ -78,8 +93,7 @@ struct Cfg {
 
 struct Fp4Maps {
     CUtensorMap w, x;      // x: boxes of kBoxRows rows, or of one to gather
-    CUtensorMap ws, xs;    // block scales, 32 bytes of a row: 128 rows, NT (or one to gather); unused where a row's
-                           // scales are no multiple of 16 bytes
+    CUtensorMap ws, xs;    // block scales of two steps (encode_scales, encode_odd_scales); xs is not read to gather
 };
 
 // D (256 x N over both CTAs) = A B^T of 64 columns, scaled by 4 E4M3 scales a row, plus D where accumulate.
@@ -103,86 +117,139 @@ __device__ __forceinline__ uint32_t nvfp4_idesc(int N) {
     return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(2 * kM >> 7) << 27);
 }
 
-// Block scales of step s of a row of KB, a number that is no multiple of 16: loads of UNIT (2 or 4) bytes. Behind the end
-// of the row: 0.
-template <int UNIT>
-__device__ __forceinline__ void load_row(const uint8_t* row, int s, int KB, uint32_t (&w)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int at = 16 * s + 4 * i;
-        if constexpr (UNIT == 4) {
-            w[i] = *reinterpret_cast<const uint32_t*>(row + min(at, KB - 4));
-        } else {
-            const uint32_t lo = *reinterpret_cast<const uint16_t*>(row + min(at, KB - 2));
-            w[i] = lo | (at + 2 < KB ? (uint32_t)*reinterpret_cast<const uint16_t*>(row + at + 2) << 16 : 0u);
-        }
-        if (at >= KB) w[i] = 0u;
-    }
-}
-
-// A warp that puts the scales of 128 rows (blk 0: of W, then of x) of two steps after two steps into line order: in place,
-// from the sectors that copies brought, row after row, or (UNIT 2, 4) from global memory.
-template <typename C, int UNIT>
-__device__ __forceinline__ void scale_warp(const Fp4Product& Q, WalkOf<C::kRound> at, int pairs, int m_begin, int blk,
-                                           int rank, uint8_t* slots, uint64_t* raw, uint64_t* ready, uint64_t* empty,
+// A warp that puts the scales of 128 rows (blk 0: of W, then of x) of two steps after two steps into line order, in place,
+// from the sectors that copies brought, row after row.
+template <typename C>
+__device__ __forceinline__ void scale_warp(int count, int blk, uint8_t* slots, uint64_t* raw, uint64_t* ready,
                                            const Waiter& wait) {
-    const RowsProduct& P = Q.r;
-    const int lane = threadIdx.x & 31, KB = P.K / 16;
+    const int lane = threadIdx.x & 31;
     int slot = 0;
     uint32_t par = 0;
 #pragma unroll 1
-    for (; at.more(); at.next()) {
-        int row[4];                          // UNIT 2, 4: this lane's rows, or -1
-        if constexpr (UNIT < 16) {
-            const auto t = at.tile();
+    for (int j = 0; j < count; ++j) {
+        uint8_t* blkp = slots + slot * C::kSlotBytes + blk * C::kBlkBytes;
+        uint4* to = reinterpret_cast<uint4*>(blkp) + lane;
+        if (!wait(&raw[slot], par)) return;
+        uint32_t w[4][8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (blk == 0) {
-                    const int n = t.m0 + rank * kM + 32 * i + lane;
-                    row[i] = n < P.N ? t.e * P.N + n : -1;
-                } else {
-                    const int col = (blk - 1) * 128 + 32 * i + lane;
-                    row[i] = col < t.n ? x_row(P, t.r0 + col) : -1;
-                }
-            }
+        for (int i = 0; i < 4; ++i) {
+            // the halves of rows 4 .. 7 of every eight have changed places (32-byte swizzle): no bank is read twice
+            const uint8_t* p = blkp + (32 * i + lane) * kSectorBytes;
+            const int odd = (lane >> 2) & 1;
+            const uint4 a = *reinterpret_cast<const uint4*>(p + 16 * odd);
+            const uint4 b = *reinterpret_cast<const uint4*>(p + 16 * (odd ^ 1));
+            w[i][0] = a.x, w[i][1] = a.y, w[i][2] = a.z, w[i][3] = a.w;
+            w[i][4] = b.x, w[i][5] = b.y, w[i][6] = b.z, w[i][7] = b.w;
         }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) to[32 * k] = make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (elect_one()) mbar_arrive(&ready[slot]);
+        if (++slot == C::kSlots) slot = 0, par ^= 1u;
+    }
+}
+
+// Rows of KB scales, a multiple of 2 but not of 16, are no strides of a tensor map; 2^lg(KB) rows together are. One copy then
+// brings every 2^lg-th row: of each the three 16-byte pieces that 32 bytes may lie in, from byte (row KB) mod 16 on. Row l
+// of the 128 is row l >> lg of copy l mod 2^lg.
+__host__ __device__ __forceinline__ int strided_lg(int KB) { return KB & 2 ? 3 : KB & 4 ? 2 : 1; }
+__device__ __forceinline__ int odd_place(int l, int lg) { return (((l & ((1 << lg) - 1)) << (7 - lg)) + (l >> lg)) * kOddBytes; }
+
+struct OddCopies {
+    int lg, x[8], y[8];
+    __device__ __forceinline__ void rows(int first, int KB) {
+        lg = strided_lg(KB);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x[c] = ((first + c) & ((1 << lg) - 1)) * KB & ~15, y[c] = (first + c) >> lg;
+    }
+    __device__ __forceinline__ void bring(uint32_t to, const CUtensorMap* map, int byte, uint64_t* bar) const {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c < 1 << lg) tma_load_2d(to + c * ((kM >> lg) * kOddBytes), map, x[c] + byte, y[c], bar);
+    }
+};
+
+// The same for rows of KB scales that OddCopies, or the gather warps in their order, brought. The array's last rows, where they
+// make no 2^lg, lie behind the map's end (zeros): the warp loads them itself.
+template <typename C>
+__device__ __forceinline__ void odd_scale_warp(const Fp4Product& Q, WalkOf<C::kRound> at, int pairs, int m_begin, int blk,
+                                               int rank, uint8_t* slots, uint64_t* raw, uint64_t* ready, const Waiter& wait) {
+    const RowsProduct& P = Q.r;
+    const int lane = threadIdx.x & 31, KB = P.K / 16, l0 = (blk - 1) * 128;
+    const uint8_t* base = blk == 0 ? Q.ws : Q.xs;
+    const int lg = strided_lg(KB), rows = blk == 0 ? P.E * P.N : P.x_rows, whole = rows >> lg ? rows >> lg << lg : rows;
+    const bool listed = blk != 0 && P.gather;
+    TileOf<C::kRound> t{};
+    int entry[4] = {};
+    const auto ask = [&] {
+        t = at.tile();
+        if (!listed) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) entry[i] = P.list[t.r0 + min(l0 + 32 * i + lane, t.n - 1)];
+    };
+    if (at.more()) ask();
+    int slot = 0;
+    uint32_t par = 0;
+#pragma unroll 1
+    while (at.more()) {
+        const int first = blk == 0 ? t.e * P.N + t.m0 + rank * kM : t.r0 + l0;
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = !listed ? first + 32 * i + lane : (unsigned)entry[i] < (unsigned)P.R ? entry[i] / P.k : 0;
+            o[i] = (uint32_t)row * KB & 15u;
+        }
+        // rows the copies leave out, four lanes each
+        const int spare0 = max(first, whole), spares = listed ? 0 : min(rows, first + 128) - spare0, spare = spare0 + (lane >> 2);
+        at.next();
+        if (at.more()) ask();
 #pragma unroll 1
         for (int j = 0; j < pairs; ++j) {
-            uint8_t* blkp = slots + slot * C::kSlotBytes + blk * kBlkBytes;
-            uint4* to = reinterpret_cast<uint4*>(blkp) + lane;
-            if constexpr (UNIT < 16) {
-                const uint8_t* base = blk == 0 ? Q.ws : Q.xs;
-                if (!wait(&empty[slot], par ^ 1u)) return;
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t w[4][4];
+            const int byte = kSectorBytes * (m_begin + j);
+            uint8_t* blkp = slots + slot * C::kSlotBytes + blk * C::kBlkBytes;
+            uint16_t late[4];
+            if (spares > 0) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        load_row<UNIT>(base + (size_t)max(row[i], 0) * KB, 2 * (m_begin + j) + h, KB, w[i]);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (row[i] < 0) w[i][k] = 0u;
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) to[128 * h + 32 * k] = make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
+                for (int k = 0; k < 4; ++k) {
+                    const int b = byte + 8 * (lane & 3) + 2 * k;
+                    late[k] = *reinterpret_cast<const uint16_t*>(base + (size_t)min(spare, rows - 1) * KB + min(b, KB - 2));
                 }
-            } else {
-                if (!wait(&raw[slot], par)) return;
-                uint32_t w[4][8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // the halves of rows 4 .. 7 of every eight have changed places (32-byte swizzle): no bank is read twice
-                    const uint8_t* p = blkp + (32 * i + lane) * kSectorBytes;
-                    const int odd = (lane >> 2) & 1;
-                    const uint4 a = *reinterpret_cast<const uint4*>(p + 16 * odd);
-                    const uint4 b = *reinterpret_cast<const uint4*>(p + 16 * (odd ^ 1));
-                    w[i][0] = a.x, w[i][1] = a.y, w[i][2] = a.z, w[i][3] = a.w;
-                    w[i][4] = b.x, w[i][5] = b.y, w[i][6] = b.z, w[i][7] = b.w;
-                }
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < 8; ++k) to[32 * k] = make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
             }
+            if (!wait(&raw[slot], par)) return;
+            if (spares > 0) {
+                const int l = spare - first;
+                uint8_t* p = blkp + odd_place(l, lg) + (spare * KB & 15) + 8 * (lane & 3);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (lane >> 2 < spares) *reinterpret_cast<uint16_t*>(p + 2 * k) = late[k];
+                __syncwarp();
+            }
+            uint32_t w[4][8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t* p = reinterpret_cast<const uint32_t*>(
+                    blkp + odd_place(32 * i + lane, lg) + (o[i] & 12u));
+                uint32_t r[9];
+#pragma unroll
+                for (int k = 0; k < 9; ++k) r[k] = p[k];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) w[i][k] = __funnelshift_r(r[k], r[k + 1], 8 * (o[i] & 2u));
+            }
+            if (KB < byte + kSectorBytes) {            // the row ends in these steps
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int left = KB - (byte + 4 * k);
+                    const uint32_t keep = left >= 4 ? 0xFFFFFFFFu : left > 0 ? 0xFFFFu : 0u;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i][k] &= keep;
+                }
+            }
+            __syncwarp();
+            uint4* to = reinterpret_cast<uint4*>(blkp) + lane;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) to[32 * k] = make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
             fence_proxy_async_smem();
             __syncwarp();
             if (elect_one()) mbar_arrive(&ready[slot]);
@@ -265,11 +332,11 @@ __device__ __forceinline__ void scale2(float& a, float& b, const float2 s, float
 }
 
 // SPLITS: pairs of a cluster, which share a tile's K.
-template <int NT, int SPLITS>
-__global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(Cfg<NT>::kThreads, 1)
+template <int NT, bool ODD, int SPLITS>
+__global__ void __cluster_dims__(2 * SPLITS, 1, 1) __launch_bounds__(Cfg<NT, ODD>::kThreads, 1)
 rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_tiles, int max_tiles, WsHeader* hdr,
                 unsigned long long wait_limit) {
-    using C = Cfg<NT>;
+    using C = Cfg<NT, ODD>;
     const RowsProduct& P = Q.r;
     extern __shared__ uint8_t fp4_smem_raw[];
     // the swizzle pattern follows shared-memory address bits: align the base to 1024 (both CTAs of a
@@ -307,7 +374,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                 mbar_init(&acc_empty[i], 2 * kEpiWarps);
             }
             for (int i = 0; i < C::kSlots; ++i) {
-                mbar_init(&sf_raw[i], 1 + (P.gather ? 32 * kGatherWarps : 0));
+                mbar_init(&sf_raw[i], P.gather ? 1 + 32 * kGatherWarps : ODD ? C::kBlocks : 1);
                 mbar_init(&sf_ready[i], C::kBlocks);
                 mbar_init(&sf_empty[i], 1);
             }
@@ -338,7 +405,6 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
     const int s_begin = nk * pair / SPLITS, s_end = nk * (pair + 1) / SPLITS;      // this pair's steps
     // scales come for steps 2 m and 2 m + 1 together, by TMA where their rows can be strides of a tensor map
     const int m_begin = s_begin >> 1, m_pairs = ((s_end - 1) >> 1) - m_begin + 1, KB = P.K / 16;
-    const bool sf_tma = KB % 16 == 0;
     using Walk = WalkOf<C::kRound>;
     using Tile = TileOf<C::kRound>;
     const Walk tiles(tab, P.E, m_tiles, blockIdx.x / kCluster, gridDim.x / kCluster, total);
@@ -371,17 +437,24 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                 const int wy = t.e * P.N + t.m0 + rank * kM;
                 const int boxes = P.gather ? 0 : (share + C::kBoxRows - 1) / C::kBoxRows;
                 const uint32_t bytes = kABytes + boxes * (C::kBoxRows * kStepBytes);
+                OddCopies odd;
+                if constexpr (ODD) odd.rows(wy, KB);
 #pragma unroll 1
                 for (int s = s_begin; s < s_end; ++s, ++step) {
-                    if (sf_tma && (s == s_begin || (s & 1) == 0)) {
+                    if ((!ODD || P.gather) && (s == s_begin || (s & 1) == 0)) {
                         const int sl = two % C::kSlots, u = two / C::kSlots;
                         if (u > 0) ok = wait(&sf_empty[sl], (u - 1) & 1);
                         if (!ok) break;
                         const uint32_t to = sm_base + C::kOffSlots + sl * C::kSlotBytes;
-                        if (elect_one()) {
-                            mbar_arrive_expect_tx(&sf_raw[sl], kBlkBytes + (P.gather ? 0 : NT * kSectorBytes));
+                        if constexpr (ODD) {
+                            if (elect_one()) {
+                                mbar_arrive_expect_tx(&sf_raw[sl], kM * kOddBytes);
+                                odd.bring(to, &maps.ws, (s >> 1) * kSectorBytes, &sf_raw[sl]);
+                            }
+                        } else if (elect_one()) {
+                            mbar_arrive_expect_tx(&sf_raw[sl], C::kBlkBytes + (P.gather ? 0 : NT * kSectorBytes));
                             tma_load_2d(to, &maps.ws, (s >> 1) * kSectorBytes, wy, &sf_raw[sl]);
-                            if (!P.gather) tma_load_2d(to + kBlkBytes, &maps.xs, (s >> 1) * kSectorBytes, t.r0, &sf_raw[sl]);
+                            if (!P.gather) tma_load_2d(to + C::kBlkBytes, &maps.xs, (s >> 1) * kSectorBytes, t.r0, &sf_raw[sl]);
                         }
                         ++two;
                     }
@@ -430,7 +503,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                             if (!ok) break;
                             tc_fence_after();
                             const uint64_t a = stage0 + st * (C::kStage / 16), b = a + kABytes / 16;
-                            const uint64_t sf = scales0 + (sl * C::kSlotBytes + (s & 1) * (kBlkBytes / 2)) / 16;
+                            const uint64_t sf = scales0 + (sl * C::kSlotBytes + (s & 1) * (16 * kM)) / 16;
                             const uint32_t tsf = tmem + C::kSf + (C::kSfSets > 1 ? (s & 1) * C::kSfCols : 0);
                             // columns: 4 for each MMA's scales of W, then 4 kXBlocks for each MMA's of x
 #pragma unroll
@@ -439,7 +512,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
 #pragma unroll
                                 for (int k = 0; k < C::kXBlocks; ++k)
                                     copy_scales(tsf + 4 * kMmas + 4 * (C::kXBlocks * j + k),
-                                                sf + ((1 + k) * kBlkBytes + j * 512) / 16);
+                                                sf + ((1 + k) * C::kBlkBytes + j * 512) / 16);
                             }
 #pragma unroll
                             for (int j = 0; j < kMmas; ++j)      // 32 bytes of K an MMA: 2 address units
@@ -469,10 +542,13 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                 // row r of this warp's copy j
                 constexpr int kPer = (NT / 2 / 4 + kGatherWarps - 1) / kGatherWarps;
                 const int w = warp - kGatherWarp0;
-                // and the scales of all columns, 16 bytes a lane, two lanes a row: lane pair l of the four warps has rows l,
-                // 64 + l, ... (gathered by TMA, rows of 32 bytes cost as much as rows of 128)
-                constexpr int kSfPer = (NT + 63) / 64;
-                const int half = lane & 1, sf_l = 16 * w + (lane >> 1);
+                // and the scales of all columns, 16 bytes a lane, neighbours first the pieces of a row (gathered by TMA, rows
+                // of 32 bytes cost as much as rows of 128)
+                constexpr int kPieces = C::kRowBytes / 16, kSfPer = (NT * kPieces + 127) / 128;
+                const auto sf_row = [&](int i) { return (32 * w + lane + 128 * i) / kPieces; };
+                const auto sf_piece = [&](int i) { return (32 * w + lane + 128 * i) % kPieces; };
+                const size_t sf_bytes = (size_t)P.x_rows * KB;
+                const int lg = strided_lg(KB);
                 int step = 0, two = 0;
                 bool ok = true;
                 Walk at = tiles;
@@ -485,7 +561,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                     const int col = rank * (t.mma_n() / 2) + l;
                     entry[0] = P.list[t.r0 + min(col, t.n - 1)];
 #pragma unroll
-                    for (int i = 0; i < kSfPer; ++i) entry[1 + i] = P.list[t.r0 + min(64 * i + sf_l, t.n - 1)];
+                    for (int i = 0; i < kSfPer; ++i) entry[1 + i] = P.list[t.r0 + min(sf_row(i), t.n - 1)];
                 };
                 if (at.more()) ask();
 #pragma unroll 1
@@ -496,7 +572,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                     if (src < 0) src = P.x_rows;                     // past the last row: zeros
                     int sf_src[kSfPer];
 #pragma unroll
-                    for (int i = 0; i < kSfPer; ++i) sf_src[i] = row_of(entry[1 + i], 64 * i + sf_l);
+                    for (int i = 0; i < kSfPer; ++i) sf_src[i] = row_of(entry[1 + i], sf_row(i));
                     at.next();
                     if (at.more()) ask();
                     const int mine = (copies - w + kGatherWarps - 1) / kGatherWarps;
@@ -507,19 +583,27 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                         for (int i = 0; i < 4; ++i) rows4[j][i] = __shfl_sync(0xffffffffu, src, 4 * j + i);
 #pragma unroll 1
                     for (int s = s_begin; s < s_end; ++s, ++step) {
-                        if (sf_tma && (s == s_begin || (s & 1) == 0)) {
-                            const int sl = two % C::kSlots, u = two / C::kSlots, byte = (s >> 1) * kSectorBytes + 16 * half;
+                        if (s == s_begin || (s & 1) == 0) {
+                            const int sl = two % C::kSlots, u = two / C::kSlots;
                             if (u > 0) ok = wait(&sf_empty[sl], (u - 1) & 1);
                             if (!ok) break;
-                            // in the order of the 32-byte swizzle: the halves of rows 4 .. 7 of every eight change places
-                            const uint32_t to = sm_base + C::kOffSlots + sl * C::kSlotBytes + kBlkBytes + sf_l * kSectorBytes +
-                                                16 * (half ^ ((sf_l >> 2) & 1));
+                            const uint32_t to = sm_base + C::kOffSlots + sl * C::kSlotBytes + C::kBlkBytes;
 #pragma unroll
                             for (int i = 0; i < kSfPer; ++i) {
-                                if (64 * i + sf_l >= NT) break;
-                                const bool there = sf_src[i] >= 0 && byte < KB;
-                                cp_async16_zfill(to + i * 64 * kSectorBytes, there ? Q.xs + (size_t)sf_src[i] * KB + byte : Q.xs,
-                                                 there ? 16 : 0);
+                                const int l = sf_row(i), piece = sf_piece(i), byte = (s >> 1) * kSectorBytes + 16 * piece;
+                                if (l >= NT) break;
+                                size_t from = (size_t)max(sf_src[i], 0) * KB;
+                                if constexpr (ODD) {           // as odd_scale_warp wants them; the array may end in a piece
+                                    from = (from & ~(size_t)15) + byte;
+                                    const int left = from < sf_bytes ? (int)min(sf_bytes - from, (size_t)16) : 0;
+                                    const int there = sf_src[i] >= 0 ? left : 0;
+                                    cp_async16_zfill(to + (l >> 7) * C::kBlkBytes + odd_place(l & 127, lg) + 16 * piece,
+                                                     Q.xs + (there > 0 ? from : 0), there);
+                                } else {                       // in the order of the 32-byte swizzle (scale_warp)
+                                    const bool there = sf_src[i] >= 0 && byte < KB;
+                                    cp_async16_zfill(to + l * kSectorBytes + 16 * (piece ^ ((l >> 2) & 1)),
+                                                     Q.xs + (there ? from + byte : 0), there ? 16 : 0);
+                                }
                             }
                             cp_async_arrive_noinc(&sf_raw[sl]);
                             ++two;
@@ -543,16 +627,35 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                     drain(step);
                     drain_scales(two);
                 }
+            } else if (const int blk = warp - kGatherWarp0; ODD && blk < C::kBlocks) {
+                // these warps bring the scales (24 copies of the TMA warp's, in one go, held up those of its operands: 4096 x
+                // 8192 x 2016 took 54 us)
+                int two = 0;
+                bool ok = true;
+#pragma unroll 1
+                for (Walk at = tiles; at.more() && ok; at.next()) {
+                    const Tile t = at.tile();
+                    OddCopies odd;
+                    odd.rows(blk == 0 ? t.e * P.N + t.m0 + rank * kM : t.r0 + 128 * (blk - 1), KB);
+#pragma unroll 1
+                    for (int j = 0; j < m_pairs; ++j, ++two) {
+                        const int sl = two % C::kSlots, u = two / C::kSlots;
+                        if (u > 0) ok = wait(&sf_empty[sl], (u - 1) & 1);
+                        if (!ok) break;
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(&sf_raw[sl], (blk == 0 ? kM : C::kXRows) * kOddBytes);
+                            odd.bring(sm_base + C::kOffSlots + sl * C::kSlotBytes + blk * C::kBlkBytes,
+                                      blk == 0 ? &maps.ws : &maps.xs, (m_begin + j) * kSectorBytes, &sf_raw[sl]);
+                        }
+                    }
+                }
+                if (lane == 0) drain_scales(two);
             }
         } else {
             const int blk = warp - kScaleWarp0;
             uint8_t* slots = sm + C::kOffSlots;
-            const auto run = [&](auto unit) {
-                scale_warp<C, decltype(unit)::value>(Q, tiles, m_pairs, m_begin, blk, rank, slots, sf_raw, sf_ready, sf_empty, wait);
-            };
-            if (sf_tma) run(std::integral_constant<int, 16>{});
-            else if (KB % 4 == 0) run(std::integral_constant<int, 4>{});
-            else run(std::integral_constant<int, 2>{});
+            if constexpr (ODD) odd_scale_warp<C>(Q, tiles, m_pairs, m_begin, blk, rank, slots, sf_raw, sf_ready, wait);
+            else scale_warp<C>(tiles_here * m_pairs, blk, slots, sf_raw, sf_ready, wait);
         }
         if (SPLITS > 1 && tiles.more()) exchange.join();
     } else {
@@ -728,13 +831,13 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
 
 // Sets the kernel up on the current device, once, and says how many of its clusters run there at a time
 // (clusters of eight CTAs do not fill every GPC).
-template <int NT, int SPLITS>
+template <int NT, bool ODD, int SPLITS>
 cudaError_t resident_clusters(const DeviceInfo& dev, int* clusters) {
-    using C = Cfg<NT>;
+    using C = Cfg<NT, ODD>;
     static std::atomic<int> known[64];           // by device: one more than the clusters
     int n = known[dev.device].load(std::memory_order_acquire) - 1;
     if (n < 0) {
-        const auto kernel = rows_fp4_kernel<NT, SPLITS>;
+        const auto kernel = rows_fp4_kernel<NT, ODD, SPLITS>;
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (e != cudaSuccess) return e;
         cudaLaunchAttribute attr{};
@@ -761,40 +864,60 @@ struct Plan {
     float us;
 };
 
-// Tiles of NT columns. The estimate (us) takes the rows to be even over the experts.
-template <int NT>
+// Tiles of NT columns with one, two or four pairs each, if the estimate makes them the best so far.
+//
+// The estimate (us) is a launch, then for every round of tiles its steps and the part of its epilogue that the next tile's
+// steps do not hide; tiles that pairs share add the exchange of their sums. Its constants are fitted to the times of all
+// seven forms at 33 .. 4096 rows, 2048 and 8192 outputs and K of 512, 2048 and 4096; there the form that it takes is at
+// most 6% (0.3% on average) slower than the best. For instance:
+//     4096 x 8192 x 2048   64 columns 68.6, 128: 41.8, 224: 33.5        128 x 8192 x 2048   64: 6.7, 128: 7.0, 224: 7.6
+//      512 x 8192 x 2048   64 columns 13.3, 128: 10.0, 224: 11.3        256 x 2048 x 512    64: 5.3, 128: 5.7, 224: 6.1
+//     33 x 2048 x 4096     64 columns, one pair 7.8, two 7.2, four 6.7  33 x 2048 x 2048    one 6.2, two 6.4, four 6.3
+// The host does not know how rows spread over experts: an expert is taken to have half a tile more than its even share.
+template <int NT, bool ODD>
 cudaError_t plan_tiles(const RowsProduct& P, const DeviceInfo& dev, Plan* best) {
     const int m_tiles = (P.N + 2 * kM - 1) / (2 * kM), nk = (P.K + kStepK - 1) / kStepK;
-    const int groups = std::min(P.R, P.E), rows = (P.R + groups - 1) / groups;
-    Plan p;
-    p.nt = NT;
+    const int groups = std::min(P.R, P.E), rows = (P.R + groups - 1) / groups, pairs = dev.num_sms / 2;
     // tiles at most: every expert has rows, and its last tile one
-    p.tiles = ((P.R - groups) / NT + groups) * (long long)m_tiles;
-    // as many pairs to a tile as the device runs at a time, where each has kMinSteps steps
-    int c2 = 0, c4 = 0;
-    if constexpr (NT <= 128) {
-        if (nk >= 2 * kMinSteps && 2 * p.tiles <= dev.num_sms / 2)
-            if (cudaError_t e = resident_clusters<NT, 2>(dev, &c2); e != cudaSuccess) return e;
-        if (nk >= 4 * kMinSteps && 4 * p.tiles <= dev.num_sms / 2)
-            if (cudaError_t e = resident_clusters<NT, 4>(dev, &c4); e != cudaSuccess) return e;
+    const long long tiles = ((P.R - groups) / NT + groups) * (long long)m_tiles;
+    float parts, n, rounds;                  // tiles of an expert's rows, their rows (in 16s), tiles of a pair
+    if (groups == 1) {
+        const int p = (rows + NT - 1) / NT;
+        parts = (float)p;
+        n = (float)(((rows + p - 1) / p + 15) / 16 * 16);
+        rounds = (float)(((long long)p * m_tiles + pairs - 1) / pairs);
+    } else {
+        parts = std::max(1.0f, (float)rows / NT + 0.5f);
+        n = std::max(std::min((float)NT, rows / parts + 8), NT / 4.0f);
+        rounds = std::max(1.0f, std::ceil(groups * parts * m_tiles / pairs - 0.25f));
     }
-    p.splits = p.tiles <= c4 ? 4 : p.tiles <= c2 ? 2 : 1;
-    const int parts = (rows + NT - 1) / NT, n = ((rows + parts - 1) / parts + Cfg<NT>::kRound - 1) / Cfg<NT>::kRound * Cfg<NT>::kRound;
-    const long long even = (long long)groups * parts * m_tiles, rounds = (even + dev.num_sms / 2 - 1) / (dev.num_sms / 2);
-    const float step = 0.08f + 0.0012f * n;
-    p.us = rounds * ((nk + p.splits - 1) / p.splits * step + 1.0f + (p.splits > 1 ? 0.5f + 0.009f * n : 0.0f));
-    if (p.us < best->us) *best = p;
+    for (int splits = 1; splits <= (NT <= 128 ? 4 : 1); splits *= 2) {
+        if (splits > 1) {
+            // no more tiles than clusters that run at a time, and kMinSteps steps for each pair
+            if (nk < kMinSteps * splits || tiles * splits > pairs) break;
+            int clusters = 0;
+            if constexpr (NT <= 128) {
+                const cudaError_t e = splits == 2 ? resident_clusters<NT, ODD, 2>(dev, &clusters)
+                                                  : resident_clusters<NT, ODD, 4>(dev, &clusters);
+                if (e != cudaSuccess) return e;
+            }
+            if (tiles > clusters) break;
+        }
+        const float joined = splits == 1 ? 0.0f : splits == 2 ? 0.5f + 0.0095f * n : 0.5f + 0.0165f * n;
+        const float us = 4.2f + rounds * ((nk + splits - 1) / splits * (0.21f + 0.00025f * n) + 0.0074f * n) + joined;
+        if (us < best->us) *best = Plan{NT, splits, tiles, us};
+    }
     return cudaSuccess;
 }
 
-template <int NT, int SPLITS>
+template <int NT, bool ODD, int SPLITS>
 cudaError_t launch_clusters(const Fp4Product& P, const Fp4Maps& maps, int tiles, WsHeader* hdr,
                             const DeviceInfo& dev, uint64_t wait_limit, cudaStream_t s) {
     int resident = 0;
-    if (cudaError_t e = resident_clusters<NT, SPLITS>(dev, &resident); e != cudaSuccess) return e;
+    if (cudaError_t e = resident_clusters<NT, ODD, SPLITS>(dev, &resident); e != cudaSuccess) return e;
     if (resident < 1) return cudaErrorInvalidConfiguration;
     const int clusters = SPLITS > 1 ? tiles : std::min(tiles, resident), m_tiles = (P.r.N + 2 * kM - 1) / (2 * kM);
-    return launch_pdl(rows_fp4_kernel<NT, SPLITS>, 2 * SPLITS * clusters, Cfg<NT>::kThreads, Cfg<NT>::kSmem, s, P, maps,
+    return launch_pdl(rows_fp4_kernel<NT, ODD, SPLITS>, 2 * SPLITS * clusters, Cfg<NT, ODD>::kThreads, Cfg<NT, ODD>::kSmem, s, P, maps,
                       m_tiles, tiles, hdr, (unsigned long long)wait_limit);
 }
 
@@ -810,45 +933,63 @@ bool encode_scales(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* m, const v
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT>
+// The same for OddCopies of box_rows rows together: 2^lg rows are one of the map. Where there are fewer, these are its one.
+bool encode_odd_scales(PFN_cuTensorMapEncodeTiled_v12000 fn, CUtensorMap* m, const void* base, uint64_t KB, uint64_t rows,
+                       uint32_t box_rows) {
+    const int lg = strided_lg((int)KB);
+    const cuuint64_t dims[2] = {KB * std::min<uint64_t>(rows, 1u << lg), std::max<uint64_t>(rows >> lg, 1)};
+    const cuuint64_t strides[1] = {KB << lg};
+    const cuuint32_t box[2] = {kOddBytes, box_rows >> lg};
+    const cuuint32_t one[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT, bool ODD>
 cudaError_t launch_tiles(const Fp4Product& P, const Plan& plan, WsHeader* hdr, const DeviceInfo& dev,
                          uint64_t wait_limit, cudaStream_t s) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
     Fp4Maps maps;
     const uint64_t bytes = P.r.K / 2;
     if (fn == nullptr || !encode_rows(fn, &maps.w, P.r.w, true, bytes, (uint64_t)P.r.E * P.r.N, kM)) return cudaErrorInvalidValue;
-    if (!encode_rows(fn, &maps.x, P.r.x, true, bytes, P.r.x_rows, P.r.gather ? 1 : Cfg<NT>::kBoxRows)) return cudaErrorInvalidValue;
-    maps.ws = maps.xs = maps.w;
-    if (const uint64_t KB = P.r.K / 16; KB % 16 == 0 &&
-        (!encode_scales(fn, &maps.ws, P.ws, KB, (uint64_t)P.r.E * P.r.N, kM) ||
-         !encode_scales(fn, &maps.xs, P.xs, KB, P.r.x_rows, P.r.gather ? 1 : NT)))
+    if (!encode_rows(fn, &maps.x, P.r.x, true, bytes, P.r.x_rows, P.r.gather ? 1 : Cfg<NT, ODD>::kBoxRows)) return cudaErrorInvalidValue;
+    const uint64_t KB = P.r.K / 16, w_rows = (uint64_t)P.r.E * P.r.N;
+    if (ODD ? !encode_odd_scales(fn, &maps.ws, P.ws, KB, w_rows, kM) ||
+                  !encode_odd_scales(fn, &maps.xs, P.xs, KB, P.r.x_rows, Cfg<NT, ODD>::kXRows)
+            : !encode_scales(fn, &maps.ws, P.ws, KB, w_rows, kM) ||
+              !encode_scales(fn, &maps.xs, P.xs, KB, P.r.x_rows, P.r.gather ? 1 : NT))
         return cudaErrorInvalidValue;
     const int tiles = (int)plan.tiles;
     if constexpr (NT <= 128) {
-        if (plan.splits == 4) return launch_clusters<NT, 4>(P, maps, tiles, hdr, dev, wait_limit, s);
-        if (plan.splits == 2) return launch_clusters<NT, 2>(P, maps, tiles, hdr, dev, wait_limit, s);
+        if (plan.splits == 4) return launch_clusters<NT, ODD, 4>(P, maps, tiles, hdr, dev, wait_limit, s);
+        if (plan.splits == 2) return launch_clusters<NT, ODD, 2>(P, maps, tiles, hdr, dev, wait_limit, s);
     }
-    return launch_clusters<NT, 1>(P, maps, tiles, hdr, dev, wait_limit, s);
+    return launch_clusters<NT, ODD, 1>(P, maps, tiles, hdr, dev, wait_limit, s);
+}
+
+template <bool ODD>
+cudaError_t launch(const Fp4Product& P, WsHeader* hdr, const DeviceInfo& dev, uint64_t wait_limit, cudaStream_t s) {
+    Plan plan{};
+    plan.us = 3.0e38f;
+    const int groups = std::min(P.r.R, P.r.E), rows = (P.r.R + groups - 1) / groups;
+    cudaError_t e;
+    if ((e = plan_tiles<64, ODD>(P.r, dev, &plan)) != cudaSuccess) return e;
+    if ((e = plan_tiles<128, ODD>(P.r, dev, &plan)) != cudaSuccess) return e;
+    // Gathered rows cost the widest tiles more, few rows to an expert most (K = 2048, 1024 outputs, 256 experts of 128 rows
+    // each: 128 columns 76.2 us, 224: 81.7; 64 experts of 512: 56.7, 54.7).
+    if ((!P.r.gather || rows >= 256) && (e = plan_tiles<224, ODD>(P.r, dev, &plan)) != cudaSuccess) return e;
+    if (plan.tiles > kMaxTiles) return cudaErrorInvalidConfiguration;
+    if (plan.nt == 64) return launch_tiles<64, ODD>(P, plan, hdr, dev, wait_limit, s);
+    if (plan.nt == 128) return launch_tiles<128, ODD>(P, plan, hdr, dev, wait_limit, s);
+    return launch_tiles<224, ODD>(P, plan, hdr, dev, wait_limit, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rows_fp4(const Fp4Product& P, WsHeader* hdr, const DeviceInfo& dev, uint64_t wait_limit,
                             cudaStream_t s) {
-    Plan plan{};
-    plan.us = 3.0e38f;
-    const int groups = std::min(P.r.R, P.r.E), rows = (P.r.R + groups - 1) / groups;
-    cudaError_t e;
-    if (rows <= 64) {
-        if ((e = plan_tiles<64>(P.r, dev, &plan)) != cudaSuccess) return e;
-    } else {
-        if ((e = plan_tiles<128>(P.r, dev, &plan)) != cudaSuccess) return e;
-        if ((e = plan_tiles<224>(P.r, dev, &plan)) != cudaSuccess) return e;
-    }
-    if (plan.tiles > kMaxTiles) return cudaErrorInvalidConfiguration;
-    if (plan.nt == 64) return launch_tiles<64>(P, plan, hdr, dev, wait_limit, s);
-    if (plan.nt == 128) return launch_tiles<128>(P, plan, hdr, dev, wait_limit, s);
-    return launch_tiles<224>(P, plan, hdr, dev, wait_limit, s);
+    return P.r.K % kStepK == 0 ? launch<false>(P, hdr, dev, wait_limit, s) : launch<true>(P, hdr, dev, wait_limit, s);
 }
 
 }  // namespace nvfp4
