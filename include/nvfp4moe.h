@@ -48,7 +48,9 @@
  *     Work is enqueued asynchronously on it.
  *   - nvfp4_gemv_w4a16 and the single-token layer request their weights (of a layer also the router's
  *     and the shared gate's rows) before they wait for the kernel before them on the stream; they, the
- *     8-bit quantiser and the products let the next kernel start before their outputs are written. So a
+ *     8-bit quantiser, the products, the calls that write rows (nvfp4_quantize_rows, nvfp4_dequantize_rows,
+ *     rmsnorm_residual, moe_swiglu) and those that sort them (moe_permute, moe_combine,
+ *     moe_combine_backward) let the next kernel start before their outputs are written. So a
  *     matrix that one of these calls writes (a router's rows from a product, say) must not be a weight of a
  *     GEMV or single-token layer enqueued right behind it: let any other kernel or a copy come between.
  *   - Argument and shape checks run on the host, before anything is enqueued; a
@@ -534,7 +536,7 @@ NVFP4_API nvfp4_status moe_combine(const void* rows, int32_t rows_type, const fl
  * t*k + j without positions:
  *   d_rows[p] = w[t,j] * dy[t]   rounded to the rows' type;   d_w[t,j] = sum_n dy[t,n] * rows[p,n]   in fp32, in a
  *   fixed order. A position outside [0, T*k) writes no row and has d_w 0; rows that no position names are left
- *   as they were; one that two entries name is either's.
+ *   as they were; one that two entries name is either's (with d_rows = rows their d_w is undefined).
  *   dy      bf16 or fp32 [T, N] device (dy_type);  rows  as moe_combine's (NULL where d_w is NULL)
  *   w       fp32 [T, k] device or NULL (all 1)
  *   d_rows  like rows, written, or NULL;  d_w  fp32 [T, k], written, or NULL. d_rows may be rows.

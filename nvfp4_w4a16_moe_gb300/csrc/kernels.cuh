@@ -247,11 +247,11 @@ struct Fp4Product {
     int parts;
 };
 // Up to kStreamRows rows in all, of up to kStreamBytes4 of codes: weights streamed through warp-level MMAs; otherwise
-// tcgen05 tiles. Device us, stream / tiles, weights that are not in the L2: one row 8192 x 2048 (8 MiB) 4.6 / 7.2,
-// 2048 x 8192 5.8 / 7.5, 1024 x 2048 3.4 / 5.8; 8 rows 8192 x 2048 4.9 / 6.9; 8 experts of 1024 x 2048 with a row each
-// 6.2 / 8.3; but 16 experts (two tokens: 16 MiB) 9.4 / 9.4 and one row of 248320 x 2048 (243 MiB) 80 / 50 to 61:
-// expanding codes to f16 costs the streaming kernel 3.6 TB/s.
-constexpr long long kStreamBytes4 = 16ll << 20;
+// tcgen05 tiles. Device us, stream / tiles, weights that are not in the L2: one row of 8192 x 2048 (8 MiB) 5.1 / 7.7,
+// 2048 x 8192 6.3 / 7.9, 1024 x 512 3.2 / 4.8; 8 rows of 8192 x 2048 5.8 / 7.5; 8 experts of 1024 x 2048 with a row each
+// 6.2 / 8.3; but 16384 x 2048 (16 MiB) with one row 9.2 / 9.2, with eight 9.5 / 8.1, and one row of 248320 x 2048
+// (243 MiB) 80 / 62: expanding codes to f16 costs the streaming kernel 3.6 TB/s.
+constexpr long long kStreamBytes4 = 12ll << 20;
 cudaError_t launch_fp4_stream(const Fp4Product& P, const DeviceInfo& dev, cudaStream_t s);
 cudaError_t launch_rows_fp4(const Fp4Product& P, WsHeader* hdr, const DeviceInfo& dev, uint64_t wait_limit,
                             cudaStream_t s);

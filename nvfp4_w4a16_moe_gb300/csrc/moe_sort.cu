@@ -10,7 +10,10 @@
 // Bound: HBM. A row is read once and written once: T * k * N elements either way. All rows of a token are asked for
 // before the first is used: entries that a token does not have read the row of one that it has, and rows that are not
 // there row 0, and what was read is taken out afterwards. (Asked for one behind the other's branch, the combine of 4096
-// tokens of 8 x 2048 took 84 us.)
+// tokens of 8 x 2048 took 84 us.) us of 4096 tokens of 8 x 2048 in bf16, and of the bytes at the copy rate: permute 24.8
+// (22.2), combine 32.9 (24.7), backward 54 (41.9): rows in the lists' order are read at 5.2 TB/s, and asking for the next
+// token's positions ahead changes nothing. Rows of 2046 take 28, 31 and 61; of 2047, which start at odd elements and are
+// read two bytes at a time, 38, 57 and 151.
 #include <type_traits>
 
 #include "common.cuh"

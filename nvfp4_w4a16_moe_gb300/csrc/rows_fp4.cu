@@ -28,7 +28,8 @@
 // clock (0.29 us for 224 columns, 6 PFLOP/s: 4096 x 8192 x 8192 in 90 us), and below K = 1024 the outputs, which memory
 // takes at 4.5 TB/s (4096 x 8192 x 512: 22 us, of which a fill of y takes 17). 4096 x 8192 x 2048 takes 33.4 us, 4.1
 // PFLOP/s. With few rows to many experts the weights from memory (64 tokens to eight of 256 experts of 1024 x 2048 each:
-// 38 us for the 200 MB of some 170 experts), with few rows of one matrix the start of a launch: some 4.5 us pass before and after the steps.
+// 38 us for the 200 MB of some 170 experts), with few rows of one
+// matrix the start of a launch: some 4.5 us pass before and after the steps.
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -45,13 +46,14 @@ constexpr int kABytes = kM * kStepBytes;
 constexpr int kStepK = 2 * kStepBytes;   // elements of a step
 constexpr int kMmas = kStepK / 64;       // MMAs of a step
 constexpr int kSectorBytes = 32;         // block scales of a row in two steps
-constexpr int kOddBytes = 48;            // ... with the 16-byte pieces that they lie in, where rows are no multiple of 16 bytes
+constexpr int kOddBytes = 48;            // ... with the 16-byte pieces that they lie in (rows are no multiple of 16 bytes)
 constexpr int kRing = 192 * 1024;        // operands and scales
 constexpr int kMaxStages = 9;
 constexpr int kWidths = 16;
 constexpr int kMinSteps = 2;             // steps of each pair that shares a tile's K, at least
 
-// Warps: 16 of epilogue, TMA, MMA, four of gather (which bring OddCopies where no rows are gathered), one that looks up the tiles' ends, one for every 128 rows of scales.
+// Warps: 16 of epilogue, TMA, MMA, four of gather (which bring OddCopies where no rows are gathered), one that looks up the
+// tiles' ends, one for every 128 rows of scales.
 constexpr int kEpiWarps = 16, kTmaWarp = 16, kMmaWarp = 17, kGatherWarp0 = 18, kGatherWarps = 4, kEndsWarp = 22;
 constexpr int kScaleWarp0 = 23;
 
@@ -151,9 +153,9 @@ __device__ __forceinline__ void scale_warp(int count, int blk, uint8_t* slots, u
     }
 }
 
-// Rows of KB scales, a multiple of 2 but not of 16, are no strides of a tensor map; 2^lg(KB) rows together are. One copy then
-// brings every 2^lg-th row: of each the three 16-byte pieces that 32 bytes may lie in, from byte (row KB) mod 16 on. Row l
-// of the 128 is row l >> lg of copy l mod 2^lg.
+// Rows of KB scales, a multiple of 2 but not of 16, are no strides of a tensor map; 2^lg(KB) rows together are. One copy
+// then brings every 2^lg-th row: of each the three 16-byte pieces that 32 bytes may lie in, from byte (row KB) mod 16 on.
+// Row l of the 128 is row l >> lg of copy l mod 2^lg.
 __host__ __device__ __forceinline__ int strided_lg(int KB) { return KB & 2 ? 3 : KB & 4 ? 2 : 1; }
 __device__ __forceinline__ int odd_place(int l, int lg) { return (((l & ((1 << lg) - 1)) << (7 - lg)) + (l >> lg)) * kOddBytes; }
 
@@ -171,8 +173,8 @@ struct OddCopies {
     }
 };
 
-// The same for rows of KB scales that OddCopies, or the gather warps in their order, brought. The array's last rows, where they
-// make no 2^lg, lie behind the map's end (zeros): the warp loads them itself.
+// The same for rows of KB scales that OddCopies, or the gather warps in their order, brought. The array's last rows, where
+// they make no 2^lg, lie behind the map's end (zeros): the warp loads them itself.
 template <typename C>
 __device__ __forceinline__ void odd_scale_warp(const Fp4Product& Q, WalkOf<C::kRound> at, int pairs, int m_begin, int blk,
                                                int rank, uint8_t* slots, uint64_t* raw, uint64_t* ready, const Waiter& wait) {
@@ -220,7 +222,7 @@ __device__ __forceinline__ void odd_scale_warp(const Fp4Product& Q, WalkOf<C::kR
             if (!wait(&raw[slot], par)) return;
             if (spares > 0) {
                 const int l = spare - first;
-                uint8_t* p = blkp + odd_place(l, lg) + (spare * KB & 15) + 8 * (lane & 3);
+                uint8_t* p = blkp + odd_place(l, lg) + ((uint32_t)spare * KB & 15u) + 8 * (lane & 3);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     if (lane >> 2 < spares) *reinterpret_cast<uint16_t*>(p + 2 * k) = late[k];
@@ -869,7 +871,7 @@ struct Plan {
 // The estimate (us) is a launch, then for every round of tiles its steps and the part of its epilogue that the next tile's
 // steps do not hide; tiles that pairs share add the exchange of their sums. Its constants are fitted to the times of all
 // seven forms at 33 .. 4096 rows, 2048 and 8192 outputs and K of 512, 2048 and 4096; there the form that it takes is at
-// most 6% (0.3% on average) slower than the best. For instance:
+// most 6% (0.4% on average) slower than the best; over 2 to 256 experts, whose rows it does not know, at most 16% (1.7%).
 //     4096 x 8192 x 2048   64 columns 68.6, 128: 41.8, 224: 33.5        128 x 8192 x 2048   64: 6.7, 128: 7.0, 224: 7.6
 //      512 x 8192 x 2048   64 columns 13.3, 128: 10.0, 224: 11.3        256 x 2048 x 512    64: 5.3, 128: 5.7, 224: 6.1
 //     33 x 2048 x 4096     64 columns, one pair 7.8, two 7.2, four 6.7  33 x 2048 x 2048    one 6.2, two 6.4, four 6.3

@@ -50,7 +50,8 @@ def _weight(nv, w, N, K):
 
 DENSE = [(1, 1, 32), (1, 130, 32), (1, 128, 2048), (2, 513, 2016), (3, 8192, 2048), (7, 300, 1056), (8, 256, 4096),
          (9, 40, 64), (16, 1000, 96), (17, 2048, 512), (64, 5003, 2048), (65, 129, 288), (128, 512, 1024), (129, 257, 544),
-         (200, 2600, 512), (256, 256, 256), (257, 255, 224), (300, 513, 4096), (700, 1030, 160), (2000, 2600, 512)]
+         (200, 2600, 512), (256, 256, 256), (257, 255, 224), (300, 513, 4096), (700, 1030, 160), (2000, 2600, 512),
+         (64, 8192, 4096), (500, 2048, 8192), (256, 1500, 16384), (40, 8000, 4064), (250, 1500, 16352)]   # pairs share K
 
 
 @pytest.mark.parametrize("T,N,K", DENSE)
@@ -371,8 +372,10 @@ def test_empty_and_refusals(nv):
 # ---------------------------------------------------------------- waits
 
 @pytest.mark.parametrize("rows", ["list", "gather", "scatter"])
-@pytest.mark.parametrize("T,N,K", [(2000, 2600, 512), (2000, 2600, 544), (64, 6000, 2048), (128, 513, 4096), (300, 300, 1056)],
-                         ids=["one_pair", "one_pair_odd", "two_pairs", "four_pairs", "odd"])
+@pytest.mark.parametrize("T,N,K", [(2000, 2600, 512), (2000, 2600, 544), (64, 6000, 2048), (128, 513, 4096), (300, 300, 1056),
+                                   (64, 8192, 4096), (40, 8000, 4064), (128, 513, 4064)],
+                         ids=["one_pair", "one_pair_odd", "few_tiles", "four_pairs", "odd", "two_pairs", "two_pairs_odd",
+                              "four_pairs_odd"])
 def test_a_wait_that_runs_out_is_reported(nv, T, N, K, rows):
     """A limit of 1 ns is over at the first poll that fails, and the first operands take a round trip to memory: the
     status and the NaN are always there, and the next call is exact again."""
