@@ -15,7 +15,7 @@
 //     in another order is needed. Rows whose scales are no multiple of 16 bytes
 //     (K is none of 256) are no strides of a tensor map; two, four or eight of them together are (OddCopies): 48 bytes of
 //     each, out of which the same warp takes its 32. (That warp loading them from global memory: 4096 x 8192 x 2016 in 76
-//     us, rows gathered for 256 experts in 190; now 52 and 101.) Behind the end of K the scales are 0, so neither the codes
+//     us, rows gathered for 256 experts in 190; now 44 and 101.) Behind the end of K the scales are 0, so neither the codes
 //     nor NaN scales that lie there count.
 //   The MMA thread copies a step's scales from the ring to tensor memory (tcgen05.cp, to all four lane quarters), right
 //     before the step's MMAs: the tensor pipe runs copies and MMAs of one thread in the order of issue.
@@ -106,6 +106,13 @@ __device__ __forceinline__ void mma_nvfp4(uint32_t d, uint64_t a, uint64_t b, ui
         " tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}"
         :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
 }
+// tma_load_2d into the same place of every CTA of the mask, each of whose barriers counts the bytes.
+__device__ __forceinline__ void tma_load_2d_to(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar, uint16_t mask) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
+        "[%0], [%1, {%2, %3}], [%4], %5;"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(su32(bar)), "h"(mask) : "memory");
+}
 // 32 lines of 16 bytes to four columns of tensor memory, the same in all lane quarters, in both CTAs.
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" :: "r"(tmem), "l"(desc) : "memory");
@@ -170,6 +177,15 @@ struct OddCopies {
 #pragma unroll
         for (int c = 0; c < 8; ++c)
             if (c < 1 << lg) tma_load_2d(to + c * ((kM >> lg) * kOddBytes), map, x[c] + byte, y[c], bar);
+    }
+    // Half of the copies, into both CTAs of a pair: the other one brings the rest. (Each CTA bringing all: 4096 x 8192 x
+    // 2016 in 52 us, now 44. Scales whose rows are strides gain nothing by it.)
+    __device__ __forceinline__ void bring_half(uint32_t to, const CUtensorMap* map, int byte, uint64_t* bar, int rank,
+                                               uint16_t mask) const {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c < 1 << lg && (c & 1) == rank)
+                tma_load_2d_to(to + c * ((kM >> lg) * kOddBytes), map, x[c] + byte, y[c], bar, mask);
     }
 };
 
@@ -630,8 +646,9 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                     drain_scales(two);
                 }
             } else if (const int blk = warp - kGatherWarp0; ODD && blk < C::kBlocks) {
-                // these warps bring the scales (24 copies of the TMA warp's, in one go, held up those of its operands: 4096 x
-                // 8192 x 2016 took 54 us)
+                // these warps bring the scales (24 copies of the TMA warp's, in one go, held up those of its operands). The other
+                // CTA's copies may land before this one's bytes are expected, but not before the slot is free: MMAs of both
+                // CTAs' slots are done together.
                 int two = 0;
                 bool ok = true;
 #pragma unroll 1
@@ -646,8 +663,10 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                         if (!ok) break;
                         if (elect_one()) {
                             mbar_arrive_expect_tx(&sf_raw[sl], (blk == 0 ? kM : C::kXRows) * kOddBytes);
-                            odd.bring(sm_base + C::kOffSlots + sl * C::kSlotBytes + blk * C::kBlkBytes,
-                                      blk == 0 ? &maps.ws : &maps.xs, (m_begin + j) * kSectorBytes, &sf_raw[sl]);
+                            const uint32_t to = sm_base + C::kOffSlots + sl * C::kSlotBytes + blk * C::kBlkBytes;
+                            const int byte = (m_begin + j) * kSectorBytes;
+                            if (blk == 0) odd.bring(to, &maps.ws, byte, &sf_raw[sl]);
+                            else odd.bring_half(to, &maps.xs, byte, &sf_raw[sl], rank, pair_mask);
                         }
                     }
                 }
