@@ -113,6 +113,14 @@ __device__ __forceinline__ void tma_load_2d_to(uint32_t dst, const CUtensorMap* 
         "[%0], [%1, {%2, %3}], [%4], %5;"
         :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(su32(bar)), "h"(mask) : "memory");
 }
+__device__ __forceinline__ void tma_gather4_to(uint32_t dst, const CUtensorMap* map, int x, int r0, int r1, int r2, int r3,
+                                               uint64_t* bar, uint16_t mask) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.multicast::cluster "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(su32(bar)), "h"(mask)
+        : "memory");
+}
 // 32 lines of 16 bytes to four columns of tensor memory, the same in all lane quarters, in both CTAs.
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" :: "r"(tmem), "l"(desc) : "memory");
@@ -392,7 +400,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                 mbar_init(&acc_empty[i], 2 * kEpiWarps);
             }
             for (int i = 0; i < C::kSlots; ++i) {
-                mbar_init(&sf_raw[i], P.gather ? 1 + 32 * kGatherWarps : ODD ? C::kBlocks : 1);
+                mbar_init(&sf_raw[i], !ODD ? 1 : P.gather ? 1 + 32 * kGatherWarps : C::kBlocks);
                 mbar_init(&sf_ready[i], C::kBlocks);
                 mbar_init(&sf_empty[i], 1);
             }
@@ -470,7 +478,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                                 odd.bring(to, &maps.ws, (s >> 1) * kSectorBytes, &sf_raw[sl]);
                             }
                         } else if (elect_one()) {
-                            mbar_arrive_expect_tx(&sf_raw[sl], C::kBlkBytes + (P.gather ? 0 : NT * kSectorBytes));
+                            mbar_arrive_expect_tx(&sf_raw[sl], C::kBlkBytes + (P.gather ? 2 * share : NT) * kSectorBytes);
                             tma_load_2d(to, &maps.ws, (s >> 1) * kSectorBytes, wy, &sf_raw[sl]);
                             if (!P.gather) tma_load_2d(to + C::kBlkBytes, &maps.xs, (s >> 1) * kSectorBytes, t.r0, &sf_raw[sl]);
                         }
@@ -560,9 +568,9 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                 // row r of this warp's copy j
                 constexpr int kPer = (NT / 2 / 4 + kGatherWarps - 1) / kGatherWarps;
                 const int w = warp - kGatherWarp0;
-                // and the scales of all columns, 16 bytes a lane, neighbours first the pieces of a row (gathered by TMA, rows
-                // of 32 bytes cost as much as rows of 128)
-                constexpr int kPieces = C::kRowBytes / 16, kSfPer = (NT * kPieces + 127) / 128;
+                // Scales, ODD: of all columns, 16 bytes a lane, neighbours first the pieces of a row. Otherwise the same copies
+                // bring those of the CTA's own columns into both.
+                constexpr int kPieces = kOddBytes / 16, kSfPer = ODD ? (NT * kPieces + 127) / 128 : 0;
                 const auto sf_row = [&](int i) { return (32 * w + lane + 128 * i) / kPieces; };
                 const auto sf_piece = [&](int i) { return (32 * w + lane + 128 * i) % kPieces; };
                 const size_t sf_bytes = (size_t)P.x_rows * KB;
@@ -588,7 +596,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                     const auto row_of = [&](int e, int col) { return col < n && (unsigned)e < (unsigned)P.R ? e / P.k : -1; };
                     int src = row_of(entry[0], l < share ? rank * share + l : n);
                     if (src < 0) src = P.x_rows;                     // past the last row: zeros
-                    int sf_src[kSfPer];
+                    int sf_src[kSfPer + 1];
 #pragma unroll
                     for (int i = 0; i < kSfPer; ++i) sf_src[i] = row_of(entry[1 + i], sf_row(i));
                     at.next();
@@ -606,24 +614,29 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                             if (u > 0) ok = wait(&sf_empty[sl], (u - 1) & 1);
                             if (!ok) break;
                             const uint32_t to = sm_base + C::kOffSlots + sl * C::kSlotBytes + C::kBlkBytes;
+                            if constexpr (ODD) {       // as odd_scale_warp wants them; the array may end in a piece
 #pragma unroll
-                            for (int i = 0; i < kSfPer; ++i) {
-                                const int l = sf_row(i), piece = sf_piece(i), byte = (s >> 1) * kSectorBytes + 16 * piece;
-                                if (l >= NT) break;
-                                size_t from = (size_t)max(sf_src[i], 0) * KB;
-                                if constexpr (ODD) {           // as odd_scale_warp wants them; the array may end in a piece
-                                    from = (from & ~(size_t)15) + byte;
+                                for (int i = 0; i < kSfPer; ++i) {
+                                    const int l = sf_row(i), piece = sf_piece(i);
+                                    if (l >= NT) break;
+                                    const size_t from = ((size_t)max(sf_src[i], 0) * KB & ~(size_t)15) +
+                                                        (s >> 1) * kSectorBytes + 16 * piece;
                                     const int left = from < sf_bytes ? (int)min(sf_bytes - from, (size_t)16) : 0;
                                     const int there = sf_src[i] >= 0 ? left : 0;
                                     cp_async16_zfill(to + (l >> 7) * C::kBlkBytes + odd_place(l & 127, lg) + 16 * piece,
                                                      Q.xs + (there > 0 ? from : 0), there);
-                                } else {                       // in the order of the 32-byte swizzle (scale_warp)
-                                    const bool there = sf_src[i] >= 0 && byte < KB;
-                                    cp_async16_zfill(to + l * kSectorBytes + 16 * (piece ^ ((l >> 2) & 1)),
-                                                     Q.xs + (there ? from + byte : 0), there ? 16 : 0);
+                                }
+                                cp_async_arrive_noinc(&sf_raw[sl]);
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < kPer; ++j) {
+                                    if (j >= mine) break;
+                                    if (elect_one())
+                                        tma_gather4_to(to + (rank * share + 4 * (w + kGatherWarps * j)) * kSectorBytes, &maps.xs,
+                                                       (s >> 1) * kSectorBytes, rows4[j][0], rows4[j][1], rows4[j][2], rows4[j][3],
+                                                       &sf_raw[sl], pair_mask);
                                 }
                             }
-                            cp_async_arrive_noinc(&sf_raw[sl]);
                             ++two;
                         }
                         const int st = step % C::kStages, u = step / C::kStages;

@@ -183,6 +183,7 @@ CASES = [  # T, k, E, N, K, kind, parts
     (300, 2, 4, 260, 416, "one", 2), (257, 1, 2, 127, 640, "even", 1), (200, 8, 17, 386, 1056, "skew", 2),
     (1024, 1, 256, 64, 128, "skew", 2), (33, 1, 33, 136, 4096, "even", 136), (90, 8, 6, 1024, 2048, "skew", 2),
     (700, 1, 2, 261, 1984, "one", 1), (450, 2, 3, 130, 1920, "even", 1), (600, 1, 2, 135, 2016, "skew", 1),
+    (300, 2, 4, 130, 256, "skew", 1), (40, 4, 9, 70, 768, "skew", 1), (900, 1, 2, 200, 512, "skew", 1),
 ]
 
 
