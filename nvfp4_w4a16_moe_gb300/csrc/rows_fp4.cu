@@ -15,7 +15,7 @@
 //     in another order is needed. Rows whose scales are no multiple of 16 bytes
 //     (K is none of 256) are no strides of a tensor map; two, four or eight of them together are (OddCopies): 48 bytes of
 //     each, out of which the same warp takes its 32. (That warp loading them from global memory: 4096 x 8192 x 2016 in 76
-//     us, rows gathered for 256 experts in 190; now 44 and 101.) Behind the end of K the scales are 0, so neither the codes
+//     us, rows gathered for 256 experts in 190; now 44 and 98.) Behind the end of K the scales are 0, so neither the codes
 //     nor NaN scales that lie there count.
 //   The MMA thread copies a step's scales from the ring to tensor memory (tcgen05.cp, to all four lane quarters), right
 //     before the step's MMAs: the tensor pipe runs copies and MMAs of one thread in the order of issue.
@@ -1010,9 +1010,10 @@ cudaError_t launch(const Fp4Product& P, WsHeader* hdr, const DeviceInfo& dev, ui
     cudaError_t e;
     if ((e = plan_tiles<64, ODD>(P.r, dev, &plan)) != cudaSuccess) return e;
     if ((e = plan_tiles<128, ODD>(P.r, dev, &plan)) != cudaSuccess) return e;
-    // Gathered rows cost the widest tiles more, few rows to an expert most (K = 2048, 1024 outputs, 256 experts of 128 rows
-    // each: 128 columns 76.2 us, 224: 81.7; 64 experts of 512: 56.7, 54.7).
-    if ((!P.r.gather || rows >= 256) && (e = plan_tiles<224, ODD>(P.r, dev, &plan)) != cudaSuccess) return e;
+    // Gathered rows cost the widest tiles more, the fewer an expert has and where all of a tile's scales come in pieces (us,
+    // 128 / 224 columns, 1024 outputs: K = 2048, 94 rows to an expert 64.7 / 65.7, 128: 73.3 / 72.0, 512: 53.6 / 47.7;
+    // K = 2016, 128 rows 97 / 109, 256: 82.6 / 83.1, 512: 43.5 / 42.0).
+    if ((!P.r.gather || rows >= (ODD ? 256 : 128)) && (e = plan_tiles<224, ODD>(P.r, dev, &plan)) != cudaSuccess) return e;
     if (plan.tiles > kMaxTiles) return cudaErrorInvalidConfiguration;
     if (plan.nt == 64) return launch_tiles<64, ODD>(P, plan, hdr, dev, wait_limit, s);
     if (plan.nt == 128) return launch_tiles<128, ODD>(P, plan, hdr, dev, wait_limit, s);
