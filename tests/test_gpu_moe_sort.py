@@ -33,7 +33,7 @@ def _close(got, want, S, k, dtype):
 
 
 SHAPES = [(1, 8, 8, 2048), (1, 2, 1, 1), (5, 7, 3, 8), (64, 256, 8, 2048), (33, 16, 4, 1111), (9, 4, 2, 250), (3, 40, 8, 2056),
-          (2, 5, 5, 4099)]
+          (2, 5, 5, 4099), (7, 5, 3, 257), (6, 9, 4, 511), (4, 6, 6, 769), (40, 16, 2, 255), (20, 4, 1, 513), (11, 3, 2, 3)]
 
 
 @pytest.mark.parametrize("T,E,k,N", SHAPES)
@@ -169,6 +169,41 @@ def test_in_place_nan_and_the_same_bits_every_time(nv):
     y = nv.moe_combine(bad, k, w, pos, add=add)
     changed = (y != first[0]) | y.isnan()
     assert changed.nonzero().tolist() == [[5, 3], [7, 4]] and y[5, 3].isnan() and y[7, 4].isinf()
+
+
+@pytest.mark.parametrize("N", [1, 63, 255, 257, 511, 513, 1025])
+def test_odd_lengths_in_place_and_between_others(nv, N):
+    """Rows of an odd length share 4-byte words with their neighbours: every element is written, once, none beside the
+    tensor, and in place the same."""
+    T, E, k = 37, 16, 3
+    g, logits, x = _case(T, E, k, N, N)
+    ids, w, offsets, lst = nv.moe_route_topk(logits.cuda(), k)
+    x = x.to(BF16).cuda()
+
+    def inside(rows):
+        buf = torch.full((rows * N + 16,), 7.0, dtype=BF16, device="cuda")
+        return buf, buf[:rows * N].view(rows, N)
+    buf, rows = inside(T * k)
+    _, pos = nv.moe_permute(x, lst, k, rows=rows)
+    assert torch.equal(rows, x[lst.long() // k]) and (buf[-16:] == 7).all()
+    back, dy = torch.randn(T * k, N, generator=g).to(BF16).cuda(), torch.randn(T, N, generator=g).to(BF16).cuda()
+    buf, y = inside(T)
+    y.copy_(x)
+    nv.moe_combine(back, k, w, pos, add=y, y=y)
+    assert torch.equal(y, nv.moe_combine(back, k, w, pos, add=x)) and (buf[-16:] == 7).all()
+    d_rows, d_w = nv.moe_combine_backward(dy, back, w, pos)
+    buf, here = inside(T * k)
+    here.copy_(back)
+    _, again = nv.moe_combine_backward(dy, here, w, pos, d_rows=here)
+    assert torch.equal(here, d_rows) and torch.equal(again, d_w) and (buf[-16:] == 7).all()
+    # some rows alone: the others keep what they had
+    few = torch.where(torch.arange(T * k, device="cuda") % 3 == 1, pos, -1).to(torch.int32)
+    buf, here = inside(T * k)
+    here.fill_(5.0)
+    nv.moe_combine_backward(dy, back, w, few, d_rows=here)
+    named = torch.zeros(T * k, dtype=torch.bool, device="cuda")
+    named[few[few >= 0].long()] = True
+    assert torch.equal(here[named], d_rows[named]) and (here[~named] == 5).all() and (buf[-16:] == 7).all()
 
 
 def test_streams_graphs_and_nothing_to_do(nv):
