@@ -28,8 +28,8 @@
 // clock (0.29 us for 224 columns, 6 PFLOP/s: 4096 x 8192 x 8192 in 90 us), and below K = 1024 the outputs, which memory
 // takes at 4.5 TB/s (4096 x 8192 x 512: 22 us, of which a fill of y takes 17). 4096 x 8192 x 2048 takes 33.4 us, 4.1
 // PFLOP/s. With few rows to many experts the weights from memory (64 tokens to eight of 256 experts of 1024 x 2048 each:
-// 38 us for the 200 MB of some 170 experts), with few rows of one
-// matrix the start of a launch: some 4.5 us pass before and after the steps.
+// 38 us for the 200 MB of some 170 experts), with few rows of one matrix the start of a launch: some 4.5 us pass before
+// and after the steps.
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -95,7 +95,7 @@ struct Cfg {
 
 struct Fp4Maps {
     CUtensorMap w, x;      // x: boxes of kBoxRows rows, or of one to gather
-    CUtensorMap ws, xs;    // block scales of two steps (encode_scales, encode_odd_scales); xs is not read to gather
+    CUtensorMap ws, xs;    // block scales of two steps (encode_scales, encode_odd_scales); xs to gather: of one row
 };
 
 // D (256 x N over both CTAs) = A B^T of 64 columns, scaled by 4 E4M3 scales a row, plus D where accumulate.
@@ -106,8 +106,9 @@ __device__ __forceinline__ void mma_nvfp4(uint32_t d, uint64_t a, uint64_t b, ui
         " tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}"
         :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
 }
-// tma_load_2d into the same place of every CTA of the mask, each of whose barriers counts the bytes.
-__device__ __forceinline__ void tma_load_2d_to(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar, uint16_t mask) {
+// tma_load_2d and tma_gather4 into the same place of every CTA of the mask, each of whose barriers counts the bytes.
+__device__ __forceinline__ void tma_load_2d_to(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
+                                               uint16_t mask) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
         "[%0], [%1, {%2, %3}], [%4], %5;"
