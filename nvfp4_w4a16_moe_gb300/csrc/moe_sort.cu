@@ -10,10 +10,10 @@
 // Bound: HBM. A row is read once and written once: T * k * N elements either way. All rows of a token are asked for
 // before the first is used: entries that a token does not have read the row of one that it has, and rows that are not
 // there row 0, and what was read is taken out afterwards. (Asked for one behind the other's branch, the combine of 4096
-// tokens of 8 x 2048 took 84 us.) us of 4096 tokens of 8 x 2048 in bf16, and of the bytes at the copy rate: permute 24.8
-// (22.2), combine 32.9 (24.7), backward 54 (41.9): rows in the lists' order are read at 5.2 TB/s, and asking for the next
-// token's positions ahead changes nothing. Rows of 2046 take 28, 31 and 61; of 2047, which start at odd elements and are
-// read two bytes at a time, 38, 57 and 151.
+// tokens of 8 x 2048 took 84 us.) us of 4096 tokens of 8 x 2048 in bf16, and of the bytes at the copy rate: permute 21.6
+// (22.2), combine 27.9 (24.7), backward 50.7 (41.9): the gradients' reads and writes mixed reach 5.6 TB/s. Asking for the
+// next token's positions ahead changes nothing. Rows of 2046 take 25, 28 and 50; of 2047, which start at odd elements and
+// are read two bytes at a time, 36, 52 and 144.
 #include <type_traits>
 
 #include "common.cuh"
@@ -42,12 +42,27 @@ struct Piece {
     static constexpr int kWords = F32 ? 8 : V == 1 ? 8 : 4;      // bf16: pairs, or (V = 1) one a word
     uint32_t w[kWords];
 
+    // Rows that a call reads or writes once leave the caches first, but not where two accesses of a thread share a sector
+    // (us, 4096 tokens of 8 x 2048 in bf16, without / with: permute 24.8 / 21.6, combine 32.9 / 27.9, backward 53.9 / 50.7;
+    // of 4 x 2048 in fp32 backward 52.0 / 57.1).
+    static constexpr bool kOnce = !(F32 && V == 8);
+    template <bool ONCE, typename T>
+    static __device__ __forceinline__ T get_at(const T* p) {
+        if constexpr (ONCE) return __ldcs(p);
+        else return *p;
+    }
+    template <bool ONCE, typename T>
+    static __device__ __forceinline__ void put_at(T* p, T v) {
+        if constexpr (ONCE) __stcs(p, v);
+        else *p = v;
+    }
+    template <bool ONCE>                // kOnce or false
     __device__ __forceinline__ void load(const void* base, size_t row, int N, int unit) {
         if constexpr (V == 8) {
             const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + (row * N + unit * 8) * (F32 ? 4 : 2));
 #pragma unroll
             for (int i = 0; i < kWords / 4; ++i) {
-                const uint4 u = p[i];
+                const uint4 u = get_at<ONCE>(p + i);
                 w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
             }
         } else {
@@ -56,26 +71,30 @@ struct Piece {
                 const int c = column<V>(unit, i);
                 w[i] = 0u;
                 if (c < N) {
-                    if constexpr (F32) w[i] = static_cast<const uint32_t*>(base)[row * N + c];
-                    else if constexpr (V == 2) w[i] = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(base) + row * N + c);
-                    else w[i] = static_cast<const uint16_t*>(base)[row * N + c];
+                    const uint16_t* p = static_cast<const uint16_t*>(base) + row * N + c;       // bf16
+                    if constexpr (F32) w[i] = get_at<ONCE>(static_cast<const uint32_t*>(base) + row * N + c);
+                    else if constexpr (V == 2) w[i] = get_at<ONCE>(reinterpret_cast<const uint32_t*>(p));
+                    else w[i] = get_at<ONCE>(p);
                 }
             }
         }
     }
+    template <bool ONCE>
     __device__ __forceinline__ void store(void* base, size_t row, int N, int unit) const {
         if constexpr (V == 8) {
             uint4* p = reinterpret_cast<uint4*>(static_cast<uint8_t*>(base) + (row * N + unit * 8) * (F32 ? 4 : 2));
 #pragma unroll
-            for (int i = 0; i < kWords / 4; ++i) p[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            for (int i = 0; i < kWords / 4; ++i)
+                put_at<ONCE>(p + i, make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
         } else {
 #pragma unroll
             for (int i = 0; i < 8 / V; ++i) {
                 const int c = column<V>(unit, i);
                 if (c >= N) continue;
-                if constexpr (F32) static_cast<uint32_t*>(base)[row * N + c] = w[i];
-                else if constexpr (V == 2) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(base) + row * N + c) = w[i];
-                else static_cast<uint16_t*>(base)[row * N + c] = (uint16_t)w[i];
+                uint16_t* p = static_cast<uint16_t*>(base) + row * N + c;                       // bf16
+                if constexpr (F32) put_at<ONCE>(static_cast<uint32_t*>(base) + row * N + c, w[i]);
+                else if constexpr (V == 2) put_at<ONCE>(reinterpret_cast<uint32_t*>(p), w[i]);
+                else put_at<ONCE>(p, (uint16_t)w[i]);
             }
         }
     }
@@ -121,12 +140,12 @@ permute_kernel(const void* x, const int32_t* list, int R, int k, int N, void* ro
         Piece<F32, V> p[kTogether];
 #pragma unroll
         for (int i = 0; i < kTogether; ++i)
-            if (u0 + 32 * i < units) p[i].load(x, t, N, u0 + 32 * i);
+            if (u0 + 32 * i < units) p[i].template load<false>(x, t, N, u0 + 32 * i);
 #pragma unroll
         for (int i = 0; i < kTogether; ++i) {
             if (u0 + 32 * i >= units) break;
             p[i].keep(good);
-            p[i].store(rows, r, N, u0 + 32 * i);
+            p[i].template store<Piece<F32, V>::kOnce>(rows, r, N, u0 + 32 * i);
         }
     }
 }
@@ -159,7 +178,7 @@ combine_rows_kernel(const void* rows, const float* w, const int32_t* positions, 
     const size_t t = total >> 32 ? at / units : (size_t)((unsigned)at / units);
     const int unit = (int)(at - t * units);
     Piece<false, F32 || YF32 ? (V == 8 ? 8 : 1) : V> a;
-    if (add != nullptr) a.load(add, t, N, unit);
+    if (add != nullptr) a.template load<decltype(a)::kOnce>(add, t, N, unit);
     float acc[8] = {};
     for (int j0 = 0; j0 < k; j0 += KA) {
         int p[KA];
@@ -168,7 +187,7 @@ combine_rows_kernel(const void* rows, const float* w, const int32_t* positions, 
         Piece<F32, V> v[KA];
         find_entries<KA>(positions, w, t, j0, k, R, p, there, c);
 #pragma unroll
-        for (int j = 0; j < KA; ++j) v[j].load(rows, p[j], N, unit);
+        for (int j = 0; j < KA; ++j) v[j].template load<Piece<F32, V>::kOnce>(rows, p[j], N, unit);
 #pragma unroll
         for (int j = 0; j < KA; ++j) {
             v[j].keep(there[j]);
@@ -183,7 +202,7 @@ combine_rows_kernel(const void* rows, const float* w, const int32_t* positions, 
     }
     Piece<YF32, V> out;
     out.set(acc);
-    out.store(y, t, N, unit);
+    out.template store<false>(y, t, N, unit);
 }
 
 // One CTA a token.
@@ -204,11 +223,11 @@ combine_backward_kernel(const void* dy, const void* rows, const float* w, const 
         for (int j = 0; j < KA; ++j) part[j] = 0.f;
         for (int u = threadIdx.x; u < units; u += blockDim.x) {
             Piece<DYF32, V> gp;
-            gp.load(dy, t, N, u);
+            gp.template load<Piece<DYF32, V>::kOnce>(dy, t, N, u);
             if (d_w != nullptr) {
                 Piece<F32, V> v[KA];
 #pragma unroll
-                for (int j = 0; j < KA; ++j) v[j].load(rows, p[j], N, u);
+                for (int j = 0; j < KA; ++j) v[j].template load<Piece<F32, V>::kOnce>(rows, p[j], N, u);
 #pragma unroll
                 for (int j = 0; j < KA; ++j) {
                     v[j].keep(there[j]);
@@ -225,7 +244,7 @@ combine_backward_kernel(const void* dy, const void* rows, const float* w, const 
                     for (int i = 0; i < 8; ++i) g[i] = c[j] * gp.get(i);
                     Piece<F32, V> out;
                     out.set(g);
-                    out.store(d_rows, p[j], N, u);
+                    out.template store<Piece<F32, V>::kOnce>(d_rows, p[j], N, u);
                 }
         }
         if (d_w == nullptr) continue;
