@@ -250,7 +250,7 @@ struct Fp4Product {
 // tcgen05 tiles. Device us, stream / tiles, weights that are not in the L2: one row of 8192 x 2048 (8 MiB) 5.1 / 7.7,
 // 2048 x 8192 6.3 / 7.9, 1024 x 512 3.2 / 4.8; 8 rows of 8192 x 2048 5.8 / 7.5; 8 experts of 1024 x 2048 with a row each
 // 6.2 / 8.3; but 16384 x 2048 (16 MiB) with one row 9.2 / 9.2, with eight 9.5 / 8.1, and one row of 248320 x 2048
-// (243 MiB) 80 / 62: expanding codes to f16 costs the streaming kernel 3.6 TB/s.
+// (243 MiB) 80 / 59: expanding codes to f16 costs the streaming kernel 3.6 TB/s.
 constexpr long long kStreamBytes4 = 12ll << 20;
 cudaError_t launch_fp4_stream(const Fp4Product& P, const DeviceInfo& dev, cudaStream_t s);
 cudaError_t launch_rows_fp4(const Fp4Product& P, WsHeader* hdr, const DeviceInfo& dev, uint64_t wait_limit,
