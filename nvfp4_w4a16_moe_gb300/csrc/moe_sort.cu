@@ -248,6 +248,9 @@ combine_backward_kernel(const void* dy, const void* rows, const float* w, const 
                 }
         }
         if (d_w == nullptr) continue;
+        // a token's dy may hold infinities or NaN: no product of its entries without a row counts
+#pragma unroll
+        for (int j = 0; j < KA; ++j) part[j] = there[j] ? part[j] : 0.f;
         // KA sums over the lanes: each exchange of halves leaves a lane with half as many sums, the rest as usual
         int mine = 0;                  // which sum part[0] is in the end
 #pragma unroll

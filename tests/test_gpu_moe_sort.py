@@ -256,3 +256,29 @@ def test_rows_past_32_bits(nv):
     d_rows, d_w = nv.moe_combine_backward(x, rows, w, pos)
     assert torch.equal(d_w[-4:], (x[-4:].float() ** 2).sum(1, keepdim=True).expand(4, k))
     assert torch.equal(d_rows[:5], rows[:5] * 0.5) and torch.equal(d_rows[-8:], rows[-8:] * 0.5)
+
+
+@pytest.mark.parametrize("k,N", [(1, 64), (2, 250), (3, 257), (8, 2048), (11, 40)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_gradients_of_entries_that_are_not_there_beside_values_that_are_not_finite(nv, k, N, dtype, bad):
+    """d_w of an entry without a row is 0 whatever dy holds, and its row of d_rows is left alone."""
+    T = 5
+    g = _gen(k * N)
+    pos = torch.randperm(T * k, generator=g).to(torch.int32)
+    here = pos.clone()
+    for t, j, p in ((0, 0, -1), (2, k - 1, T * k), (3, k // 2, -(1 << 31)), (4, 0, (1 << 31) - 1)):
+        here[t * k + j] = p
+    w, rows = torch.randn(T, k, generator=g), torch.randn(T * k, N, generator=g).to(dtype)
+    for dy_type in (BF16, F32):
+        dy = torch.randn(T, N, generator=g).to(dy_type)
+        dy[:4, N // 3], dy[2, N - 1] = bad, -bad
+        d_rows = torch.full((T * k, N), 3.0, dtype=dtype, device="cuda")
+        _, d_w = nv.moe_combine_backward(dy.cuda(), rows.cuda(), w.cuda(), here.cuda(), d_rows=d_rows)
+        gone = ((here < 0) | (here >= T * k)).view(T, k)
+        got = d_w.cpu()
+        assert not got[gone].any() and not got[gone].isnan().any()
+        assert not got[:4][~gone[:4]].isfinite().any() and got[4][~gone[4]].isfinite().all()
+        left = torch.ones(T * k, dtype=torch.bool)
+        left[here[~gone.view(-1)].long()] = False
+        assert left.sum() == gone.sum() and (d_rows.cpu()[left] == 3).all()
