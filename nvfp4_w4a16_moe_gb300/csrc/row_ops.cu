@@ -83,6 +83,13 @@ __device__ __forceinline__ uint32_t absmax8(const float (&v)[8]) {
     return __float_as_uint(m) & 0x7FFFFFFFu;
 }
 
+// g / (1 + exp(-g)), for g < 0 as g exp(g) / (1 + exp(g)): exp(-g) passes fp32 from g = -88.7 down, where the quotient is
+// still a normal number to -92. Digits go with those of a subnormal exp(g), all of them below -104.
+__device__ __forceinline__ float silu(float g) {
+    const float e = __expf(-fabsf(g));
+    return __fdividef(g < 0.f ? g * e : g, 1.0f + e);
+}
+
 // Over the threads of a row; s: one word a warp. All threads of the CTA call it.
 __device__ __forceinline__ float row_sum(float v, int group, float* s) {
     const int warp = threadIdx.x >> 5, warps = group >> 5, first = warp / warps * warps;
@@ -148,7 +155,7 @@ rows_kernel(const RowParams P) {
             float up[8];
             in2[u].get(up);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] = v[u][i] * fast_rcp(1.0f + __expf(-v[u][i])) * up[i];
+            for (int i = 0; i < 8; ++i) v[u][i] = silu(v[u][i]) * up[i];
         }
     }
     if constexpr (norm) {

@@ -226,6 +226,38 @@ def test_swiglu(nv, kind, dtype, R, I):
     _check_rows(nv, kind, rows, ref.silu_up(d), err)
 
 
+@pytest.mark.parametrize("kind", [0, 1, 2])
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+def test_swiglu_of_gates_far_below_zero(nv, kind, dtype):
+    """exp(-g) passes fp32 at g = -88.7, silu(g) does not: with a large up the product is an ordinary number."""
+    I = 128
+    g = _gen(kind)
+    gate = torch.empty(9, I)
+    for r, (lo, hi) in enumerate(((-87, -80), (-88.7, -88), (-89.5, -88.7), (-91, -88.5), (-92, -90), (-92, -80), (-92, 5), (-60, -50),
+                                  (60, 90))):
+        gate[r] = lo + (hi - lo) * torch.rand(I, generator=g)
+    gate = gate.to(dtype)
+    silu = gate.double() * torch.sigmoid(gate.double())
+    up = (torch.randn(9, I, generator=g).double() / silu.abs()).clamp(-1e38, 1e38).to(dtype)
+    gu = torch.cat([gate, up], dim=1)
+    d = ref.f64(gu)
+    # the fast exponential is off by 2 + 1.173 |g| units of exp(-|g|), which are those of subnormals from |g| = 87.4 on;
+    # the division by 2 units of 2^-23; the sum and two products round (g exp(g) is a subnormal below -91.9)
+    unit = np.maximum(2.0 ** -23, 2.0 ** -149 * np.exp(np.abs(d[:, :I])))
+    err = (2 + 1.2 * np.abs(d[:, :I])) * unit + 2 * 2.0 ** -23 + 3 * 2.0 ** -24 + unit / 64
+    x = ref.silu_up(d)
+    assert (np.abs(x) > 2.0 ** -20).mean() > 0.99 and (d[:, :I] < -88.8).mean() > 0.3
+    _check_rows(nv, kind, nv.moe_swiglu(gu.cuda(), kind), x, err)
+
+
+def test_swiglu_of_gates_without_a_finite_value(nv):
+    inf, nan = float("inf"), float("nan")
+    gate, up = [inf, -inf, nan, 1e38, -1e38, -0.0, 0.0, 3.0], [2.0, 2.0, 2.0, 2.0, 2.0, 2.0, 2.0, inf]
+    got = nv.moe_swiglu(torch.tensor([gate + up], device="cuda"))[0].tolist()
+    assert got[0] == inf and np.isnan(got[1:3]).all() and got[3] == float(torch.tensor(2e38).to(BF16))
+    assert got[4:7] == [0.0, 0.0, 0.0] and got[7] == inf
+
+
 def test_swiglu_of_widths_that_only_some_kinds_take(nv):
     for kind, I in ((0, 8), (0, 1000), (1, 16), (1, 1136)):
         gu = torch.randn(5, 2 * I, generator=_gen(I)).to(BF16)
