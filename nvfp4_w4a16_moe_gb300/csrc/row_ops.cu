@@ -188,12 +188,10 @@ rows_kernel(const RowParams P) {
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
             if (!here || unit >= units) continue;
-            // the values are fp32 with errors of their own: 448 / a and a / 448 within 2^-22 do
-            const float a = __uint_as_float(m);
-            const bool tiny = a < kTinyAmax;
-            const float inv = m == 0u ? 1.0f : kE4m3Max * fast_rcp(tiny ? a * 0x1p64f : a);
-            if ((unit & 15) == 0) static_cast<float*>(P.out.scales)[row * KB + (unit >> 4)] = m == 0u ? 1.0f : a * (1.0f / kE4m3Max);
-            if (tiny)
+            // a / 448 and 448 / a as the quantiser of bf16 rows has them; the codes are those of fl32(x (448 / a))
+            const float inv = block_inverse(m);
+            if ((unit & 15) == 0) static_cast<float*>(P.out.scales)[row * KB + (unit >> 4)] = block_scale(m);
+            if (__uint_as_float(m) < kTinyAmax)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[u][i] *= 0x1p64f;
 #pragma unroll

@@ -166,6 +166,32 @@ def test_norm_of_widths_that_only_some_kinds_take(nv, kind, H):
     _check_rows(nv, kind, rows, x, _norm_error(H))
 
 
+@pytest.mark.parametrize("H", [16, 128, 1008, 2048, 5120, 20480])
+def test_e4m3_scales_of_rows_known_to_the_bit(nv, H):
+    """Rows whose mean square is a power of four and gates whose sigmoid is 1 give fp32 values without a rounding: the
+    scales are a / 448 rounded once, as fp8_quantize_block128's, and the codes off by the roundings of 448 / a and of one
+    product at most."""
+    T = 12
+    g = _gen(H)
+    sign = torch.randint(0, 2, (T, H), generator=g) * 2.0 - 1.0
+    power = torch.pow(2.0, torch.randint(-12, 13, (T, 1), generator=g).float())
+    w = (torch.randn(H, generator=g) * 0.5).to(BF16).float()
+    w = torch.where((w.abs() < 2.0 ** -14) | (w < -0.99), torch.zeros(()), w)       # 1 + w is exact
+    x = ref.f64(sign) * (1.0 + ref.f64(w))
+    _, (q, s) = nv.rmsnorm_residual((sign * power).to(BF16).cuda(), w.to(BF16).cuda(), 0.0, kind=nv.ROWS_FP8)
+    gates = torch.pow(2.0, torch.randint(7, 10, (T, H), generator=g).float())       # exp(-128) is no part of 1 + exp(-128)
+    up = torch.randn(T, H, generator=g).to(BF16).float() * power
+    x2 = ref.f64(gates) * ref.f64(up)
+    q2, s2 = nv.moe_swiglu(torch.cat([gates, up], dim=1).to(BF16).cuda(), nv.ROWS_FP8)
+    for codes, scales, want in ((q, s, x), (q2, s2, x2)):
+        for j in range(scales.shape[1]):
+            a = np.abs(want[:, j * 128:(j + 1) * 128]).max(axis=1).astype(np.float32)
+            assert np.array_equal(_np(scales)[:, j], a / np.float32(448.0))
+        ref.check_fp8(_np(codes.view(torch.uint8)), _np(scales).astype(np.float64), want, 0.0)
+    back, sb = nv.fp8_quantize_block128(torch.from_numpy(x2).to(BF16).cuda())
+    assert torch.equal(sb, s2)
+
+
 def test_norm_in_place_and_copies(nv):
     g = _gen(8)
     h, d = (torch.randn(33, 2048, generator=g).to(BF16).cuda() for _ in range(2))
