@@ -150,9 +150,10 @@ __device__ __forceinline__ uint32_t nvfp4_idesc(int N) {
 }
 
 // A warp that puts the scales of 128 rows (blk 0: of W, then of x) of two steps after two steps into line order, in place,
-// from the sectors that copies brought, row after row.
+// from the sectors that copies brought, row after row. ready: barriers of the pair's first CTA, whose copies into tensor
+// memory read both CTAs' lines.
 template <typename C>
-__device__ __forceinline__ void scale_warp(int count, int blk, uint8_t* slots, uint64_t* raw, uint64_t* ready,
+__device__ __forceinline__ void scale_warp(int count, int blk, uint8_t* slots, uint64_t* raw, uint32_t ready,
                                            const Waiter& wait) {
     const int lane = threadIdx.x & 31;
     int slot = 0;
@@ -177,8 +178,9 @@ __device__ __forceinline__ void scale_warp(int count, int blk, uint8_t* slots, u
 #pragma unroll
         for (int k = 0; k < 8; ++k) to[32 * k] = make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
         fence_proxy_async_smem();
+        fence_release_smem();
         __syncwarp();
-        if (elect_one()) mbar_arrive(&ready[slot]);
+        if (elect_one()) arrive_cluster_fenced(ready + 8 * slot);
         if (++slot == C::kSlots) slot = 0, par ^= 1u;
     }
 }
@@ -216,7 +218,7 @@ struct OddCopies {
 // they make no 2^lg, lie behind the map's end (zeros): the warp loads them itself.
 template <typename C>
 __device__ __forceinline__ void odd_scale_warp(const Fp4Product& Q, WalkOf<C::kRound> at, int pairs, int m_begin, int blk,
-                                               int rank, uint8_t* slots, uint64_t* raw, uint64_t* ready, const Waiter& wait) {
+                                               int rank, uint8_t* slots, uint64_t* raw, uint32_t ready, const Waiter& wait) {
     const RowsProduct& P = Q.r;
     const int lane = threadIdx.x & 31, KB = P.K / 16, l0 = (blk - 1) * 128;
     const uint8_t* base = blk == 0 ? Q.ws : Q.xs;
@@ -292,8 +294,9 @@ __device__ __forceinline__ void odd_scale_warp(const Fp4Product& Q, WalkOf<C::kR
 #pragma unroll
             for (int k = 0; k < 8; ++k) to[32 * k] = make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
             fence_proxy_async_smem();
+            fence_release_smem();
             __syncwarp();
-            if (elect_one()) mbar_arrive(&ready[slot]);
+            if (elect_one()) arrive_cluster_fenced(ready + 8 * slot);
             if (++slot == C::kSlots) slot = 0, par ^= 1u;
         }
     }
@@ -393,7 +396,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
     uint64_t* acc_full = empty + C::kStages;                           // tensor-memory buffer summed
     uint64_t* acc_empty = acc_full + C::kBufs;                         // first CTA: ... and read in both
     uint64_t* sf_raw = acc_empty + C::kBufs;                           // scales of two steps landed
-    uint64_t* sf_ready = sf_raw + C::kSlots;                           // ... and are in line order
+    uint64_t* sf_ready = sf_raw + C::kSlots;                           // first CTA: ... and are in line order in both
     uint64_t* sf_empty = sf_ready + C::kSlots;                         // ... and copied to tensor memory
     uint64_t* ends_full = sf_empty + C::kSlots;                        // scales and rows of a tile's outputs
     uint64_t* ends_empty = ends_full + C::kEnds;                       // ... and read
@@ -416,7 +419,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
             }
             for (int i = 0; i < C::kSlots; ++i) {
                 mbar_init(&sf_raw[i], !ODD ? 1 : P.gather ? 1 + 32 * kGatherWarps : C::kBlocks);
-                mbar_init(&sf_ready[i], C::kBlocks);
+                mbar_init(&sf_ready[i], 2 * C::kBlocks);
                 mbar_init(&sf_empty[i], 1);
             }
             for (int i = 0; i < C::kEnds; ++i) {
@@ -534,7 +537,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                     uint32_t idesc = 0;
 #pragma unroll 1
                     for (int s = s_begin; s < s_end; ++s) {
-                        if (s == s_begin || (s & 1) == 0) ok = wait.one(&sf_ready[sl], sl_par);
+                        if (rank == 0 && (s == s_begin || (s & 1) == 0)) ok = wait.one<true>(&sf_ready[sl], sl_par);
                         if (ok) ok = wait.one(&full[st], st_par);
                         if (!ok) break;
                         const bool sl_done = (s & 1) != 0 || s == s_end - 1;
@@ -707,8 +710,9 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
         } else {
             const int blk = warp - kScaleWarp0;
             uint8_t* slots = sm + C::kOffSlots;
-            if constexpr (ODD) odd_scale_warp<C>(Q, tiles, m_pairs, m_begin, blk, rank, slots, sf_raw, sf_ready, wait);
-            else scale_warp<C>(tiles_here * m_pairs, blk, slots, sf_raw, sf_ready, wait);
+            const uint32_t ready = map_rank(su32(sf_ready), first_rank);
+            if constexpr (ODD) odd_scale_warp<C>(Q, tiles, m_pairs, m_begin, blk, rank, slots, sf_raw, ready, wait);
+            else scale_warp<C>(tiles_here * m_pairs, blk, slots, sf_raw, ready, wait);
         }
         if (SPLITS > 1 && tiles.more()) exchange.join();
     } else {

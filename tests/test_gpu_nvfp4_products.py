@@ -399,6 +399,23 @@ def test_a_wait_that_runs_out_is_reported(nv, T, N, K, rows):
         _check_exact(y, want, dtype)
 
 
+@pytest.mark.parametrize("T,N,K,rows", [(300, 1030, 4096, "list"), (300, 1030, 4064, "list"), (700, 600, 2048, "gather"),
+                                        (700, 600, 2080, "gather"), (100, 513, 8192, "list")])
+def test_scales_that_change_from_call_to_call(nv, T, N, K, rows):
+    """The same buffers with other block scales, call behind call: both CTAs of a pair multiply by this call's."""
+    a, xd, wd, off, lst, R = _case(T, 1, 1, N, K, "one", rows, 1, T)
+    want = torch.from_numpy(_want(a, xd, wd, off, lst, R)[0]).float().cuda()
+    xs, ws = a["x_scales"].clone(), a["w_scales"].clone()
+    ys = [torch.zeros(R, N, device="cuda") for _ in range(12)]
+    for i, y in enumerate(ys):
+        for t, s, step in ((a["x_scales"], xs, 8 * (i % 4)), (a["w_scales"], ws, 8 * (i // 4))):      # codes of twice the scale
+            t.copy_(s)
+            t.add_(step)
+        nv.moe_grouped_gemm_nvfp4(**a, y=y)
+    for i, y in enumerate(ys):
+        assert torch.equal(y, want * 2.0 ** (i % 4 + i // 4))
+
+
 @pytest.mark.parametrize("limit", [200, 2000, 20000])
 def test_waits_that_may_run_out(nv, limit):
     """Limits around what the waits take: the status and the NaN go together, whatever has finished is right, and

@@ -215,3 +215,24 @@ def test_sizes_past_32_bits_are_refused(nv, N):  # noqa: F811
                  lambda: nv.nvfp4_dequantize_rows(Operand((4, N), U8), Operand((4, N // 8), U8), x[2], y=y),
                  lambda: nv.moe_combine(Operand((4, N), BF16), 2, y=y)):
         _refused(nv, call, nv.NVFP4_ERR_UNSUPPORTED_SHAPE)
+
+
+def test_scales_cross_a_pair_of_ctas_at_its_scope():
+    """The first CTA of a pair reads scales that the second one's warps stored: the arrival that hands them over releases to
+    the cluster, and the wait for it acquires from there. (An order that only the source can show.)"""
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "nvfp4_w4a16_moe_gb300", "csrc")
+    with open(os.path.join(csrc, "pair_tc.cuh")) as f:
+        pair = f.read()
+    with open(os.path.join(csrc, "rows_fp4.cu")) as f:
+        kernel = f.read()
+    body = lambda name: re.search(r"\b%s\(.*?\n}" % name, pair, re.S).group(0)  # noqa: E731
+    assert "fence.release.sync_restrict::shared::cta.cluster" in body("fence_release_smem")
+    assert "mbarrier.arrive.relaxed.cluster.shared::cluster.b64" in body("arrive_cluster_fenced")
+    for name in ("test", "try"):
+        assert "mbarrier.%s_wait.parity.acquire.cluster.shared::cta.b64" % name in body("mbar_%s_wait_cluster" % name)
+    stores = re.findall(r"fence_proxy_async_smem\(\);\s*(\S+)\s*__syncwarp\(\);\s*if \(elect_one\(\)\) (\w+)\(", kernel)
+    assert stores == [("fence_release_smem();", "arrive_cluster_fenced")] * 2      # rows of scales that are strides, and others
+    assert kernel.count("fence_proxy_async_smem()") == 2
+    assert re.findall(r"wait\.one(\S*)\(&sf_ready\[", kernel) == ["<true>"]
