@@ -15,7 +15,7 @@
 //     in another order is needed. Rows whose scales are no multiple of 16 bytes
 //     (K is none of 256) are no strides of a tensor map; two, four or eight of them together are (OddCopies): 48 bytes of
 //     each, out of which the same warp takes its 32. (That warp loading them from global memory: 4096 x 8192 x 2016 in 76
-//     us, rows gathered for 256 experts in 190; now 44 and 98.) Behind the end of K the scales are 0, so neither the codes
+//     us, rows gathered for 256 experts in 190; now 58 and 99.) Behind the end of K the scales are 0, so neither the codes
 //     nor NaN scales that lie there count.
 //   The MMA thread copies a step's scales from the ring to tensor memory (tcgen05.cp, to all four lane quarters), right
 //     before the step's MMAs: the tensor pipe runs copies and MMAs of one thread in the order of issue.
@@ -95,7 +95,7 @@ struct Cfg {
 
 struct Fp4Maps {
     CUtensorMap w, x;      // x: boxes of kBoxRows rows, or of one to gather
-    CUtensorMap ws, xs;    // block scales of two steps (encode_scales, encode_odd_scales); xs to gather: of one row
+    CUtensorMap ws, xs;    // block scales of two steps (encode_scales, encode_odd_scales); xs is not read to gather
 };
 
 // D (256 x N over both CTAs) = A B^T of 64 columns, scaled by 4 E4M3 scales a row, plus D where accumulate.
@@ -105,22 +105,6 @@ __device__ __forceinline__ void mma_nvfp4(uint32_t d, uint64_t a, uint64_t b, ui
         "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
         " tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}"
         :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
-}
-// tma_load_2d and tma_gather4 into the same place of every CTA of the mask, each of whose barriers counts the bytes.
-__device__ __forceinline__ void tma_load_2d_to(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
-                                               uint16_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
-        "[%0], [%1, {%2, %3}], [%4], %5;"
-        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(su32(bar)), "h"(mask) : "memory");
-}
-__device__ __forceinline__ void tma_gather4_to(uint32_t dst, const CUtensorMap* map, int x, int r0, int r1, int r2, int r3,
-                                               uint64_t* bar, uint16_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.multicast::cluster "
-        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;"
-        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(su32(bar)), "h"(mask)
-        : "memory");
 }
 // tma_load_2d with a cache policy: what leaves the L2 first, or as usual.
 __device__ __forceinline__ uint64_t l2_policy(bool first) {
@@ -202,15 +186,6 @@ struct OddCopies {
 #pragma unroll
         for (int c = 0; c < 8; ++c)
             if (c < 1 << lg) tma_load_2d(to + c * ((kM >> lg) * kOddBytes), map, x[c] + byte, y[c], bar);
-    }
-    // Half of the copies, into both CTAs of a pair: the other one brings the rest. (Each CTA bringing all: 4096 x 8192 x
-    // 2016 in 52 us, now 44. Scales whose rows are strides gain nothing by it.)
-    __device__ __forceinline__ void bring_half(uint32_t to, const CUtensorMap* map, int byte, uint64_t* bar, int rank,
-                                               uint16_t mask) const {
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            if (c < 1 << lg && (c & 1) == rank)
-                tma_load_2d_to(to + c * ((kM >> lg) * kOddBytes), map, x[c] + byte, y[c], bar, mask);
     }
 };
 
@@ -418,7 +393,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                 mbar_init(&acc_empty[i], 2 * kEpiWarps);
             }
             for (int i = 0; i < C::kSlots; ++i) {
-                mbar_init(&sf_raw[i], !ODD ? 1 : P.gather ? 1 + 32 * kGatherWarps : C::kBlocks);
+                mbar_init(&sf_raw[i], P.gather ? 1 + 32 * kGatherWarps : ODD ? C::kBlocks : 1);
                 mbar_init(&sf_ready[i], 2 * C::kBlocks);
                 mbar_init(&sf_empty[i], 1);
             }
@@ -500,7 +475,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                                 odd.bring(to, &maps.ws, (s >> 1) * kSectorBytes, &sf_raw[sl]);
                             }
                         } else if (elect_one()) {
-                            mbar_arrive_expect_tx(&sf_raw[sl], C::kBlkBytes + (P.gather ? 2 * share : NT) * kSectorBytes);
+                            mbar_arrive_expect_tx(&sf_raw[sl], C::kBlkBytes + (P.gather ? 0 : NT * kSectorBytes));
                             tma_load_2d(to, &maps.ws, (s >> 1) * kSectorBytes, wy, &sf_raw[sl]);
                             if (!P.gather) tma_load_2d(to + C::kBlkBytes, &maps.xs, (s >> 1) * kSectorBytes, t.r0, &sf_raw[sl]);
                         }
@@ -590,9 +565,9 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                 // row r of this warp's copy j
                 constexpr int kPer = (NT / 2 / 4 + kGatherWarps - 1) / kGatherWarps;
                 const int w = warp - kGatherWarp0;
-                // Scales, ODD: of all columns, 16 bytes a lane, neighbours first the pieces of a row. Otherwise the same copies
-                // bring those of the CTA's own columns into both.
-                constexpr int kPieces = kOddBytes / 16, kSfPer = ODD ? (NT * kPieces + 127) / 128 : 0;
+                // and the scales of all columns, 16 bytes a lane, neighbours first the pieces of a row (by copies of four rows, 32
+                // bytes of each, they cost as much as rows of 128)
+                constexpr int kPieces = C::kRowBytes / 16, kSfPer = (NT * kPieces + 127) / 128;
                 const auto sf_row = [&](int i) { return (32 * w + lane + 128 * i) / kPieces; };
                 const auto sf_piece = [&](int i) { return (32 * w + lane + 128 * i) % kPieces; };
                 const size_t sf_bytes = (size_t)P.x_rows * KB;
@@ -618,7 +593,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                     const auto row_of = [&](int e, int col) { return col < n && (unsigned)e < (unsigned)P.R ? e / P.k : -1; };
                     int src = row_of(entry[0], l < share ? rank * share + l : n);
                     if (src < 0) src = P.x_rows;                     // past the last row: zeros
-                    int sf_src[kSfPer + 1];
+                    int sf_src[kSfPer];
 #pragma unroll
                     for (int i = 0; i < kSfPer; ++i) sf_src[i] = row_of(entry[1 + i], sf_row(i));
                     at.next();
@@ -636,29 +611,24 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                             if (u > 0) ok = wait(&sf_empty[sl], (u - 1) & 1);
                             if (!ok) break;
                             const uint32_t to = sm_base + C::kOffSlots + sl * C::kSlotBytes + C::kBlkBytes;
-                            if constexpr (ODD) {       // as odd_scale_warp wants them; the array may end in a piece
 #pragma unroll
-                                for (int i = 0; i < kSfPer; ++i) {
-                                    const int l = sf_row(i), piece = sf_piece(i);
-                                    if (l >= NT) break;
-                                    const size_t from = ((size_t)max(sf_src[i], 0) * KB & ~(size_t)15) +
-                                                        (s >> 1) * kSectorBytes + 16 * piece;
+                            for (int i = 0; i < kSfPer; ++i) {
+                                const int l = sf_row(i), piece = sf_piece(i), byte = (s >> 1) * kSectorBytes + 16 * piece;
+                                if (l >= NT) break;
+                                size_t from = (size_t)max(sf_src[i], 0) * KB;
+                                if constexpr (ODD) {           // as odd_scale_warp wants them; the array may end in a piece
+                                    from = (from & ~(size_t)15) + byte;
                                     const int left = from < sf_bytes ? (int)min(sf_bytes - from, (size_t)16) : 0;
                                     const int there = sf_src[i] >= 0 ? left : 0;
                                     cp_async16_zfill(to + (l >> 7) * C::kBlkBytes + odd_place(l & 127, lg) + 16 * piece,
                                                      Q.xs + (there > 0 ? from : 0), there);
-                                }
-                                cp_async_arrive_noinc(&sf_raw[sl]);
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < kPer; ++j) {
-                                    if (j >= mine) break;
-                                    if (elect_one())
-                                        tma_gather4_to(to + (rank * share + 4 * (w + kGatherWarps * j)) * kSectorBytes, &maps.xs,
-                                                       (s >> 1) * kSectorBytes, rows4[j][0], rows4[j][1], rows4[j][2], rows4[j][3],
-                                                       &sf_raw[sl], pair_mask);
+                                } else {                       // in the order of the 32-byte swizzle (scale_warp)
+                                    const bool there = sf_src[i] >= 0 && byte < KB;
+                                    cp_async16_zfill(to + l * kSectorBytes + 16 * (piece ^ ((l >> 2) & 1)),
+                                                     Q.xs + (there ? from + byte : 0), there ? 16 : 0);
                                 }
                             }
+                            cp_async_arrive_noinc(&sf_raw[sl]);
                             ++two;
                         }
                         const int st = step % C::kStages, u = step / C::kStages;
@@ -681,9 +651,7 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                     drain_scales(two);
                 }
             } else if (const int blk = warp - kGatherWarp0; ODD && blk < C::kBlocks) {
-                // these warps bring the scales (24 copies of the TMA warp's, in one go, held up those of its operands). The other
-                // CTA's copies may land before this one's bytes are expected, but not before the slot is free: MMAs of both
-                // CTAs' slots are done together.
+                // these warps bring the scales (24 copies of the TMA warp's, in one go, held up those of its operands)
                 int two = 0;
                 bool ok = true;
 #pragma unroll 1
@@ -698,10 +666,8 @@ rows_fp4_kernel(const Fp4Product Q, const __grid_constant__ Fp4Maps maps, int m_
                         if (!ok) break;
                         if (elect_one()) {
                             mbar_arrive_expect_tx(&sf_raw[sl], (blk == 0 ? kM : C::kXRows) * kOddBytes);
-                            const uint32_t to = sm_base + C::kOffSlots + sl * C::kSlotBytes + blk * C::kBlkBytes;
-                            const int byte = (m_begin + j) * kSectorBytes;
-                            if (blk == 0) odd.bring(to, &maps.ws, byte, &sf_raw[sl]);
-                            else odd.bring_half(to, &maps.xs, byte, &sf_raw[sl], rank, pair_mask);
+                            odd.bring(sm_base + C::kOffSlots + sl * C::kSlotBytes + blk * C::kBlkBytes,
+                                      blk == 0 ? &maps.ws : &maps.xs, (m_begin + j) * kSectorBytes, &sf_raw[sl]);
                         }
                     }
                 }
@@ -1033,10 +999,10 @@ cudaError_t launch(const Fp4Product& P, WsHeader* hdr, const DeviceInfo& dev, ui
     cudaError_t e;
     if ((e = plan_tiles<64, ODD>(P.r, dev, &plan)) != cudaSuccess) return e;
     if ((e = plan_tiles<128, ODD>(P.r, dev, &plan)) != cudaSuccess) return e;
-    // Gathered rows cost the widest tiles more, the fewer an expert has and where all of a tile's scales come in pieces (us,
-    // 128 / 224 columns, 1024 outputs: K = 2048, 94 rows to an expert 64.7 / 65.7, 128: 73.3 / 72.0, 512: 53.6 / 47.7;
-    // K = 2016, 128 rows 97 / 109, 256: 82.6 / 83.1, 512: 43.5 / 42.0).
-    if ((!P.r.gather || rows >= (ODD ? 256 : 128)) && (e = plan_tiles<224, ODD>(P.r, dev, &plan)) != cudaSuccess) return e;
+    // Gathered rows cost the widest tiles more, all of whose scales come in pieces, unless an expert has many (us, 128 / 224
+    // columns, 1024 outputs: K = 2048, 94 rows to an expert 61 / 69, 256: 62 / 68, 512: 57 / 59, 4096: 51 / 48; K = 2016,
+    // 94 rows 71 / 88, 256: 86 / 91, 512: 79 / 77, 4096: 74 / 64).
+    if ((!P.r.gather || rows >= 512) && (e = plan_tiles<224, ODD>(P.r, dev, &plan)) != cudaSuccess) return e;
     if (plan.tiles > kMaxTiles) return cudaErrorInvalidConfiguration;
     if (plan.nt == 64) return launch_tiles<64, ODD>(P, plan, hdr, dev, wait_limit, s);
     if (plan.nt == 128) return launch_tiles<128, ODD>(P, plan, hdr, dev, wait_limit, s);

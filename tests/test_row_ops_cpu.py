@@ -236,3 +236,21 @@ def test_scales_cross_a_pair_of_ctas_at_its_scope():
     assert stores == [("fence_release_smem();", "arrive_cluster_fenced")] * 2      # rows of scales that are strides, and others
     assert kernel.count("fence_proxy_async_smem()") == 2
     assert re.findall(r"wait\.one(\S*)\(&sf_ready\[", kernel) == ["<true>"]
+
+
+def test_copies_go_to_one_cta():
+    """Ranks of several GPUs load the library, and loads that a cluster's CTAs share are for one GPU's own memory alone: no
+    copy from memory names more than one CTA. (What does are the tensor cores' arrivals on barriers.)"""
+    import glob
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    sources = glob.glob(os.path.join(root, "nvfp4_w4a16_moe_gb300", "csrc", "*.cu*")) + [os.path.join(root, "include", "nvfp4moe.h")]
+    assert len(sources) > 10
+    for path in sources:
+        with open(path) as f:
+            text = re.sub(r'"\s*\n\s*"', "", f.read())       # instructions in several literals
+        for literal in re.findall(r'"([^"\n]*multicast[^"\n]*)"', text):
+            for instruction in literal.split(";"):
+                if "multicast" in instruction:
+                    assert instruction.strip().startswith("tcgen05.commit."), (os.path.basename(path), instruction)
