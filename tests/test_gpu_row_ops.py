@@ -345,3 +345,16 @@ def test_rows_past_32_bits(nv):
     assert torch.equal(q[-3:].view(torch.uint8), qt.view(torch.uint8)) and torch.equal(s[-3:], st)
     del q, s
     assert torch.equal(nv.moe_swiglu(x)[-3:], nv.moe_swiglu(tail))
+
+
+def test_all_three_arrays_of_rows_past_32_bits(nv):
+    """2.3e9 elements, rows of zeros but for the last three: codes, block scales and row scales of each are where they should
+    be, and 1 and zeros everywhere else."""
+    R, K = 70001, 32768
+    x = torch.zeros(R, K, dtype=BF16, device="cuda")
+    tail = (torch.randn(3, K, generator=_gen(1)) * 8).to(BF16).cuda()
+    x[-3:] = tail
+    packed, scales, rs = nv.nvfp4_quantize_rows(x)
+    want = nv.nvfp4_quantize_rows(tail)
+    assert torch.equal(packed[-3:], want[0]) and torch.equal(scales[-3:], want[1]) and torch.equal(rs[-3:], want[2])
+    assert (want[2] < 0.1).all() and (rs[:-3] == 1).all() and not packed[:-3].any() and not scales[:-3].any()
