@@ -44,14 +44,12 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
 }
-// Arrivals that hand plain stores to this CTA's shared memory to a thread of either CTA, which waits at the scope of the
-// cluster: the threads that stored fence first, one of them arrives then. The fence is the release, of shared memory alone
-// (one that waits for global memory too, at every arrival of NVFP4 scales: 4096 x 8192 x 2048 in 45 us for 33).
-__device__ __forceinline__ void fence_release_smem() {
-    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
-}
-__device__ __forceinline__ void arrive_cluster_fenced(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
+// The same where it hands plain stores to this CTA's shared memory, its own and those of the lanes it has met since, to a
+// thread of either CTA that waits at the scope of the cluster. The release is of shared memory alone (one that waits for
+// global memory too, at every arrival of NVFP4 scales: 4096 x 8192 x 2048 in 45 us for 33).
+__device__ __forceinline__ void arrive_cluster_release_smem(uint32_t cluster_addr) {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;\n"
+                 " mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
 }
 
 // One look at a barrier's phase, without suspending the thread.

@@ -162,9 +162,8 @@ __device__ __forceinline__ void scale_warp(int count, int blk, uint8_t* slots, u
 #pragma unroll
         for (int k = 0; k < 8; ++k) to[32 * k] = make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
         fence_proxy_async_smem();
-        fence_release_smem();
         __syncwarp();
-        if (elect_one()) arrive_cluster_fenced(ready + 8 * slot);
+        if (elect_one()) arrive_cluster_release_smem(ready + 8 * slot);
         if (++slot == C::kSlots) slot = 0, par ^= 1u;
     }
 }
@@ -269,9 +268,8 @@ __device__ __forceinline__ void odd_scale_warp(const Fp4Product& Q, WalkOf<C::kR
 #pragma unroll
             for (int k = 0; k < 8; ++k) to[32 * k] = make_uint4(w[0][k], w[1][k], w[2][k], w[3][k]);
             fence_proxy_async_smem();
-            fence_release_smem();
             __syncwarp();
-            if (elect_one()) arrive_cluster_fenced(ready + 8 * slot);
+            if (elect_one()) arrive_cluster_release_smem(ready + 8 * slot);
             if (++slot == C::kSlots) slot = 0, par ^= 1u;
         }
     }

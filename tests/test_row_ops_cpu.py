@@ -228,12 +228,12 @@ def test_scales_cross_a_pair_of_ctas_at_its_scope():
     with open(os.path.join(csrc, "rows_fp4.cu")) as f:
         kernel = f.read()
     body = lambda name: re.search(r"\b%s\(.*?\n}" % name, pair, re.S).group(0)  # noqa: E731
-    assert "fence.release.sync_restrict::shared::cta.cluster" in body("fence_release_smem")
-    assert "mbarrier.arrive.relaxed.cluster.shared::cluster.b64" in body("arrive_cluster_fenced")
+    release = body("arrive_cluster_release_smem")
+    assert 0 < release.index("fence.release.sync_restrict::shared::cta.cluster") < release.index("mbarrier.arrive.relaxed.cluster.shared::cluster.b64")
     for name in ("test", "try"):
         assert "mbarrier.%s_wait.parity.acquire.cluster.shared::cta.b64" % name in body("mbar_%s_wait_cluster" % name)
-    stores = re.findall(r"fence_proxy_async_smem\(\);\s*(\S+)\s*__syncwarp\(\);\s*if \(elect_one\(\)\) (\w+)\(", kernel)
-    assert stores == [("fence_release_smem();", "arrive_cluster_fenced")] * 2      # rows of scales that are strides, and others
+    arrivals = re.findall(r"fence_proxy_async_smem\(\);\s*__syncwarp\(\);\s*if \(elect_one\(\)\) (\w+)\(", kernel)
+    assert arrivals == ["arrive_cluster_release_smem"] * 2      # rows of scales that are strides, and others
     assert kernel.count("fence_proxy_async_smem()") == 2
     assert re.findall(r"wait\.one(\S*)\(&sf_ready\[", kernel) == ["<true>"]
 
