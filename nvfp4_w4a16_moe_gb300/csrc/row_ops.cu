@@ -12,9 +12,10 @@
 //
 // Bound: HBM, 2 to 8 bytes read and 0.56 to 4 written per element; from launch to the first bytes pass some 1.5 us (5 x
 // 1000 takes 1.6). us of 4096 x 2048 / 65536 x 2048, and of the latter's bytes at the copy rate (6.8 TB/s): norm with
-// delta to bf16 12.2 / 156 (158), to E4M3 12.2 / 151 (139), to NVFP4 12.0 / 150 (129); SwiGLU 8.5 / 117 (118), 10.1 / 128
-// (99), 10.0 / 124 (90); quantise 6.6 / 73 (51); back 5.6 / 68 (51). Where rows end in 4 bits the arithmetic of the
-// blocks (a maximum, a scale and its reciprocal, 16 codes) takes what is left to the bytes' time.
+// delta to bf16 11.8 / 155 (158), to E4M3 12.4 / 152 (139), to NVFP4 11.8 / 148 (129); SwiGLU 7.7 / 114 (118), 9.6 / 122
+// (99), 9.9 / 126 (90); quantise 6.6 / 72 (51); back 5.6 / 68 (51). Where rows end in 4 bits the instructions of the blocks
+// (a maximum, a scale and its reciprocal, 16 codes) bound it: 81 % of the issue slots and 77 % of the integer pipe are
+// used in the quantiser, 79 % and 62 % in the SwiGLU.
 #include "common.cuh"
 #include "kernels.cuh"
 #include "quant.cuh"
@@ -243,16 +244,16 @@ cudaError_t launch_u(RowParams P, cudaStream_t s) {
     return launch_pdl(rows_kernel<SRC, OUT, U>, (unsigned)(((long long)P.R + per - 1) / per), threads, 0, s, P);
 }
 
-// Up to 1024 columns: a warp a row, no barriers. More: four units a thread, but two where a norm's sum stands between
-// reading and writing (us, two / four units a thread: norm of 65536 x 2048 into bf16 155 / 158, E4M3 149 / 160, NVFP4
-// 150 / 146; SwiGLU 127 / 116, 125 / 128, 134 / 123; quantiser 85 / 72; norm of 7 x 1056 1.6 / 1.8). The rule goes by the
-// columns alone, so that a row's sum does not depend on how many rows there are.
+// Up to 1024 columns: a warp a row, no barriers. More: four units a thread in the quantiser, two where a norm's sum stands
+// between reading and writing or an exponential is to be taken (us, two / four units a thread: quantiser of 65536 x 2048
+// 85 / 72; norm of it into bf16 154 / 156, E4M3 153 / 168, NVFP4 149 / 145; SwiGLU 114 / 114, 122 / 125, 126 / 125; 7 x 1056
+// norm 1.6 / 1.8, SwiGLU into E4M3 1.6 / 2.3). The rule goes by the columns alone, so that a row's sum does not depend on
+// how many rows there are.
 template <int SRC, int OUT>
 cudaError_t launch_rows(const RowParams& P, cudaStream_t s) {
     const int units = P.K >> 3;
-    constexpr bool norm = SRC == kNorm || SRC == kNormDelta;
     if (units <= 32) return launch_u<SRC, OUT, 1>(P, s);
-    if (units <= (norm ? 2 * kRowThreads : 64)) return launch_u<SRC, OUT, 2>(P, s);
+    if (units <= (SRC == kPlain ? 64 : 2 * kRowThreads)) return launch_u<SRC, OUT, 2>(P, s);
     if (units <= NVFP4_MAX_ROW_K / 16) return launch_u<SRC, OUT, 4>(P, s);
     return launch_u<SRC, OUT, 8>(P, s);
 }
