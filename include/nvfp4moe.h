@@ -444,8 +444,11 @@ NVFP4_API nvfp4_status nvfp4_dequantize_rows(const uint8_t* packed, const uint8_
  * rmsnorm_residual - the residual add and the (1 + w) RMSNorm in front of a layer made of the products:
  *   h_out = bf16(h + delta)            (h itself without delta)
  *   x     = h_out / sqrt(mean_i h_out[t,i]^2 + eps) * (1 + norm_w)
- *   with x written once, in the form that out says: rounded to bf16, or quantised from its fp32 value as
- *   fp8_quantize_block128 and nvfp4_quantize_rows say (their nearest values, decided in fp32 here).
+ *   with x written once, in the form that out says: rounded to bf16, or quantised from its fp32 value, which has
+ *   roundings of its own, as fp8_quantize_block128 and nvfp4_quantize_rows say. Scales of 8-bit blocks are a / 448
+ *   rounded once; a code whose quotient is within 2^-22 of a rounding point may be either neighbour (8 bits: the
+ *   quotient is x times the rounded 448 / a; NVFP4: x times an approximate reciprocal of e s).
+ *   The squares are summed in fp32: the sum has to stay below 2^128 (with values of up to 2^56 it does).
  *   Defined by: as moe_layer_forward_residual's norm (tutorials index, row 01; write-up, "Fused Kernels").
  *   h      bf16 [T, H] device;  delta  bf16 [T, H] device or NULL;  norm_w  bf16 [H] device
  *   h_out  bf16 [T, H] device, written; may be h or delta. NULL without delta.
@@ -458,7 +461,8 @@ NVFP4_API nvfp4_status rmsnorm_residual(const uint16_t* h, const uint16_t* delta
 
 /*
  * moe_swiglu - between the gate/up and the down product: x[r,i] = silu(gu[r,i]) * gu[r,I+i], written as
- * rmsnorm_residual writes its rows.
+ * rmsnorm_residual writes its rows. In fp32 with a fast exponential: x is off by (6 + 1.2 |gate|) * 2^-23 of it;
+ * from gates of -87 down the digits of exp(gate) go (a subnormal), and below -104 x is 0.
  *   Defined by: lynn-engine README, P28 note (gate/up + SiLU yields a [top_k, I] intermediate).
  *   gu  bf16 or fp32 [R, 2I] device (gu_type: NVFP4_OUT_BF16 or NVFP4_OUT_F32), the rows of a product over
  *       [gate; up]

@@ -14,8 +14,8 @@
 // 1000 takes 1.6). us of 4096 x 2048 / 65536 x 2048, and of the latter's bytes at the copy rate (6.8 TB/s): norm with
 // delta to bf16 11.8 / 155 (158), to E4M3 12.4 / 152 (139), to NVFP4 11.8 / 148 (129); SwiGLU 7.7 / 114 (118), 9.6 / 122
 // (99), 9.9 / 126 (90); quantise 6.6 / 72 (51); back 5.6 / 68 (51). Where rows end in 4 bits the instructions of the blocks
-// (a maximum, a scale and its reciprocal, 16 codes) bound it: 81 % of the issue slots and 77 % of the integer pipe are
-// used in the quantiser, 79 % and 62 % in the SwiGLU.
+// (a maximum, a scale and its reciprocal, 16 codes) bound it: 82 % of the issue slots and 77 % of the integer pipe are
+// used in the quantiser, 86 % and 65 % in the SwiGLU.
 #include "common.cuh"
 #include "kernels.cuh"
 #include "quant.cuh"

@@ -24,12 +24,13 @@
 //   A warp looks up a tile ahead what the epilogue needs of its rows (scales, places of y), so that no epilogue warp waits
 //     for a list entry. The epilogue writes past L1.
 //
-// What bounds it: with many rows the operands on their way into shared memory, 30 KB a step and SM at some 64 bytes a
-// clock (0.29 us for 224 columns, 6 PFLOP/s: 4096 x 8192 x 8192 in 90 us), and below K = 1024 the outputs, which memory
-// takes at 4.5 TB/s (4096 x 8192 x 512: 22 us, of which a fill of y takes 17). 4096 x 8192 x 2048 takes 33.4 us, 4.1
-// PFLOP/s. With few rows to many experts the weights from memory (64 tokens to eight of 256 experts of 1024 x 2048 each:
-// 36 us for the 200 MB of some 170 experts), with few rows of one matrix the start of a launch: some 4.5 us pass before
-// and after the steps.
+// What bounds it. With many rows the operands on their way into shared memory, 30 KB a step and SM: a step of 224 columns
+// takes 0.24 us between K = 1024 and 2048 and 0.30 from 4096 on (at 1.93 GHz 66 and 54 bytes a clock; its MMAs need 240
+// clocks); 4096 x 8192 x 8192 takes 91 us, 6 PFLOP/s. Below that also what a tile's epilogue takes beyond the next tile's
+// steps: 4096 x 8192 x 2048 takes 33.4 us (4.1 PFLOP/s) for eight rounds of tiles, each 1.9 of steps, some 1.0 of epilogue and
+// 0.6 of stores (28.2 without any stores), and 4.5 around them; 4096 x 8192 x 512 takes 22.7, 18.7 without stores, and a
+// fill of y 17. With few rows to many experts the weights from memory (64 tokens to eight of 256 experts of 1024 x 2048
+// each: 36 us for the 190 MB of some 160 experts), with few rows of one matrix the start of a launch.
 #include <atomic>
 #include <cmath>
 #include <cstring>
